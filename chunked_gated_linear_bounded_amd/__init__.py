@@ -14,9 +14,15 @@ built, every entry point raises; there is no fallback.
     g = kda.chunk_bwd(q, k, v, a, beta, dout)                          # gradients (training)
     out, S = kda.KdaChunkFunction.apply(q, k, v, a, beta)              # the same, under autograd
     G = kda.gate_cumsum(a, g_min=-5.0, chunk=64)
+
+The gated delta rule, one decay per token and value head (gdr.py):
+
+    out, S = kda.gdr_chunk_fwd(q, k, v, g, beta, return_final_state=True)
+    o_t = kda.gdr_decode_step(q_t, k_t, v_t, g_t, beta_t, S)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -76,6 +82,12 @@ def lib():
         L.kda_decode_step.restype = i
         L.kda_chunk_fwd_noalloc.argtypes = [vp] * 5 + [f] + [i] * 7 + [vp, vp, vp, i, vp, vp]
         L.kda_chunk_fwd_noalloc.restype = i
+        L.kda_gdr_workspace_bytes.argtypes = [i] * 8
+        L.kda_gdr_workspace_bytes.restype = sz
+        L.kda_gdr_chunk_fwd.argtypes = [vp, vp] * 5 + [vp] + [i] * 7 + [f] + [vp] * 4 + [sz, vp]
+        L.kda_gdr_chunk_fwd.restype = i
+        L.kda_gdr_decode_step.argtypes = [vp] * 5 + [i] * 6 + [f, vp, vp, vp]
+        L.kda_gdr_decode_step.restype = i
         _lib = L
     return _lib
 
@@ -101,6 +113,17 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _stream_of(stream, device):
+    """The stream a call on `device` launches on, as the integer ctypes passes on: the given one, else
+    that device's current stream."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _on_device(device):
+    """A context in which `device` is the current one: launches go to it, wherever the caller is."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _empty(shape, dtype, device, stream):
@@ -448,3 +471,6 @@ def decode_step(q, k, v, a, beta, state, g_min=-5.0, gate="bounded", out=None, s
     if st != KDA_OK:
         raise KdaError("kda_decode_step", st)
     return out
+
+
+from .gdr import (gdr_chunk_fwd, gdr_chunk_fwd_varlen, gdr_decode_step, gdr_workspace_bytes)  # noqa: E402

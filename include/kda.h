@@ -80,8 +80,9 @@ typedef enum {
     KDA_ERR_HIP = -7,       /* a HIP call or kernel launch failed               */
     KDA_ERR_ALIGN = -8,     /* a pointer is not aligned as required             */
     KDA_ERR_MODE = -9,      /* gate_mode unknown                                */
-    KDA_ERR_SCRATCH = -10   /* kda_chunk_fwd_noalloc: the problem needs more than
+    KDA_ERR_SCRATCH = -10,  /* kda_chunk_fwd_noalloc: the problem needs more than
                                KDA_NOALLOC_SCRATCH_BYTES of device scratch      */
+    KDA_ERR_SCALE = -11     /* scale not finite (gated delta rule, latent attention) */
 } kda_status;
 
 /* Bytes of device scratch that kda_chunk_fwd_noalloc works in: a static device array of the
@@ -287,6 +288,48 @@ int kda_chunk_bwd(const void *q, const void *k, const void *v, const void *a, co
 int kda_decode_step(const void *q, const void *k, const void *v, const void *a, const void *beta,
                     float g_min, int B, int H, int dk, int dv, int io_dtype, int gate_mode,
                     float *state, void *out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The gated delta rule: the recurrence with ONE log-decay per token and value head, not bounded
+ * below, and with key heads shared by groups of value heads:
+ *
+ *   S_t = e^{g_t} S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,   o_t = scale S_t q_t
+ *
+ * Value head h uses the queries and keys of key head h / (H / Hk).  Conventions as above, except:
+ *  - q, k : [B][Hk][T][dk]   v : [B][H][T][dv]   g, beta : [B][H][T]   (all in io_dtype);
+ *    g is the log-decay itself, g <= 0 (anything below -1000, -inf too, is a decay to zero).
+ *  - Every input comes with its element strides for b, h and t (a NULL kda_strides: contiguous);
+ *    the last dimension is contiguous.  Rows of q and k must start at multiples of 16 bytes:
+ *    pointer and strides.  v, g and beta need only their element's alignment.
+ *  - T is any length from 0; the last chunk of a sequence may be short.
+ *  - cu_seqlens NULL: a batch of N sequences of T tokens.  Otherwise packed documents as in
+ *    kda_chunk_fwd_varlen: one stream of T tokens ([Hk][T][dk], ..., strides b unused), N documents,
+ *    states [N][H][dv][dk]; boundaries are read on the device only, and rows of out that no
+ *    document covers are not written.
+ *  - out : [B][H][T][dv] contiguous.  initial_state (nullable) and final_state (nullable):
+ *    [N][H][dv][dk] float32, they may be the same array.
+ *  - dk, dv in {64, 128}; H a multiple of Hk; H and (without cu_seqlens) N at most 65535.
+ * Operands of the matrix products that feed the state keep 22 bits, so the float32 final state is
+ * accurate to about 1e-6 of its norm also with bf16 inputs. */
+typedef struct {
+    long long b, h, t; /* strides in elements of batch entry, head and token */
+} kda_strides;
+
+/* Bytes of workspace kda_gdr_chunk_fwd needs; 0 for an invalid problem. */
+size_t kda_gdr_workspace_bytes(int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
+
+int kda_gdr_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                      const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
+                      const void *beta, const kda_strides *beta_strides, const int *cu_seqlens, int N, int Hk,
+                      int H, int T, int dk, int dv, int io_dtype, float scale, const float *initial_state,
+                      void *out, float *final_state, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token per (batch, value head), the state updated in place.  Contiguous q, k : [B][Hk][dk],
+ * v, out : [B][H][dv], g, beta : [B][H], state : [B][H][dv][dk] float32.  q, k, v, state and out
+ * 16-byte aligned. */
+int kda_gdr_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, int B, int Hk,
+                        int H, int dk, int dv, int io_dtype, float scale, float *state, void *out,
+                        hipStream_t stream);
 
 #ifdef __cplusplus
 }
