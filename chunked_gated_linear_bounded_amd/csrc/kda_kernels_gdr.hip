@@ -21,10 +21,10 @@ size_t gdr_fwd_bytes(const GdrLaunch &p) {
     return key_part(p, L) + (size_t)p.B * p.H * gdr_slots(p) * L.val_bytes();
 }
 
-template <int DK, bool F32, int NW>
+template <int DK, bool F32, int NCT>
 static hipError_t run_state(const GdrStateArgs &a, hipStream_t stream) {
     const int units = (a.seqs.N * a.H + 7) / 8 * 8;
-    hipLaunchKernelGGL((gdr_state_kernel<DK, F32, 0, NW, F32 ? 2 : 1>), dim3(units * (a.dv / 16 / NW)), dim3(64 * NW), 0, stream, a);
+    hipLaunchKernelGGL((gdr_state_kernel<DK, F32, NCT, 0, F32 ? 2 : 1>), dim3(units * (a.dv / 16 / NCT)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -38,16 +38,14 @@ static hipError_t fwd_t(const GdrLaunch &p) {
     if (nslot > 0 && p.T > 0) {
         const GdrChunkArgs a{p.q, p.k, p.g, p.beta, st3(p.sq), st3(p.sk), st3(p.sg), st3(p.sb), seqs,
                              p.Hk, r, nslot, p.scale, p.workspace, vals};
-        hipLaunchKernelGGL((gdr_chunk_kernel<DK, F32, MP>), dim3(nslot, p.Hk, p.B), dim3(256), 0, p.stream, a);
+        hipLaunchKernelGGL((gdr_chunk_kernel<DK, F32, MP>), dim3(nslot, p.H, p.B), dim3(256), 0, p.stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const GdrStateArgs a{p.workspace, vals, p.v, st3(p.sv), seqs, p.H, r, nslot, p.dv, p.scale,
                          p.final_state, p.init_state, p.out, nullptr};
-    // waves per work-group: as many as still leave every CU one
-    const long long waves = (long long)p.N * p.H * (p.dv / 16);
-    if (waves >= 4 * 256) return run_state<DK, F32, 4>(a, p.stream);
-    if (waves >= 2 * 256) return run_state<DK, F32, 2>(a, p.stream);
+    // 32 columns a work-group as soon as 16 would need more than one a CU
+    if ((long long)p.N * p.H * (p.dv / 16) > 256) return run_state<DK, F32, 2>(a, p.stream);
     return run_state<DK, F32, 1>(a, p.stream);
 }
 
