@@ -19,6 +19,8 @@ The gated delta rule, one decay per token and value head (gdr.py):
 
     out, S = kda.gdr_chunk_fwd(q, k, v, g, beta, return_final_state=True)
     o_t = kda.gdr_decode_step(q_t, k_t, v_t, g_t, beta_t, S)
+    grads = kda.gdr_chunk_bwd(q, k, v, g, beta, dout)                # dq, dk, dv, dg, dbeta, dinitial_state
+    out, S = kda.GdrChunkFunction.apply(q, k, v, g, beta)            # the same, under autograd
 """
 from __future__ import annotations
 
@@ -82,10 +84,12 @@ def lib():
         L.kda_decode_step.restype = i
         L.kda_chunk_fwd_noalloc.argtypes = [vp] * 5 + [f] + [i] * 7 + [vp, vp, vp, i, vp, vp]
         L.kda_chunk_fwd_noalloc.restype = i
-        L.kda_gdr_workspace_bytes.argtypes = [i] * 8
+        L.kda_gdr_workspace_bytes.argtypes = [i] * 9
         L.kda_gdr_workspace_bytes.restype = sz
         L.kda_gdr_chunk_fwd.argtypes = [vp, vp] * 5 + [vp] + [i] * 7 + [f] + [vp] * 4 + [sz, vp]
         L.kda_gdr_chunk_fwd.restype = i
+        L.kda_gdr_chunk_bwd.argtypes = [vp, vp] * 6 + [vp] + [i] * 7 + [f] + [vp] * 9 + [sz, vp]
+        L.kda_gdr_chunk_bwd.restype = i
         L.kda_gdr_decode_step.argtypes = [vp] * 5 + [i] * 6 + [f, vp, vp, vp]
         L.kda_gdr_decode_step.restype = i
         _lib = L
@@ -473,4 +477,5 @@ def decode_step(q, k, v, a, beta, state, g_min=-5.0, gate="bounded", out=None, s
     return out
 
 
-from .gdr import (gdr_chunk_fwd, gdr_chunk_fwd_varlen, gdr_decode_step, gdr_workspace_bytes)  # noqa: E402
+from .gdr import (GdrChunkFunction, gdr_chunk_bwd, gdr_chunk_bwd_varlen, gdr_chunk_fwd,  # noqa: E402
+                  gdr_chunk_fwd_varlen, gdr_decode_step, gdr_workspace_bytes)

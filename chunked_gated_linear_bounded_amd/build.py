@@ -39,6 +39,7 @@ UNITS = [
     ("kda_kernels_lowrank.hip", "kda_kernels_lowrank.o", []),
     ("kda_kernels_bwd.hip", "kda_kernels_bwd.o", []),
     ("kda_kernels_gdr.hip", "kda_kernels_gdr.o", []),
+    ("kda_kernels_gdr_bwd.hip", "kda_kernels_gdr_bwd.o", []),
     ("kda_abi.cpp", "kda_abi.o", []),
     ("kda_abi_gdr.cpp", "kda_abi_gdr.o", []),
 ]

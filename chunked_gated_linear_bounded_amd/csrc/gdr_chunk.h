@@ -187,6 +187,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         hd[128 + lane] = bv;
         // what the state stage bounds its operands with (GdrLayout)
         const float ck = wave_max(fabsf(bv) * ex2((float)G) * sK1[lane]), bm = wave_max(fabsf(bv));
+        const float cl = wave_max(ex2((float)(last - G)) * sK1[lane]);
         float kc = in ? sKm[lane] * ex2((float)(last - G)) : 0.f;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) kc += __shfl_xor(kc, d, 64);
@@ -197,6 +198,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
             hd[197] = ck;
             hd[198] = bm;
             hd[200] = kc;
+            hd[201] = cl;
         }
     }
     __syncthreads();

@@ -51,11 +51,11 @@ int inputs(kda::GdrLaunch &p, const void *q, const kda_strides *qs, const void *
     const int unit = p.fp32 ? 4 : 8, esz = p.fp32 ? 4 : 2;
     if (!isfinite(scale)) return KDA_ERR_SCALE;
     if (p.T > 0 && (!q || !k || !v || !g || !beta)) return KDA_ERR_NULL;
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, esz) || !aligned(g, esz) || !aligned(beta, esz) ||
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, esz) || !aligned(beta, esz) ||
         !aligned(cu, 4) || !aligned(init, 16))
         return KDA_ERR_ALIGN;
     if (!set_strides(p.sq, qs, p.Hk, p.T, p.dk, unit) || !set_strides(p.sk, ks, p.Hk, p.T, p.dk, unit) ||
-        !set_strides(p.sv, vs, p.H, p.T, p.dv, 1) || !set_strides(p.sg, gs, p.H, p.T, 1, 1) ||
+        !set_strides(p.sv, vs, p.H, p.T, p.dv, unit) || !set_strides(p.sg, gs, p.H, p.T, 1, 1) ||
         !set_strides(p.sb, bs, p.H, p.T, 1, 1))
         return KDA_ERR_ALIGN;
     if (need > 0 && (!workspace || given < need)) return KDA_ERR_WORKSPACE;
@@ -72,10 +72,10 @@ int inputs(kda::GdrLaunch &p, const void *q, const kda_strides *qs, const void *
 
 extern "C" {
 
-size_t kda_gdr_workspace_bytes(int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype) {
+size_t kda_gdr_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype) {
     if (check_shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype) != KDA_OK) return 0;
     const kda::GdrLaunch p = shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype);
-    return kda::gdr_fwd_bytes(p);
+    return backward ? kda::gdr_bwd_bytes(p) : kda::gdr_fwd_bytes(p);
 }
 
 int kda_gdr_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
@@ -95,6 +95,32 @@ int kda_gdr_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k
     p.final_state = final_state;
     p.stream = stream;
     return kda::launch_gdr_fwd(p) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                      const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
+                      const void *beta, const kda_strides *beta_strides, const void *dout,
+                      const kda_strides *dout_strides, const int *cu_seqlens, int N, int Hk, int H, int T, int dk,
+                      int dv, int io_dtype, float scale, const float *initial_state, const float *dfinal_state,
+                      void *dq, void *dk_out, void *dv_out, void *dg, void *dbeta, float *dinitial_state,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
+    if (st != KDA_OK) return st;
+    kda::GdrLaunch p = shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
+    if (T > 0 && (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta)) return KDA_ERR_NULL;
+    if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk_out, 16) || !aligned(dv_out, 16) || !aligned(dg, 4) ||
+        !aligned(dbeta, 4) || !aligned(dfinal_state, 16) || !aligned(dinitial_state, 16) ||
+        !set_strides(p.sdo, dout_strides, H, T, dv, p.fp32 ? 4 : 8))
+        return KDA_ERR_ALIGN;
+    st = inputs(p, q, q_strides, k, k_strides, v, v_strides, g, g_strides, beta, beta_strides, cu_seqlens, scale,
+                initial_state, workspace, workspace_bytes, kda::gdr_bwd_bytes(p));
+    if (st != KDA_OK || (T == 0 && !dinitial_state)) return st;
+    p.dout = dout;
+    p.dfinal = dfinal_state;
+    p.dq = dq; p.dk_ = dk_out; p.dv_ = dv_out; p.dg = dg; p.dbeta = dbeta;
+    p.dinit = dinitial_state;
+    p.stream = stream;
+    return kda::launch_gdr_bwd(p) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 int kda_gdr_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, int B, int Hk,

@@ -69,10 +69,10 @@ def _shapes(q, k, v, g, beta, cu_seqlens):
     return lead, cu_seqlens.numel() - 1, Hk, H, T, dk, dv
 
 
-def gdr_workspace_bytes(N, Hk, H, T, dk, dv, dtype, packed=False) -> int:
+def gdr_workspace_bytes(N, Hk, H, T, dk, dv, dtype, packed=False, backward=False) -> int:
     """Bytes of workspace for a call on N sequences (packed: N documents in a stream of T tokens)."""
     io = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(lib().kda_gdr_workspace_bytes(int(packed), N, Hk, H, T, dk, dv, io))
+    return int(lib().kda_gdr_workspace_bytes(int(backward), int(packed), N, Hk, H, T, dk, dv, io))
 
 
 def _workspace(workspace, need, dev, stream):
@@ -124,6 +124,70 @@ def gdr_chunk_fwd_varlen(q, k, v, g, beta, cu_seqlens, scale=1.0, out=None, fina
         raise TypeError("cu_seqlens must be a torch.Tensor")
     return _fwd(q, k, v, g, beta, cu_seqlens, scale, out, final_state, return_final_state, initial_state, workspace,
                 stream)
+
+
+def _bwd(q, k, v, g, beta, dout, cu_seqlens, scale, initial_state, dfinal_state, workspace, stream, want_dinitial):
+    lead, N, Hk, H, T, dk, dv = _shapes(q, k, v, g, beta, cu_seqlens)
+    dtype, dev = q.dtype, q.device
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a torch.Tensor")
+    if dout.shape != v.shape:
+        raise ValueError("dout must have v's shape")
+    args = []
+    for t, name, inner in ((q, "q", True), (k, "k", True), (v, "v", True), (g, "g", False), (beta, "beta", False),
+                           (dout, "dout", True)):
+        args += _view(t, name, dtype, dev, inner)
+    cu = None if cu_seqlens is None else _plain(cu_seqlens, "cu_seqlens", torch.int32, dev, (N + 1,))
+    s0 = _plain(initial_state, "initial_state", torch.float32, dev, (N, H, dv, dk))
+    df = _plain(dfinal_state, "dfinal_state", torch.float32, dev, (N, H, dv, dk))
+    with _on_device(dev):
+        out = {n: _empty(shape, dtype, dev, stream) for n, shape in (
+            ("dq", q.shape), ("dk", q.shape), ("dv", v.shape), ("dg", g.shape), ("dbeta", g.shape))}
+        out["dinitial_state"] = _empty((N, H, dv, dk), torch.float32, dev, stream) if want_dinitial else None
+        need = gdr_workspace_bytes(N, Hk, H, T, dk, dv, dtype, cu is not None, backward=True)
+        workspace = _workspace(workspace, need, dev, stream)
+        st = lib().kda_gdr_chunk_bwd(*args, cu, N, Hk, H, T, dk, dv, _DTYPES[dtype], float(scale), s0, df,
+                                     *(None if t is None else t.data_ptr() for t in out.values()),
+                                     workspace.data_ptr(), workspace.numel(), _stream_of(stream, dev))
+    if st != KDA_OK:
+        raise KdaError("kda_gdr_chunk_bwd", st)
+    return out
+
+
+def gdr_chunk_bwd(q, k, v, g, beta, dout, scale=1.0, initial_state=None, dfinal_state=None, workspace=None, stream=None,
+                  want_dinitial=True):
+    """Gradients of sum(dout * out) + sum(dfinal_state * final_state) of gdr_chunk_fwd, from its inputs
+    alone.  Returns a dict of dq, dk (summed over the value heads that share a key head), dv, dg, dbeta
+    in the inputs' dtype and dinitial_state in float32 (None unless want_dinitial)."""
+    return _bwd(q, k, v, g, beta, dout, None, scale, initial_state, dfinal_state, workspace, stream, want_dinitial)
+
+
+def gdr_chunk_bwd_varlen(q, k, v, g, beta, dout, cu_seqlens, scale=1.0, initial_state=None, dfinal_state=None,
+                         workspace=None, stream=None, want_dinitial=True):
+    """gdr_chunk_bwd of packed documents (gdr_chunk_fwd_varlen).  Tokens behind the last document get
+    zero gradients."""
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be a torch.Tensor")
+    return _bwd(q, k, v, g, beta, dout, cu_seqlens, scale, initial_state, dfinal_state, workspace, stream, want_dinitial)
+
+
+class GdrChunkFunction(torch.autograd.Function):
+    """out, final_state = GdrChunkFunction.apply(q, k, v, g, beta, scale, initial_state, cu_seqlens): the
+    chunked forward with its backward, for a batch or (cu_seqlens given) for packed documents."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, scale=1.0, initial_state=None, cu_seqlens=None):
+        out, fs = _fwd(q, k, v, g, beta, cu_seqlens, scale, None, None, True, initial_state, None, None)
+        ctx.save_for_backward(q, k, v, g, beta, initial_state, cu_seqlens)
+        ctx.scale = scale
+        return out, fs
+
+    @staticmethod
+    def backward(ctx, dout, dfinal):
+        q, k, v, g, beta, s0, cu = ctx.saved_tensors
+        d = _bwd(q, k, v, g, beta, dout.contiguous(), cu, ctx.scale, s0, dfinal.contiguous(), None, None,
+                 s0 is not None and ctx.needs_input_grad[6])
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], None, d["dinitial_state"], None
 
 
 def gdr_decode_step(q, k, v, g, beta, state, scale=1.0, out=None, stream=None):

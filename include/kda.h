@@ -299,8 +299,8 @@ int kda_decode_step(const void *q, const void *k, const void *v, const void *a, 
  *  - q, k : [B][Hk][T][dk]   v : [B][H][T][dv]   g, beta : [B][H][T]   (all in io_dtype);
  *    g is the log-decay itself, g <= 0 (anything below -1000, -inf too, is a decay to zero).
  *  - Every input comes with its element strides for b, h and t (a NULL kda_strides: contiguous);
- *    the last dimension is contiguous.  Rows of q and k must start at multiples of 16 bytes:
- *    pointer and strides.  v, g and beta need only their element's alignment.
+ *    the last dimension is contiguous.  Rows of q, k, v and dout must start at multiples of 16
+ *    bytes: pointer and strides.  g and beta need only their element's alignment.
  *  - T is any length from 0; the last chunk of a sequence may be short.
  *  - cu_seqlens NULL: a batch of N sequences of T tokens.  Otherwise packed documents as in
  *    kda_chunk_fwd_varlen: one stream of T tokens ([Hk][T][dk], ..., strides b unused), N documents,
@@ -315,14 +315,28 @@ typedef struct {
     long long b, h, t; /* strides in elements of batch entry, head and token */
 } kda_strides;
 
-/* Bytes of workspace kda_gdr_chunk_fwd needs; 0 for an invalid problem. */
-size_t kda_gdr_workspace_bytes(int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
+/* Bytes of workspace kda_gdr_chunk_fwd (backward 0) or kda_gdr_chunk_bwd (backward 1) needs;
+ * 0 for an invalid problem. */
+size_t kda_gdr_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
 
 int kda_gdr_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
                       const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
                       const void *beta, const kda_strides *beta_strides, const int *cu_seqlens, int N, int Hk,
                       int H, int T, int dk, int dv, int io_dtype, float scale, const float *initial_state,
                       void *out, float *final_state, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dout * out) + sum(dfinal_state * final_state).  dout : [B][H][T][dv] (strided),
+ * dfinal_state : [N][H][dv][dk] float32 or NULL.  dq, dk_out : [B][Hk][T][dk] (summed over the value
+ * heads of a key head), dv_out : [B][H][T][dv], dg, dbeta : [B][H][T], contiguous, in io_dtype;
+ * dinitial_state : [N][H][dv][dk] float32 or NULL.  The gradients of tokens that no document covers
+ * are written as zeros.  Everything is recomputed from the inputs; no float atomics. */
+int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                      const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
+                      const void *beta, const kda_strides *beta_strides, const void *dout,
+                      const kda_strides *dout_strides, const int *cu_seqlens, int N, int Hk, int H, int T, int dk,
+                      int dv, int io_dtype, float scale, const float *initial_state, const float *dfinal_state,
+                      void *dq, void *dk_out, void *dv_out, void *dg, void *dbeta, float *dinitial_state,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* One token per (batch, value head), the state updated in place.  Contiguous q, k : [B][Hk][dk],
  * v, out : [B][H][dv], g, beta : [B][H], state : [B][H][dv][dk] float32.  q, k, v, state and out
