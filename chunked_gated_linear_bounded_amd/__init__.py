@@ -21,6 +21,13 @@ The gated delta rule, one decay per token and value head (gdr.py):
     o_t = kda.gdr_decode_step(q_t, k_t, v_t, g_t, beta_t, S)
     grads = kda.gdr_chunk_bwd(q, k, v, g, beta, dout)                # dq, dk, dv, dg, dbeta, dinitial_state
     out, S = kda.GdrChunkFunction.apply(q, k, v, g, beta)            # the same, under autograd
+
+Latent attention, keys and values from one latent vector a token (latent.py):
+
+    out, lse = kda.latent_attn_fwd(q, k, v, k_rope, return_lse=True)
+    grads = kda.latent_attn_bwd(q, k, v, k_rope, out, lse, dout)     # dq, dk, dv, dk_rope
+    out = kda.LatentAttnFunction.apply(q, k, v, k_rope)              # the same, under autograd
+    o_t = kda.latent_decode_step(q_t, cache, block_table, lengths, scale)
 """
 from __future__ import annotations
 
@@ -92,6 +99,16 @@ def lib():
         L.kda_gdr_chunk_bwd.restype = i
         L.kda_gdr_decode_step.argtypes = [vp] * 5 + [i] * 6 + [f, vp, vp, vp]
         L.kda_gdr_decode_step.restype = i
+        L.kda_latent_attn_fwd.argtypes = [vp, vp] * 4 + [vp, vp] + [i] * 7 + [f, vp, vp, vp]
+        L.kda_latent_attn_fwd.restype = i
+        L.kda_latent_attn_bwd_workspace_bytes.argtypes = [i] * 8
+        L.kda_latent_attn_bwd_workspace_bytes.restype = sz
+        L.kda_latent_attn_bwd.argtypes = [vp, vp] * 4 + [vp] * 4 + [vp, vp] + [i] * 7 + [f] + [vp] * 5 + [sz, vp]
+        L.kda_latent_attn_bwd.restype = i
+        L.kda_latent_decode_workspace_bytes.argtypes = [i] * 7
+        L.kda_latent_decode_workspace_bytes.restype = sz
+        L.kda_latent_decode_step.argtypes = [vp] * 4 + [i] * 8 + [f, vp, vp, vp, sz, vp]
+        L.kda_latent_decode_step.restype = i
         _lib = L
     return _lib
 
@@ -479,3 +496,6 @@ def decode_step(q, k, v, a, beta, state, g_min=-5.0, gate="bounded", out=None, s
 
 from .gdr import (GdrChunkFunction, gdr_chunk_bwd, gdr_chunk_bwd_varlen, gdr_chunk_fwd,  # noqa: E402
                   gdr_chunk_fwd_varlen, gdr_decode_step, gdr_workspace_bytes)
+from .latent import (LatentAttnFunction, latent_attn_bwd, latent_attn_bwd_varlen, latent_attn_fwd,  # noqa: E402
+                     latent_attn_fwd_varlen, latent_bwd_workspace_bytes, latent_decode_step,
+                     latent_decode_workspace_bytes)

@@ -282,7 +282,7 @@ const char *kda_status_string(int status) {
     case KDA_ERR_ALIGN: return "a pointer is not aligned as required (16 bytes; beta: element size)";
     case KDA_ERR_MODE: return "unknown gate_mode";
     case KDA_ERR_SCRATCH: return "problem needs more device scratch than KDA_NOALLOC_SCRATCH_BYTES (kda_chunk_fwd_noalloc)";
-    case KDA_ERR_SCALE: return "scale must be finite";
+    case KDA_ERR_SCALE: return "scale must be finite (latent attention: and positive)";
     default: return "unknown status";
     }
 }

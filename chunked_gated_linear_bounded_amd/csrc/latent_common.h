@@ -1,0 +1,175 @@
+// Building blocks of latent attention: attention whose keys and values come from one latent vector a
+// token.  Expanded form: per head a key part k and a value v made from the latent, and a rotary key
+// part k_rope that all heads share,
+//   s_ij = scale (q_i[:dn] . k_j + q_i[dn:] . k_rope_j),  p = softmax over the visible j,  o_i = sum p_ij v_j;
+// absorbed form: the query multiplied into the latent's space, one row c_j of the cache a token,
+//   s_j = scale q . c_j,  o = sum p_j c_j[:dc].
+//
+// Everything is computed transposed: S^T = K Q^T puts keys on the accumulator's rows and queries on
+// its columns, so a lane's column is one query, the softmax reduces over a lane's own rows and two
+// lane exchanges, and the rows' scaling factors are lane scalars; and two key tiles of P^T are, as
+// they lie, the B operand of O^T = V^T P^T.  The fragment order, the permuted row index and the
+// transposed LDS read are those of gdr_common.h.
+//
+// bf16 inputs use 16x16x32 bf16 MFMAs, P and dS rounded to bf16; float32 inputs use float32 MFMAs
+// (eight 16x16x4 steps).  Softmax statistics and all sums are float32.
+#pragma once
+#include "gdr_common.h"
+
+namespace kda {
+
+struct f32x8s {
+    f32x4 a, b;
+};
+
+template <bool F32> struct AttnOp;
+template <> struct AttnOp<false> {
+    using E = __bf16;
+    using V8 = bf16x8;
+    static constexpr int FB = 1024;  // bytes of a fragment
+    __device__ __forceinline__ static f32x4 mma(const V8 &a, const V8 &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static V8 load(const E *p) { return *reinterpret_cast<const V8 *>(p); }
+    __device__ __forceinline__ static V8 zero() { return V8{}; }
+    __device__ __forceinline__ static V8 pair(const f32x4 &x, const f32x4 &y) {
+        V8 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { r[i] = (__bf16)x[i]; r[4 + i] = (__bf16)y[i]; }
+        return r;
+    }
+    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) {
+        *reinterpret_cast<__attribute__((address_space(3))) V8 *>(f + frag_slot(g, m)) = x;
+    }
+    __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
+        return *reinterpret_cast<const __attribute__((address_space(3))) V8 *>(f + frag_slot(lane >> 4, lane & 15));
+    }
+    // transposed: rows = columns perm_row(tile, .), k = rows of the fragments f0 (row tile 2 kb), f1 (2 kb + 1)
+    __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int tile, int lane) {
+        const int g = lane >> 4, s = lane & 15, m = 4 * g + (s >> 2);
+        const int off = frag_slot(s & 3, m) + 8 * (tile & 1);
+        const bf16x4 a = ld_tr16<bf16x4>(f0 + off), b = ld_tr16<bf16x4>(f1 + off);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ __forceinline__ static void store8(E *p, const f32x4 &x, const f32x4 &y) {
+        *reinterpret_cast<V8 *>(p) = pair(x, y);
+    }
+};
+template <> struct AttnOp<true> {
+    using E = float;
+    using V8 = f32x8s;
+    typedef __attribute__((address_space(3))) f32x4 lds_f4;
+    static constexpr int FB = 2048;
+    __device__ __forceinline__ static f32x4 mma(const V8 &a, const V8 &b, f32x4 c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = mma4(a.a[j], b.a[j], c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = mma4(a.b[j], b.b[j], c);
+        return c;
+    }
+    __device__ __forceinline__ static V8 load(const E *p) {
+        return V8{*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 4)};
+    }
+    __device__ __forceinline__ static V8 zero() { return V8{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}; }
+    __device__ __forceinline__ static V8 pair(const f32x4 &x, const f32x4 &y) { return V8{x, y}; }
+    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) {
+        lds_f4 *p = reinterpret_cast<lds_f4 *>(f + 2 * frag_slot(g, m));
+        p[0] = x.a;
+        p[1] = x.b;
+    }
+    __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
+        const lds_f4 *p = reinterpret_cast<const lds_f4 *>(f + 2 * frag_slot(lane >> 4, lane & 15));
+        return V8{p[0], p[1]};
+    }
+    __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int tile, int lane) {
+        const int g = lane >> 4, m = lane & 15, e = 4 * (4 * (tile & 1) + (m & 3));
+        V8 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int off = 2 * frag_slot(m >> 2, 4 * g + j) + e;
+            r.a[j] = *reinterpret_cast<const __attribute__((address_space(3))) float *>(f0 + off);
+            r.b[j] = *reinterpret_cast<const __attribute__((address_space(3))) float *>(f1 + off);
+        }
+        return r;
+    }
+    __device__ __forceinline__ static void store8(E *p, const f32x4 &x, const f32x4 &y) {
+        *reinterpret_cast<f32x4 *>(p) = x;
+        *reinterpret_cast<f32x4 *>(p + 4) = y;
+    }
+};
+
+// row tile and row of index r inside a 64-row block (the inverse of perm_row)
+__device__ __forceinline__ int perm_tile(int r) { return 2 * (r >> 5) + ((r >> 2) & 1); }
+__device__ __forceinline__ int perm_m(int r) { return 4 * ((r >> 3) & 3) + (r & 3); }
+
+// maximum / sum over the four lanes that hold one column
+__device__ __forceinline__ float col_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16, 64));
+    return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float col_sum(float x) {
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
+
+// Sequences of queries and keys.  cu_q, cu_k NULL: N sequences of T queries and S keys.  Otherwise
+// packed streams of T queries and S keys with N + 1 boundaries each, clipped to the streams.  The last
+// query of a sequence stands at its last key: query i sees keys 0 .. i + (keys - queries).
+struct AttnSeqs {
+    const int *cu_q, *cu_k;
+    int N, T, S;
+    __device__ __forceinline__ static int clip(int x, int hi) { return x < 0 ? 0 : (x > hi ? hi : x); }
+    __device__ __forceinline__ static void range(const int *cu, int n, int total, int &start, int &len) {
+        start = 0;
+        len = total;
+        if (cu) {
+            start = clip(cu[n], total);
+            const int e = clip(cu[n + 1], total);
+            len = e > start ? e - start : 0;
+        }
+    }
+    // tile j of BT rows of batch entry b on the query side (cu = cu_q) or key side: as in GdrSeqs
+    template <int BT>
+    __device__ __forceinline__ bool find(const int *cu, int total, int b, int j, int &n, int &tile) const {
+        n = b;
+        tile = j;
+        if (cu) {
+            int lo = 0, hi = N - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (clip(cu[mid], total) / BT + mid <= j) lo = mid;
+                else hi = mid - 1;
+            }
+            n = lo;
+            tile = j - (clip(cu[n], total) / BT + n);
+        }
+        return tile >= 0;
+    }
+    static int tiles(bool packed, int N, int total, int bt) { return packed ? total / bt + N : (total + bt - 1) / bt; }
+};
+
+// One operand tile of 64 rows and 8 NC columns into LDS: 16-byte pieces through registers, in
+// fragment order; rows past the last repeat it.  256 threads, piece p = i 256 + tid: row p / NC.
+template <bool F32, int NC> struct TileStage {
+    using Op = AttnOp<F32>;
+    static constexpr int N = 64 * NC / 256;
+    static_assert(64 * NC % 256 == 0, "whole pieces per thread");
+    typename Op::V8 x[N];
+    __device__ __forceinline__ void load(const typename Op::E *base, long long stride, int row0, int nrow, int tid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = i * 256 + tid, r = row0 + p / NC, c = p % NC;
+            x[i] = Op::load(base + (long long)(r < nrow ? r : nrow - 1) * stride + 8 * c);
+        }
+    }
+    // fragments [row tile][nb blocks], this tile's columns from block b0 on
+    __device__ __forceinline__ void store(lds_u8 *f, int nb, int b0, int tid) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = i * 256 + tid, r = p / NC, c = p % NC;
+            Op::put(f + (perm_tile(r) * nb + b0 + (c >> 2)) * Op::FB, c & 3, perm_m(r), x[i]);
+        }
+    }
+};
+
+}  // namespace kda

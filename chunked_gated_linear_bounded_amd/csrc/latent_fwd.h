@@ -1,0 +1,182 @@
+// Expanded latent attention, forward: one four-wave work-group per 128 queries of one head, 32
+// queries a wave (two column tiles), keys in tiles of 64 through LDS.  Per tile a wave does
+// 2 x 4 x (dn + dr) / 32 + 2 x 2 x dn / 16 MFMAs (80 at 128 + 64, 1,280 cycles) on 40 KiB of LDS
+// reads; the next tile's keys and values are in flight in registers meanwhile, so one 40 KiB buffer
+// is enough and two work-groups share a CU, one's softmax beside the other's MFMAs.
+// One pass over the keys with the running maximum and sum of the softmax; the accumulator is scaled
+// only when a maximum in the wave has grown.  Work-groups of a head share an XCD's L2; the last
+// queries, which see most keys, start first.
+#pragma once
+#include "latent_common.h"
+
+namespace kda {
+
+struct LatentFwdArgs {
+    const void *q, *k, *kr, *v;
+    Strides3 sq, sk, skr, sv;  // kr: b, (unused), t
+    AttnSeqs seqs;
+    int H, NB, ntile;          // heads; batch entries (1: packed); query tiles per batch entry
+    float scale;
+    void *out;                 // [B][H][T][dn], contiguous
+    float *lse;                // [B][H][T]
+};
+
+template <int DN, int DR, bool F32>
+__global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const LatentFwdArgs p) {
+    using Op = AttnOp<F32>;
+    using E = typename Op::E;
+    using V8 = typename Op::V8;
+    constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = DN / 16, NQ = 2;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[(4 * NKB + 4 * NDB) * Op::FB];
+    lds_u8 *sk = lds_base(smem), *sv = sk + 4 * NKB * Op::FB;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int unit = (blockIdx.x >> 3) / p.ntile * 8 + (blockIdx.x & 7);
+    const int slot = p.ntile - 1 - (blockIdx.x >> 3) % p.ntile;
+    if (unit >= p.NB * p.H) return;
+    const int b = unit / p.H, h = unit % p.H;
+    int seq, tile, q0, nq, k0, nk;
+    if (!p.seqs.template find<128>(p.seqs.cu_q, p.seqs.T, b, slot, seq, tile)) return;
+    AttnSeqs::range(p.seqs.cu_q, seq, p.seqs.T, q0, nq);
+    AttnSeqs::range(p.seqs.cu_k, seq, p.seqs.S, k0, nk);
+    if (tile * 128 >= nq) return;
+    const int qw = tile * 128 + 32 * w, shift = nk - nq;  // query i sees keys 0 .. i + shift
+    const E *kp = reinterpret_cast<const E *>(p.k) + b * p.sk.b + h * p.sk.h + (long long)k0 * p.sk.t;
+    const E *rp = reinterpret_cast<const E *>(p.kr) + b * p.skr.b + (long long)k0 * p.skr.t;
+    const E *vp = reinterpret_cast<const E *>(p.v) + b * p.sv.b + h * p.sv.h + (long long)k0 * p.sv.t;
+    const E *qp = reinterpret_cast<const E *>(p.q) + b * p.sq.b + h * p.sq.h + (long long)q0 * p.sq.t + 8 * g;
+    const int lastq = min(tile * 128 + 127, nq - 1);
+    const int nkey = max(0, min(nk, lastq + shift + 1)), ntk = (nkey + 63) / 64;
+    const float c = p.scale * kLog2e;
+
+    V8 qf[NQ][NKB];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        const int r = min(qw + 16 * x + n, nq - 1);
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) qf[x][kb] = Op::load(qp + (long long)r * p.sq.t + 32 * kb);
+    }
+    f32x4 O[NT][NQ];
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) O[t][x] = zero;
+    float m[NQ], l[NQ];  // running maximum (of the scaled scores, log2 units) and sum of a lane's column
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        m[x] = -INFINITY;
+        l[x] = 0.f;
+    }
+    TileStage<F32, DN / 8> stk, stv;
+    TileStage<F32, DR / 8> str;
+    if (ntk > 0) {
+        stk.load(kp, p.sk.t, 0, nk, tid);
+        str.load(rp, p.skr.t, 0, nk, tid);
+        stv.load(vp, p.sv.t, 0, nk, tid);
+    }
+    for (int kt = 0; kt < ntk; ++kt) {
+        barrier_lds();  // the last tile has been read
+        stk.store(sk, NKB, 0, tid);
+        str.store(sk, NKB, NDB, tid);
+        stv.store(sv, NDB, 0, tid);
+        barrier_lds();
+        if (kt + 1 < ntk) {
+            stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);
+            str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
+            stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
+        }
+        const int first = 64 * kt;
+        if (first > qw + 31 + shift) continue;  // nothing of this tile is seen by this wave
+        f32x4 s[4][NQ];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) s[t][x] = zero;
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const V8 kf = Op::get(sk + (t * NKB + kb) * Op::FB, lane);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf, qf[x][kb], s[t][x]);
+            }
+        }
+        const bool edge = first + 64 > nk || first + 63 > qw + shift;
+        float mx[NQ], alpha[NQ];
+        bool grown = false;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            if (edge) {
+                const int see = min(nk - 1, qw + 16 * x + n + shift) - first;  // last visible key of the tile
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (perm_row(t, 4 * g + i) > see) s[t][x][i] = -INFINITY;
+            }
+            float a = fmaxf(fmaxf(s[0][x][0], s[0][x][1]), fmaxf(s[0][x][2], s[0][x][3]));
+#pragma unroll
+            for (int t = 1; t < 4; ++t) a = fmaxf(a, fmaxf(fmaxf(s[t][x][0], s[t][x][1]), fmaxf(s[t][x][2], s[t][x][3])));
+            a = col_max(a);
+            mx[x] = fmaxf(m[x], a * c);
+            grown |= mx[x] > m[x];
+        }
+        if (__builtin_amdgcn_ballot_w64(grown) != 0) {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                alpha[x] = mx[x] == -INFINITY ? 1.f : ex2(m[x] - mx[x]);
+                m[x] = mx[x];
+                l[x] *= alpha[x];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[t][x][i] *= alpha[x];
+            }
+        }
+        V8 pf[2][NQ];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const float mm = m[x] == -INFINITY ? 0.f : m[x];  // a column that has seen nothing yet
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[t][x][i] = ex2(fmaf(s[t][x][i], c, -mm));
+                    sum += s[t][x][i];
+                }
+            l[x] += sum;
+            pf[0][x] = Op::pair(s[0][x], s[1][x]);
+            pf[1][x] = Op::pair(s[2][x], s[3][x]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const lds_u8 *f0 = sv + (2 * kb * NDB + (t >> 1)) * Op::FB;
+                const V8 vf = Op::get_t(f0, f0 + NDB * Op::FB, t, lane);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) O[t][x] = Op::mma(vf, pf[kb][x], O[t][x]);
+            }
+    }
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+        const int r = qw + 16 * x + n;
+        l[x] = col_sum(l[x]);
+        if (r >= nq) continue;
+        const size_t row = ((size_t)(b * p.H + h)) * p.seqs.T + q0 + r;
+        const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;  // a query that sees nothing: zeros, -inf
+#pragma unroll
+        for (int t = 0; t < NT; t += 2) {
+            f32x4 a = O[t][x], d = O[t + 1][x];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] *= inv;
+                d[i] *= inv;
+            }
+            Op::store8(reinterpret_cast<E *>(p.out) + row * DN + 16 * t + 8 * g, a, d);
+        }
+        if (g == 0) p.lse[row] = l[x] > 0.f ? (m[x] + lg2(l[x])) * kLn2 : -INFINITY;
+    }
+}
+
+}  // namespace kda

@@ -29,7 +29,7 @@ def _view(t, name, dtype, dev, inner=True):
         if t.shape[-1] > 1 and s[-1] != 1 and t.numel() > 0:
             raise ValueError("the last dimension of %s must be contiguous" % name)
         s = s[:-1]
-    return t.data_ptr(), _S3(*(s if len(s) == 3 else (0,) + s))
+    return t.data_ptr(), _S3(*((0,) * (3 - len(s)) + tuple(s)))
 
 
 def _plain(t, name, dtype, dev, shape):

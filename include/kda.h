@@ -82,7 +82,7 @@ typedef enum {
     KDA_ERR_MODE = -9,      /* gate_mode unknown                                */
     KDA_ERR_SCRATCH = -10,  /* kda_chunk_fwd_noalloc: the problem needs more than
                                KDA_NOALLOC_SCRATCH_BYTES of device scratch      */
-    KDA_ERR_SCALE = -11     /* scale not finite (gated delta rule, latent attention) */
+    KDA_ERR_SCALE = -11     /* scale not finite, or (latent attention) not positive */
 } kda_status;
 
 /* Bytes of device scratch that kda_chunk_fwd_noalloc works in: a static device array of the
@@ -344,6 +344,62 @@ int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k
 int kda_gdr_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, int B, int Hk,
                         int H, int dk, int dv, int io_dtype, float scale, float *state, void *out,
                         hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Latent attention: causal softmax attention whose keys and values come from one latent vector a
+ * token, the attention that hybrid models run beside delta-rule layers.
+ *
+ * Expanded form (prefill, training): per head a key part k and a value v that the caller has made
+ * from the latents, and a rotary key part k_rope shared by all heads,
+ *   s_ij = scale (q_i[0 .. dn) . k_j + q_i[dn .. dn + dr) . k_rope_j),
+ *   o_i = sum_j softmax_j(s_ij) v_j    over the visible keys j.
+ * The last query of a sequence stands at its last key (queries behind a cached prefix: S > T), so
+ * query i sees keys 0 .. i + S - T.  A query that sees no key gets zeros and a log-sum-exp of -inf.
+ *  - q : [B][H][T][dn + dr]   k, v : [B][H][S][dn]   k_rope : [B][S][dr]   in io_dtype, each with
+ *    element strides (NULL: contiguous; k_rope's h is unused); the last dimension is contiguous and
+ *    every row starts at a multiple of 16 bytes.
+ *  - cu_seqlens_q and cu_seqlens_k both NULL: a batch of N sequences.  Otherwise packed streams of T
+ *    queries and S keys ([H][T][..], [H][S][..], [S][dr], strides b unused) with N + 1 int32
+ *    boundaries each, on the device; they are clipped to the streams there, and rows that no
+ *    sequence covers are not written (gradients: written as zeros).
+ *  - out : [B][H][T][dn] in io_dtype, lse : [B][H][T] float32 (natural log), contiguous.
+ *  - dn in {64, 128} (v has dn channels too), dr in {32, 64}; scale > 0; finite inputs at every
+ *    token of a sequence (what lies outside the sequences is never used).
+ *  - H and (without boundaries) N at most 65535. */
+int kda_latent_attn_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                        const void *v, const kda_strides *v_strides, const void *k_rope,
+                        const kda_strides *k_rope_strides, const int *cu_seqlens_q, const int *cu_seqlens_k, int N,
+                        int H, int T, int S, int dn, int dr, int io_dtype, float scale, void *out, float *lse,
+                        hipStream_t stream);
+
+/* Bytes of workspace kda_latent_attn_bwd needs (0 for an invalid problem): delta and the heads'
+ * float32 partials of k_rope's gradient. */
+size_t kda_latent_attn_bwd_workspace_bytes(int packed, int N, int H, int T, int S, int dn, int dr, int io_dtype);
+
+/* Gradients of sum(dout * out), from the inputs and the forward's out and lse (contiguous, as it
+ * wrote them).  dq : [B][H][T][dn + dr], dk, dv : [B][H][S][dn], dk_rope : [B][S][dr] (summed over the
+ * heads), contiguous, in io_dtype.  No float atomics: the same inputs give the same bits. */
+int kda_latent_attn_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                        const void *v, const kda_strides *v_strides, const void *k_rope,
+                        const kda_strides *k_rope_strides, const void *out, const float *lse, const void *dout,
+                        const kda_strides *dout_strides, const int *cu_seqlens_q, const int *cu_seqlens_k, int N,
+                        int H, int T, int S, int dn, int dr, int io_dtype, float scale, void *dq, void *dk_out,
+                        void *dv_out, void *dk_rope, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Absorbed form, one token per sequence against a paged cache of latent rows c = [latent, rotary part]:
+ *   s_j = scale q . c_j,   out = sum_j softmax_j(s_j) c_j[0 .. dc)    over the sequence's lengths[b] rows.
+ *  - q : [B][H][dc + dr], cache : [pages][page][dc + dr], out : [B][H][dc] in io_dtype, lse : [B][H]
+ *    float32; block_table : [B][max_pages] int32, row j of sequence b is row j % page of page
+ *    block_table[b][j / page]; lengths : [B] int32; all contiguous, on the device.
+ *  - lengths are clipped to 0 .. max_pages * page and pages to the cache's on the device, so no
+ *    content of either leaves the arrays; a sequence of length 0 gives zeros and -inf.  Rows past a
+ *    sequence's length are never used, whatever they hold.
+ *  - dc in {256, 512}, dr = 64; any H up to 65535, any page size.
+ * workspace: kda_latent_decode_workspace_bytes(...) bytes (may be 0). */
+size_t kda_latent_decode_workspace_bytes(int B, int H, int page, int max_pages, int dc, int dr, int io_dtype);
+int kda_latent_decode_step(const void *q, const void *cache, const int *block_table, const int *lengths, int B, int H,
+                           int pages, int page, int max_pages, int dc, int dr, int io_dtype, float scale, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
