@@ -98,13 +98,10 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(const LatentBwdArgs p
         str.store(sk, NKB, NDB, tid);
         stv.store(sv, NDB, 0, tid);
         barrier_lds();
-        if (kt + 1 < ntk) {
-            stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);
-            str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
-            stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
-        }
+        stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);  // behind the last tile it loads nothing
+        str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
+        stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
         const int first = 64 * kt;
-        if (first > qw + 16 * NQ - 1 + shift) continue;
         const bool edge = first + 64 > nk || first + 63 > qw + shift;
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {  // 32 keys: the k of one MFMA
@@ -129,12 +126,12 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(const LatentBwdArgs p
             V8 sf[NQ];
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                const int see = min(nk - 1, qw + 16 * x + n + shift) - first;
+                const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (edge && perm_row(2 * hb + t, 4 * g + i) > see) s[t][x][i] = -INFINITY;
+                        if (edge && perm_row(2 * hb + t, i) > see) s[t][x][i] = -INFINITY;
                         const float pr = ex2(fmaf(s[t][x][i], c, -lse[x]));
                         s[t][x][i] = pr * (d[t][x][i] - delta[x]);
                     }
@@ -217,11 +214,12 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs 
 #pragma unroll
         for (int t = 0; t < NV; ++t) dv[t][x] = zero;
     }
-    TileStage<F32, (DN + DR) / 8> stq;
-    TileStage<F32, DN / 8> sto;
+    TileStage<F32, DN / 8> stq, sto;
+    TileStage<F32, DR / 8> str;
     float rl = 0.f, rd = 0.f;
     auto load = [&](int qt) {
         stq.load(qp, p.sq.t, 64 * qt, nq, tid);
+        str.load(qp + DN, p.sq.t, 64 * qt, nq, tid);
         sto.load(dp_, p.sdo.t, 64 * qt, nq, tid);
         if (tid < 64) {
             const int r = min(64 * qt + tid, nq - 1);
@@ -234,15 +232,15 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs 
     for (int qt = t_first; qt < t_end; ++qt) {
         barrier_lds();
         stq.store(sq, NKB, 0, tid);
+        str.store(sq, NKB, NDB, tid);
         sto.store(so, NDB, 0, tid);
         if (tid < 64) {
             sl[tid] = rl;
             sd[tid] = rd;
         }
         barrier_lds();
-        if (qt + 1 < t_end) load(qt + 1);
+        load(qt + 1);  // behind the last tile it loads nothing
         const int first = 64 * qt;
-        if (first + 63 + shift < kw) continue;  // this wave's keys come after all of these queries
         const bool edge = first + 64 > nq || first + shift < kw + 16 * NK - 1;
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
@@ -273,13 +271,13 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs 
             }
 #pragma unroll
             for (int x = 0; x < NK; ++x) {
-                const int key = kw + 16 * x + n;
+                const int seen = kw + 16 * x + n - shift - first - 8 * g, none = nq - first - 8 * g;  // rows seen .. none - 1
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int row = first + perm_row(2 * hb + t, 4 * g + i);
-                        if (edge && (row >= nq || key > row + shift)) s[t][x][i] = -INFINITY;
+                        const int row = perm_row(2 * hb + t, i);
+                        if (edge && (row >= none || row < seen)) s[t][x][i] = -INFINITY;
                         const float pr = ex2(fmaf(s[t][x][i], c, -l4[t][i]));
                         s[t][x][i] = pr;
                         d[t][x][i] = pr * (d[t][x][i] - d4[t][i]);

@@ -38,9 +38,10 @@ template <> struct AttnOp<false> {
         for (int i = 0; i < 4; ++i) { r[i] = (__bf16)x[i]; r[4 + i] = (__bf16)y[i]; }
         return r;
     }
-    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) {
-        *reinterpret_cast<__attribute__((address_space(3))) V8 *>(f + frag_slot(g, m)) = x;
+    __device__ __forceinline__ static void put_at(lds_u8 *p, const V8 &x) {
+        *reinterpret_cast<__attribute__((address_space(3))) V8 *>(p) = x;
     }
+    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) { put_at(f + frag_slot(g, m), x); }
     __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
         return *reinterpret_cast<const __attribute__((address_space(3))) V8 *>(f + frag_slot(lane >> 4, lane & 15));
     }
@@ -72,11 +73,12 @@ template <> struct AttnOp<true> {
     }
     __device__ __forceinline__ static V8 zero() { return V8{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}; }
     __device__ __forceinline__ static V8 pair(const f32x4 &x, const f32x4 &y) { return V8{x, y}; }
-    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) {
-        lds_f4 *p = reinterpret_cast<lds_f4 *>(f + 2 * frag_slot(g, m));
+    __device__ __forceinline__ static void put_at(lds_u8 *to, const V8 &x) {
+        lds_f4 *p = reinterpret_cast<lds_f4 *>(to);
         p[0] = x.a;
         p[1] = x.b;
     }
+    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) { put_at(f + 2 * frag_slot(g, m), x); }
     __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
         const lds_f4 *p = reinterpret_cast<const lds_f4 *>(f + 2 * frag_slot(lane >> 4, lane & 15));
         return V8{p[0], p[1]};
@@ -149,25 +151,56 @@ struct AttnSeqs {
 };
 
 // One operand tile of 64 rows and 8 NC columns into LDS: 16-byte pieces through registers, in
-// fragment order; rows past the last repeat it.  256 threads, piece p = i 256 + tid: row p / NC.
+// fragment order; 256 threads, piece p = i 256 + tid: row p / NC.  Loads go through a buffer
+// resource that starts at the tile's first row and ends behind the sequence's last: one 32-bit
+// offset a thread in place of an address a piece, and rows past the last arrive as zeros.
 template <bool F32, int NC> struct TileStage {
     using Op = AttnOp<F32>;
+    using E = typename Op::E;
     static constexpr int N = 64 * NC / 256;
     static_assert(64 * NC % 256 == 0, "whole pieces per thread");
     typename Op::V8 x[N];
-    __device__ __forceinline__ void load(const typename Op::E *base, long long stride, int row0, int nrow, int tid) {
+    // rows row0 .. of the nrow rows at base; `stride` in elements, 64 rows of it below 2^31 bytes
+    __device__ __forceinline__ void load(const E *base, long long stride, int row0, int nrow, int tid) {
+        const long long left = nrow > row0 ? ((long long)(nrow - row0 - 1) * stride + 8 * NC) * (long long)sizeof(E) : 0;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<E *>(base + (long long)row0 * stride), 0, left > 0x7fffffff ? 0x7fffffff : (int)left, 0x00027000);
+        const int step = (256 / NC) * (int)stride * (int)sizeof(E);
+        int off = (tid / NC) * (int)stride * (int)sizeof(E) + (tid % NC) * 8 * (int)sizeof(E);
+        asm volatile("" : "+v"(off));  // or all N offsets would be kept in registers across the tiles
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int p = i * 256 + tid, r = row0 + p / NC, c = p % NC;
-            x[i] = Op::load(base + (long long)(r < nrow ? r : nrow - 1) * stride + 8 * c);
+            x[i] = piece(r, off);
+            off += step;
         }
     }
-    // fragments [row tile][nb blocks], this tile's columns from block b0 on
+    static __device__ __forceinline__ typename Op::V8 piece(__amdgpu_buffer_rsrc_t r, int off) {
+        typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+        if constexpr (F32) {
+            return f32x8s{__builtin_bit_cast(f32x4, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)),
+                          __builtin_bit_cast(f32x4, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0))};
+        } else {
+            return __builtin_bit_cast(bf16x8, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        }
+    }
+    // fragments [row tile][nb blocks], this tile's columns from block b0 on.  Row r = i 256 / NC + tid /
+    // NC, so piece i lies 16 NC-th of the tile behind piece 0 but for the swizzle, which flips one
+    // address bit (128, NC = 16) with i or none: two addresses and immediate offsets.
     __device__ __forceinline__ void store(lds_u8 *f, int nb, int b0, int tid) const {
+        static_assert(NC == 4 || NC == 8 || NC == 16, "32, 64 or 128 columns");
+        if constexpr (NC == 8 || NC == 16) {
+            const int r = tid / NC, c = tid % NC, scale = Op::FB / 1024;
+            lds_u8 *to = f + (perm_tile(r) * nb + b0 + (c >> 2)) * Op::FB;
+            const int a = scale * frag_slot(c & 3, perm_m(r));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int p = i * 256 + tid, r = p / NC, c = p % NC;
-            Op::put(f + (perm_tile(r) * nb + b0 + (c >> 2)) * Op::FB, c & 3, perm_m(r), x[i]);
+            for (int i = 0; i < N; ++i)
+                Op::put_at(to + (NC == 16 ? (a ^ (scale * 128 * (i & 1))) : a) + (NC == 16 ? i >> 1 : i) * 2 * nb * Op::FB, x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int p = i * 256 + tid, r = p / NC, c = p % NC;
+                Op::put(f + (perm_tile(r) * nb + b0 + (c >> 2)) * Op::FB, c & 3, perm_m(r), x[i]);
+            }
         }
     }
 };

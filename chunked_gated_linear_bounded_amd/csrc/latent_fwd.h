@@ -81,37 +81,43 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
         str.store(sk, NKB, NDB, tid);
         stv.store(sv, NDB, 0, tid);
         barrier_lds();
-        if (kt + 1 < ntk) {
-            stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);
-            str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
-            stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
-        }
         const int first = 64 * kt;
-        if (first > qw + 31 + shift) continue;  // nothing of this tile is seen by this wave
         f32x4 s[4][NQ];
+        // a key tile's fragments are read while the one before is multiplied, and no further ahead
+        V8 kf[2][NKB];
+        auto load_k = [&](int t) {
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) kf[t & 1][kb] = Op::get(sk + (t * NKB + kb) * Op::FB, lane);
+        };
+        load_k(0);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
+            if (t < 3) load_k(t + 1);
 #pragma unroll
             for (int x = 0; x < NQ; ++x) s[t][x] = zero;
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-                const V8 kf = Op::get(sk + (t * NKB + kb) * Op::FB, lane);
+            for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf, qf[x][kb], s[t][x]);
-            }
+                for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf[t & 1][kb], qf[x][kb], s[t][x]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        // the next tile, now that this one's scores are there (before, its registers would not fit);
+        // behind the last it loads nothing
+        stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);
+        str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
+        stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
         const bool edge = first + 64 > nk || first + 63 > qw + shift;
         float mx[NQ], alpha[NQ];
         bool grown = false;
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             if (edge) {
-                const int see = min(nk - 1, qw + 16 * x + n + shift) - first;  // last visible key of the tile
+                const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;  // last visible key
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (perm_row(t, 4 * g + i) > see) s[t][x][i] = -INFINITY;
+                        if (perm_row(t, i) > see) s[t][x][i] = -INFINITY;
             }
             float a = fmaxf(fmaxf(s[0][x][0], s[0][x][1]), fmaxf(s[0][x][2], s[0][x][3]));
 #pragma unroll
@@ -148,15 +154,25 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
             pf[0][x] = Op::pair(s[0][x], s[1][x]);
             pf[1][x] = Op::pair(s[2][x], s[3][x]);
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
+        V8 vf[2][2];
+        auto load_v = [&](int t) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
                 const lds_u8 *f0 = sv + (2 * kb * NDB + (t >> 1)) * Op::FB;
-                const V8 vf = Op::get_t(f0, f0 + NDB * Op::FB, t, lane);
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) O[t][x] = Op::mma(vf, pf[kb][x], O[t][x]);
+                vf[t & 1][kb] = Op::get_t(f0, f0 + NDB * Op::FB, t, lane);
             }
+        };
+        load_v(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t + 1 < NT) load_v(t + 1);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) O[t][x] = Op::mma(vf[t & 1][kb], pf[kb][x], O[t][x]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
