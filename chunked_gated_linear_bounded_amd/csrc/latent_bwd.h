@@ -112,13 +112,13 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(const LatentBwdArgs p
                 for (int x = 0; x < NQ; ++x) s[t][x] = d[t][x] = zero;
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb) {
-                    const V8 kf = Op::get(sk + ((2 * hb + t) * NKB + kb) * Op::FB, lane);
+                    const V8 kf = Op::get(sk + ((2 * hb + t) * NKB + kb) * Op::FB, kb, lane);
 #pragma unroll
                     for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf, qf[x][kb], s[t][x]);
                 }
 #pragma unroll
                 for (int kb = 0; kb < NDB; ++kb) {
-                    const V8 vf = Op::get(sv + ((2 * hb + t) * NDB + kb) * Op::FB, lane);
+                    const V8 vf = Op::get(sv + ((2 * hb + t) * NDB + kb) * Op::FB, kb, lane);
 #pragma unroll
                     for (int x = 0; x < NQ; ++x) d[t][x] = Op::mma(vf, df[x][kb], d[t][x]);
                 }
@@ -251,13 +251,13 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs 
                 for (int x = 0; x < NK; ++x) s[t][x] = d[t][x] = zero;
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb) {
-                    const V8 qf = Op::get(sq + ((2 * hb + t) * NKB + kb) * Op::FB, lane);
+                    const V8 qf = Op::get(sq + ((2 * hb + t) * NKB + kb) * Op::FB, kb, lane);
 #pragma unroll
                     for (int x = 0; x < NK; ++x) s[t][x] = Op::mma(qf, kf[x][kb], s[t][x]);
                 }
 #pragma unroll
                 for (int kb = 0; kb < NDB; ++kb) {
-                    const V8 of = Op::get(so + ((2 * hb + t) * NDB + kb) * Op::FB, lane);
+                    const V8 of = Op::get(so + ((2 * hb + t) * NDB + kb) * Op::FB, kb, lane);
 #pragma unroll
                     for (int x = 0; x < NK; ++x) d[t][x] = Op::mma(of, vf[x][kb], d[t][x]);
                 }

@@ -8,8 +8,15 @@
 // Everything is computed transposed: S^T = K Q^T puts keys on the accumulator's rows and queries on
 // its columns, so a lane's column is one query, the softmax reduces over a lane's own rows and two
 // lane exchanges, and the rows' scaling factors are lane scalars; and two key tiles of P^T are, as
-// they lie, the B operand of O^T = V^T P^T.  The fragment order, the permuted row index and the
-// transposed LDS read are those of gdr_common.h.
+// they lie, the B operand of O^T = V^T P^T.  The permuted row index and the transposed LDS read are
+// those of gdr_common.h.
+//
+// A fragment in LDS (16 rows x 32 columns of 16 bits, 1 KiB) is two planes of 64 8-byte slots: the
+// first and the last four columns of each lane's eight.  The transposed read takes 8 bytes from each
+// of 64 rows and column groups; from a plane they are 512 bytes one after the other, where out of
+// 16-byte slots they would use every second pair of banks (60 % of the LDS cycles were conflicts).
+// Lane (g, m) of column block kb has slot 16 g + (m ^ 8 (g / 2) ^ 2 (kb % 4)): all 32 lanes of a half
+// wave fall on different banks in the plain read, in the transposed one, and when rows are stored.
 //
 // bf16 inputs use 16x16x32 bf16 MFMAs, P and dS rounded to bf16; float32 inputs use float32 MFMAs
 // (eight 16x16x4 steps).  Softmax statistics and all sums are float32.
@@ -38,17 +45,24 @@ template <> struct AttnOp<false> {
         for (int i = 0; i < 4; ++i) { r[i] = (__bf16)x[i]; r[4 + i] = (__bf16)y[i]; }
         return r;
     }
-    __device__ __forceinline__ static void put_at(lds_u8 *p, const V8 &x) {
-        *reinterpret_cast<__attribute__((address_space(3))) V8 *>(p) = x;
+    typedef __attribute__((address_space(3))) bf16x4 lds_b4;
+    __device__ __forceinline__ static int slot(int kb, int g, int m) { return 8 * (16 * g + (m ^ (8 * (g >> 1)) ^ (2 * (kb & 3)))); }
+    // f: the fragment; kb: its column block
+    __device__ __forceinline__ static void put(lds_u8 *f, int kb, int g, int m, const V8 &x) {
+        lds_u8 *p = f + slot(kb, g, m);
+        *reinterpret_cast<lds_b4 *>(p) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+        *reinterpret_cast<lds_b4 *>(p + 512) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
     }
-    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) { put_at(f + frag_slot(g, m), x); }
-    __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
-        return *reinterpret_cast<const __attribute__((address_space(3))) V8 *>(f + frag_slot(lane >> 4, lane & 15));
+    __device__ __forceinline__ static V8 get(const lds_u8 *f, int kb, int lane) {
+        const lds_u8 *p = f + slot(kb, lane >> 4, lane & 15);
+        const bf16x4 a = *reinterpret_cast<const lds_b4 *>(p), b = *reinterpret_cast<const lds_b4 *>(p + 512);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    // transposed: rows = columns perm_row(tile, .), k = rows of the fragments f0 (row tile 2 kb), f1 (2 kb + 1)
+    // transposed: rows = columns perm_row(tile, .), k = rows of the fragments f0 (row tile 2 kb), f1 (2 kb
+    // + 1) of column block tile / 2
     __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int tile, int lane) {
-        const int g = lane >> 4, s = lane & 15, m = 4 * g + (s >> 2);
-        const int off = frag_slot(s & 3, m) + 8 * (tile & 1);
+        const int g = lane >> 4, s = lane & 15;
+        const int off = slot(tile >> 1, s & 3, 4 * g + (s >> 2)) + 512 * (tile & 1);
         const bf16x4 a = ld_tr16<bf16x4>(f0 + off), b = ld_tr16<bf16x4>(f1 + off);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
@@ -73,13 +87,12 @@ template <> struct AttnOp<true> {
     }
     __device__ __forceinline__ static V8 zero() { return V8{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}; }
     __device__ __forceinline__ static V8 pair(const f32x4 &x, const f32x4 &y) { return V8{x, y}; }
-    __device__ __forceinline__ static void put_at(lds_u8 *to, const V8 &x) {
-        lds_f4 *p = reinterpret_cast<lds_f4 *>(to);
+    __device__ __forceinline__ static void put(lds_u8 *f, int, int g, int m, const V8 &x) {
+        lds_f4 *p = reinterpret_cast<lds_f4 *>(f + 2 * frag_slot(g, m));
         p[0] = x.a;
         p[1] = x.b;
     }
-    __device__ __forceinline__ static void put(lds_u8 *f, int g, int m, const V8 &x) { put_at(f + 2 * frag_slot(g, m), x); }
-    __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
+    __device__ __forceinline__ static V8 get(const lds_u8 *f, int, int lane) {
         const lds_f4 *p = reinterpret_cast<const lds_f4 *>(f + 2 * frag_slot(lane >> 4, lane & 15));
         return V8{p[0], p[1]};
     }
@@ -183,25 +196,16 @@ template <bool F32, int NC> struct TileStage {
             return __builtin_bit_cast(bf16x8, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
         }
     }
-    // fragments [row tile][nb blocks], this tile's columns from block b0 on.  Row r = i 256 / NC + tid /
-    // NC, so piece i lies 16 NC-th of the tile behind piece 0 but for the swizzle, which flips one
-    // address bit (128, NC = 16) with i or none: two addresses and immediate offsets.
+    // fragments [row tile][nb blocks], this tile's columns from block b0 on.  Rows of later pieces are
+    // 16 (NC = 16) or 32 behind, which moves the fragment by a constant and flips at most one address
+    // bit: a few addresses and immediate offsets.
     __device__ __forceinline__ void store(lds_u8 *f, int nb, int b0, int tid) const {
         static_assert(NC == 4 || NC == 8 || NC == 16, "32, 64 or 128 columns");
-        if constexpr (NC == 8 || NC == 16) {
-            const int r = tid / NC, c = tid % NC, scale = Op::FB / 1024;
-            lds_u8 *to = f + (perm_tile(r) * nb + b0 + (c >> 2)) * Op::FB;
-            const int a = scale * frag_slot(c & 3, perm_m(r));
+        const int r = tid / NC, c = tid % NC, kb = b0 + (c >> 2);
+        lds_u8 *to = f + (perm_tile(r) * nb + kb) * Op::FB;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                Op::put_at(to + (NC == 16 ? (a ^ (scale * 128 * (i & 1))) : a) + (NC == 16 ? i >> 1 : i) * 2 * nb * Op::FB, x[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int p = i * 256 + tid, r = p / NC, c = p % NC;
-                Op::put(f + (perm_tile(r) * nb + b0 + (c >> 2)) * Op::FB, c & 3, perm_m(r), x[i]);
-            }
-        }
+        for (int i = 0; i < N; ++i)
+            Op::put(to + (NC == 16 ? i >> 1 : i) * 2 * nb * Op::FB, kb, c & 3, perm_m(r) ^ (NC == 16 ? 8 * (i & 1) : 0), x[i]);
     }
 };
 

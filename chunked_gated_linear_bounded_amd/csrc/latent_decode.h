@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
             const int x = i * 256 + tid, r = x / NC, cc = x % NC;
-            Op::put(sc + (perm_tile(r) * NKB + (cc >> 2)) * Op::FB, cc & 3, perm_m(r), st[i]);
+            Op::put(sc + (perm_tile(r) * NKB + (cc >> 2)) * Op::FB, cc >> 2, cc & 3, perm_m(r), st[i]);
         }
         barrier_lds();
         if (tile + 1 < last) load(tile + 1);
@@ -109,14 +109,14 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
             for (int t = 0; t < 2; ++t) {
                 s[t] = zero;
 #pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) s[t] = Op::mma(Op::get(sc + (t * NKB + kb) * Op::FB, lane), qf[kb], s[t]);
+                for (int kb = 0; kb < NKB; ++kb) s[t] = Op::mma(Op::get(sc + (t * NKB + kb) * Op::FB, kb, lane), qf[kb], s[t]);
             }
         } else {
             f32x4 x = zero;
             const int t = ws & 1;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb)
-                if (kb0 + kb < NKB) x = Op::mma(Op::get(sc + (t * NKB + kb0 + kb) * Op::FB, lane), qf[kb], x);
+                if (kb0 + kb < NKB) x = Op::mma(Op::get(sc + (t * NKB + kb0 + kb) * Op::FB, kb0 + kb, lane), qf[kb], x);
             lds_f4 *to = reinterpret_cast<lds_f4 *>(ss + (ht * KP * 2) * 1024);
             to[(kpart * 2 + t) * 64 + lane] = x;
             barrier_lds();

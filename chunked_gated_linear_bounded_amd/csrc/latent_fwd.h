@@ -32,7 +32,9 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int unit = (blockIdx.x >> 3) / p.ntile * 8 + (blockIdx.x & 7);
-    const int slot = p.ntile - 1 - (blockIdx.x >> 3) % p.ntile;
+    // the last tiles, which see most keys, first; when all work-groups find room at once (two a CU, 512),
+    // every other head from the first tile on, so that a CU gets a long one and a short one
+    const int at = (blockIdx.x >> 3) % p.ntile, slot = gridDim.x <= 512 && (unit & 8) ? at : p.ntile - 1 - at;
     if (unit >= p.NB * p.H) return;
     const int b = unit / p.H, h = unit % p.H;
     int seq, tile, q0, nq, k0, nk;
@@ -87,7 +89,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
         V8 kf[2][NKB];
         auto load_k = [&](int t) {
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) kf[t & 1][kb] = Op::get(sk + (t * NKB + kb) * Op::FB, lane);
+            for (int kb = 0; kb < NKB; ++kb) kf[t & 1][kb] = Op::get(sk + (t * NKB + kb) * Op::FB, kb, lane);
         };
         load_k(0);
 #pragma unroll
