@@ -117,14 +117,24 @@ template <> struct AttnOp<true> {
 __device__ __forceinline__ int perm_tile(int r) { return 2 * (r >> 5) + ((r >> 2) & 1); }
 __device__ __forceinline__ int perm_m(int r) { return 4 * ((r >> 3) & 3) + (r & 3); }
 
-// maximum / sum over the four lanes that hold one column
+// maximum / sum over the four lanes that hold one column: lanes l and l ^ 32, then l and l ^ 16,
+// exchanged in the vector unit (a shuffle through LDS takes some hundred cycles)
+template <typename F>
+__device__ __forceinline__ float col_reduce(float x, F f) {
+    const unsigned u = __builtin_bit_cast(unsigned, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned r0 = r[0], r1 = r[1];  // whole values: a bit cast of a vector's element takes element 0
+    const float y = f(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+    const unsigned v = __builtin_bit_cast(unsigned, y);
+    const auto q = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    const unsigned q0 = q[0], q1 = q[1];
+    return f(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
+}
 __device__ __forceinline__ float col_max(float x) {
-    x = fmaxf(x, __shfl_xor(x, 16, 64));
-    return fmaxf(x, __shfl_xor(x, 32, 64));
+    return col_reduce(x, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float col_sum(float x) {
-    x += __shfl_xor(x, 16, 64);
-    return x + __shfl_xor(x, 32, 64);
+    return col_reduce(x, [](float a, float b) { return a + b; });
 }
 
 // Sequences of queries and keys.  cu_q, cu_k NULL: N sequences of T queries and S keys.  Otherwise

@@ -1,11 +1,11 @@
 // Expanded latent attention, forward: one four-wave work-group per 128 queries of one head, 32
 // queries a wave (two column tiles), keys in tiles of 64 through LDS.  Per tile a wave does
 // 2 x 4 x (dn + dr) / 32 + 2 x 2 x dn / 16 MFMAs (80 at 128 + 64, 1,280 cycles) on 40 KiB of LDS
-// reads; the next tile's keys and values are in flight in registers meanwhile, so one 40 KiB buffer
-// is enough and two work-groups share a CU, one's softmax beside the other's MFMAs.
-// One pass over the keys with the running maximum and sum of the softmax; the accumulator is scaled
-// only when a maximum in the wave has grown.  Work-groups of a head share an XCD's L2; the last
-// queries, which see most keys, start first.
+// reads.  The next tile is loaded into registers between the score products and stored into the other
+// of two 40 KiB buffers between the value products, one barrier a tile; two work-groups share a CU
+// (all of its LDS), one's softmax beside the other's MFMAs.  (float32: one buffer, one work-group.)
+// One pass over the keys with the running maximum and sum of the softmax.  Work-groups of a head
+// share an XCD's L2.
 #pragma once
 #include "latent_common.h"
 
@@ -27,8 +27,8 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = DN / 16, NQ = 2;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[(4 * NKB + 4 * NDB) * Op::FB];
-    lds_u8 *sk = lds_base(smem), *sv = sk + 4 * NKB * Op::FB;
+    constexpr int TILE = (4 * NKB + 4 * NDB) * Op::FB, NBUF = F32 ? 1 : 2;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * TILE];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int unit = (blockIdx.x >> 3) / p.ntile * 8 + (blockIdx.x & 7);
@@ -72,48 +72,46 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
     }
     TileStage<F32, DN / 8> stk, stv;
     TileStage<F32, DR / 8> str;
+    auto load_tile = [&](int kt, int part) {
+        if (part == 0) stk.load(kp, p.sk.t, 64 * kt, nk, tid);
+        if (part == 1) str.load(rp, p.skr.t, 64 * kt, nk, tid);
+        if (part == 2) stv.load(vp, p.sv.t, 64 * kt, nk, tid);
+    };
+    auto store_tile = [&](lds_u8 *to, int part) {
+        if (part == 0) stk.store(to, NKB, 0, tid);
+        if (part == 1) str.store(to, NKB, NDB, tid);
+        if (part == 2) stv.store(to + 4 * NKB * Op::FB, NDB, 0, tid);
+    };
     if (ntk > 0) {
-        stk.load(kp, p.sk.t, 0, nk, tid);
-        str.load(rp, p.skr.t, 0, nk, tid);
-        stv.load(vp, p.sv.t, 0, nk, tid);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) load_tile(0, part);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) store_tile(lds_base(smem), part);
+        barrier_lds();
     }
     for (int kt = 0; kt < ntk; ++kt) {
-        barrier_lds();  // the last tile has been read
-        stk.store(sk, NKB, 0, tid);
-        str.store(sk, NKB, NDB, tid);
-        stv.store(sv, NDB, 0, tid);
-        barrier_lds();
+        const lds_u8 *sk = lds_base(smem) + (NBUF == 2 ? (kt & 1) * TILE : 0), *sv = sk + 4 * NKB * Op::FB;
         const int first = 64 * kt;
         f32x4 s[4][NQ];
-        // a key tile's fragments are read while the one before is multiplied, and no further ahead
-        V8 kf[2][NKB];
-        auto load_k = [&](int t) {
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) kf[t & 1][kb] = Op::get(sk + (t * NKB + kb) * Op::FB, kb, lane);
-        };
-        load_k(0);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            if (t < 3) load_k(t + 1);
+            V8 kf[NKB];
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) kf[kb] = Op::get(sk + (t * NKB + kb) * Op::FB, kb, lane);
+            if (t < 3) load_tile(kt + 1, t);  // behind the last tile it loads nothing
 #pragma unroll
             for (int x = 0; x < NQ; ++x) s[t][x] = zero;
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf[t & 1][kb], qf[x][kb], s[t][x]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf[kb], qf[x][kb], s[t][x]);
+            __builtin_amdgcn_sched_barrier(0);  // no fragments of later tiles in registers yet
         }
-        // the next tile, now that this one's scores are there (before, its registers would not fit);
-        // behind the last it loads nothing
-        stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);
-        str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
-        stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
-        const bool edge = first + 64 > nk || first + 63 > qw + shift;
-        float mx[NQ], alpha[NQ];
+        float mx[NQ];
         bool grown = false;
+        if (first + 64 > nk || first + 63 > qw + shift) {
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-            if (edge) {
+            for (int x = 0; x < NQ; ++x) {
                 const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;  // last visible key
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -121,41 +119,46 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
                     for (int i = 0; i < 4; ++i)
                         if (perm_row(t, i) > see) s[t][x][i] = -INFINITY;
             }
+        }
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
             float a = fmaxf(fmaxf(s[0][x][0], s[0][x][1]), fmaxf(s[0][x][2], s[0][x][3]));
 #pragma unroll
             for (int t = 1; t < 4; ++t) a = fmaxf(a, fmaxf(fmaxf(s[t][x][0], s[t][x][1]), fmaxf(s[t][x][2], s[t][x][3])));
-            a = col_max(a);
-            mx[x] = fmaxf(m[x], a * c);
-            grown |= mx[x] > m[x];
+            mx[x] = col_max(a) * c;
+            grown |= mx[x] > m[x] + 8.f;  // any finite score at first: m is -inf
         }
+        // the exponentials are taken against a maximum that may be 2^8 too small: bf16 and float32 keep
+        // their relative precision there, and the accumulator is scaled a few times a row, not every tile
         if (__builtin_amdgcn_ballot_w64(grown) != 0) {
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                alpha[x] = mx[x] == -INFINITY ? 1.f : ex2(m[x] - mx[x]);
-                m[x] = mx[x];
-                l[x] *= alpha[x];
+                const float now = fmaxf(m[x], mx[x]), alpha = now == -INFINITY ? 1.f : ex2(m[x] - now);
+                m[x] = now;
+                l[x] *= alpha;
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) O[t][x][i] *= alpha[x];
+                    for (int i = 0; i < 4; ++i) O[t][x][i] *= alpha;
             }
         }
         V8 pf[2][NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             const float mm = m[x] == -INFINITY ? 0.f : m[x];  // a column that has seen nothing yet
-            float sum = 0.f;
+            f32x4 sum = zero;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     s[t][x][i] = ex2(fmaf(s[t][x][i], c, -mm));
-                    sum += s[t][x][i];
+                    sum[i] += s[t][x][i];
                 }
-            l[x] += sum;
+            l[x] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             pf[0][x] = Op::pair(s[0][x], s[1][x]);
             pf[1][x] = Op::pair(s[2][x], s[3][x]);
         }
+        lds_u8 *to = lds_base(smem) + (NBUF == 2 ? ((kt & 1) ^ 1) * TILE : 0);
         V8 vf[2][2];
         auto load_v = [&](int t) {
 #pragma unroll
@@ -169,11 +172,18 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t + 1 < NT) load_v(t + 1);
+            if (NBUF == 2 && t < 3) store_tile(to, t);  // the next tile into the other buffer
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int x = 0; x < NQ; ++x) O[t][x] = Op::mma(vf[t & 1][kb], pf[kb][x], O[t][x]);
             __builtin_amdgcn_sched_barrier(0);
+        }
+        barrier_lds();  // this tile has been read, and (two buffers) the next one is there
+        if constexpr (NBUF == 1) {
+#pragma unroll
+            for (int part = 0; part < 3; ++part) store_tile(to, part);
+            barrier_lds();
         }
     }
 #pragma unroll
