@@ -16,7 +16,11 @@ static hipError_t fwd_t(const LatentLaunch &p) {
     const int nt = AttnSeqs::tiles(p.cu_q != nullptr, p.N, p.T, 128);
     const LatentFwdArgs a{p.q, p.k, p.kr, p.v, st3(p.sq), st3(p.sk), st3(p.skr), st3(p.sv),
                           AttnSeqs{p.cu_q, p.cu_k, p.N, p.T, p.S}, p.H, p.B, nt, p.scale, p.out, p.lse};
-    hipLaunchKernelGGL((latent_fwd_kernel<DN, DR, F32>), dim3(grid_of(p.B * p.H, nt)), dim3(256), 0, p.stream, a);
+    const dim3 grid(grid_of(p.B * p.H, nt));
+    if (!F32 && grid.x <= 512)  // two on each CU: see latent_fwd.h
+        hipLaunchKernelGGL((latent_fwd_kernel<DN, DR, F32, F32 ? 1 : 2>), grid, dim3(F32 ? 256 : 512), 0, p.stream, a);
+    else
+        hipLaunchKernelGGL((latent_fwd_kernel<DN, DR, F32, 1>), grid, dim3(256), 0, p.stream, a);
     return hipGetLastError();
 }
 

@@ -173,23 +173,24 @@ struct AttnSeqs {
     static int tiles(bool packed, int N, int total, int bt) { return packed ? total / bt + N : (total + bt - 1) / bt; }
 };
 
-// One operand tile of 64 rows and 8 NC columns into LDS: 16-byte pieces through registers, in
+// One operand tile of ROWS rows and 8 NC columns into LDS: 16-byte pieces through registers, in
 // fragment order; 256 threads, piece p = i 256 + tid: row p / NC.  Loads go through a buffer
 // resource that starts at the tile's first row and ends behind the sequence's last: one 32-bit
 // offset a thread in place of an address a piece, and rows past the last arrive as zeros.
-template <bool F32, int NC> struct TileStage {
+template <bool F32, int NC, int ROWS = 64> struct TileStage {
     using Op = AttnOp<F32>;
     using E = typename Op::E;
-    static constexpr int N = 64 * NC / 256;
-    static_assert(64 * NC % 256 == 0, "whole pieces per thread");
+    static constexpr int N = (ROWS * NC + 255) / 256;
+    static constexpr bool ALL = ROWS * NC >= 256;  // every thread has a piece
+    static_assert(ROWS * NC % 256 == 0 || !ALL, "whole pieces per thread");
     typename Op::V8 x[N];
-    // rows row0 .. of the nrow rows at base; `stride` in elements, 64 rows of it below 2^31 bytes
+    // rows row0 .. of the nrow rows at base; `stride` in elements, a tile of it below 2^31 bytes
     __device__ __forceinline__ void load(const E *base, long long stride, int row0, int nrow, int tid) {
-        const long long left = nrow > row0 ? ((long long)(nrow - row0 - 1) * stride + 8 * NC) * (long long)sizeof(E) : 0;
+        const int st = (int)stride * (int)sizeof(E), left = min(max(nrow - row0, 0), ROWS);
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<E *>(base + (long long)row0 * stride), 0, left > 0x7fffffff ? 0x7fffffff : (int)left, 0x00027000);
-        const int step = (256 / NC) * (int)stride * (int)sizeof(E);
-        int off = (tid / NC) * (int)stride * (int)sizeof(E) + (tid % NC) * 8 * (int)sizeof(E);
+            const_cast<E *>(base + (long long)row0 * stride), 0, left > 0 ? (left - 1) * st + 8 * NC * (int)sizeof(E) : 0, 0x00027000);
+        const int step = (256 / NC) * st;
+        int off = (tid / NC) * st + (tid % NC) * 8 * (int)sizeof(E);
         asm volatile("" : "+v"(off));  // or all N offsets would be kept in registers across the tiles
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -213,6 +214,7 @@ template <bool F32, int NC> struct TileStage {
         static_assert(NC == 4 || NC == 8 || NC == 16, "32, 64 or 128 columns");
         const int r = tid / NC, c = tid % NC, kb = b0 + (c >> 2);
         lds_u8 *to = f + (perm_tile(r) * nb + kb) * Op::FB;
+        if (!ALL && tid >= ROWS * NC) return;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             Op::put(to + (NC == 16 ? i >> 1 : i) * 2 * nb * Op::FB, kb, c & 3, perm_m(r) ^ (NC == 16 ? 8 * (i & 1) : 0), x[i]);

@@ -1,11 +1,18 @@
-// Expanded latent attention, forward: one four-wave work-group per 128 queries of one head, 32
-// queries a wave (two column tiles), keys in tiles of 64 through LDS.  Per tile a wave does
-// 2 x 4 x (dn + dr) / 32 + 2 x 2 x dn / 16 MFMAs (80 at 128 + 64, 1,280 cycles) on 40 KiB of LDS
-// reads.  The next tile is loaded into registers between the score products and stored into the other
-// of two 40 KiB buffers between the value products, one barrier a tile; two work-groups share a CU
-// (all of its LDS), one's softmax beside the other's MFMAs.  (float32: one buffer, one work-group.)
-// One pass over the keys with the running maximum and sum of the softmax.  Work-groups of a head
-// share an XCD's L2.
+// Expanded latent attention, forward: one work-group per 128 queries of one head, keys in tiles of 64
+// through LDS, 32 queries a wave (two column tiles).  Per tile a wave does 2 x 4 x (dn + dr) / 32 + 2 x
+// 2 x dn / 16 MFMAs (80 at 128 + 64, 1,280 cycles) on 40 KiB of LDS reads.  The next tile is loaded
+// into registers between the score products and stored into the other of two 40 KiB buffers between
+// the value products, one barrier a tile.  One pass over the keys with the running maximum and sum of
+// the softmax.  Work-groups of a head share an XCD's L2; the last queries, which see most keys, start
+// first.
+//
+// NG = 1: four waves, two work-groups on a CU, one's softmax beside the other's MFMAs.  NG = 2: two
+// groups of four waves take every other key tile for the same queries and join their accumulators at
+// the end.  While no more work-groups come after the first two on a CU, a long row of a causal triangle
+// soon runs alone with one wave a SIMD (4,600 cycles a tile), and two groups keep both waves at work:
+// 16 heads x 4096 tokens (512 work-groups) 118 us with two groups, 140 with one; 1,184 work-groups of
+// ragged packed prompts 148 with two, 124 with one.  So two groups up to two work-groups a CU.
+// (float32: one group, one buffer.)
 #pragma once
 #include "latent_common.h"
 
@@ -21,20 +28,19 @@ struct LatentFwdArgs {
     float *lse;                // [B][H][T]
 };
 
-template <int DN, int DR, bool F32>
-__global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const LatentFwdArgs p) {
+template <int DN, int DR, bool F32, int NG>
+__global__ __launch_bounds__(256 * NG, F32 ? 1 : 2) void latent_fwd_kernel(const LatentFwdArgs p) {
     using Op = AttnOp<F32>;
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = DN / 16, NQ = 2;
     constexpr int TILE = (4 * NKB + 4 * NDB) * Op::FB, NBUF = F32 ? 1 : 2;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * TILE];
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    static_assert(NG == 1 || 256 * (NT * NQ + 1) * 16 <= NG * NBUF * TILE, "the second group's accumulators fit");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[NG * NBUF * TILE];
+    const int tid = threadIdx.x & 255, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int unit = (blockIdx.x >> 3) / p.ntile * 8 + (blockIdx.x & 7);
-    // the last tiles, which see most keys, first; when all work-groups find room at once (two a CU, 512),
-    // every other head from the first tile on, so that a CU gets a long one and a short one
-    const int at = (blockIdx.x >> 3) % p.ntile, slot = gridDim.x <= 512 && (unit & 8) ? at : p.ntile - 1 - at;
+    const int slot = p.ntile - 1 - (blockIdx.x >> 3) % p.ntile;
     if (unit >= p.NB * p.H) return;
     const int b = unit / p.H, h = unit % p.H;
     int seq, tile, q0, nq, k0, nk;
@@ -82,15 +88,18 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
         if (part == 1) str.store(to, NKB, NDB, tid);
         if (part == 2) stv.store(to + 4 * NKB * Op::FB, NDB, 0, tid);
     };
+    lds_u8 *mine = lds_base(smem) + grp * NBUF * TILE;
     if (ntk > 0) {
 #pragma unroll
-        for (int part = 0; part < 3; ++part) load_tile(0, part);
+        for (int part = 0; part < 3; ++part) load_tile(grp, part);
 #pragma unroll
-        for (int part = 0; part < 3; ++part) store_tile(lds_base(smem), part);
+        for (int part = 0; part < 3; ++part) store_tile(mine, part);
         barrier_lds();
     }
-    for (int kt = 0; kt < ntk; ++kt) {
-        const lds_u8 *sk = lds_base(smem) + (NBUF == 2 ? (kt & 1) * TILE : 0), *sv = sk + 4 * NKB * Op::FB;
+    int buf = 0;
+    for (int k2 = 0; k2 < ntk; k2 += NG) {  // as many rounds for either group: a tile past the last is all masked
+        const int kt = k2 + grp;
+        const lds_u8 *sk = mine + (NBUF == 2 ? buf * TILE : 0), *sv = sk + 4 * NKB * Op::FB;
         const int first = 64 * kt;
         f32x4 s[4][NQ];
 #pragma unroll
@@ -98,7 +107,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
             V8 kf[NKB];
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb) kf[kb] = Op::get(sk + (t * NKB + kb) * Op::FB, kb, lane);
-            if (t < 3) load_tile(kt + 1, t);  // behind the last tile it loads nothing
+            if (t < 3) load_tile(kt + NG, t);  // behind the last tile it loads nothing
 #pragma unroll
             for (int x = 0; x < NQ; ++x) s[t][x] = zero;
 #pragma unroll
@@ -158,7 +167,8 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
             pf[0][x] = Op::pair(s[0][x], s[1][x]);
             pf[1][x] = Op::pair(s[2][x], s[3][x]);
         }
-        lds_u8 *to = lds_base(smem) + (NBUF == 2 ? ((kt & 1) ^ 1) * TILE : 0);
+        buf ^= 1;
+        lds_u8 *to = mine + (NBUF == 2 ? buf * TILE : 0);
         V8 vf[2][2];
         auto load_v = [&](int t) {
 #pragma unroll
@@ -184,6 +194,29 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_fwd_kernel(const Late
 #pragma unroll
             for (int part = 0; part < 3; ++part) store_tile(to, part);
             barrier_lds();
+        }
+    }
+    if constexpr (NG == 2) {  // the second group hands its accumulators over; both are past the last barrier
+        typedef __attribute__((address_space(3))) f32x4 lds_f4;
+        lds_f4 *ex = reinterpret_cast<lds_f4 *>(lds_base(smem)) + tid;
+        if (grp == 1) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) ex[256 * (t * NQ + x)] = O[t][x];
+            ex[256 * NT * NQ] = f32x4{m[0], l[0], m[1], l[1]};
+        }
+        barrier_lds();
+        if (grp == 1) return;
+        const f32x4 ml = ex[256 * NT * NQ];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const float now = fmaxf(m[x], ml[2 * x]);
+            const float a = now == -INFINITY ? 0.f : ex2(m[x] - now), d = now == -INFINITY ? 0.f : ex2(ml[2 * x] - now);
+            m[x] = now;
+            l[x] = l[x] * a + ml[2 * x + 1] * d;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) O[t][x] = O[t][x] * a + ex[256 * (t * NQ + x)] * d;
         }
     }
 #pragma unroll
