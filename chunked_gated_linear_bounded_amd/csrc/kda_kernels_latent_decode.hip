@@ -6,16 +6,13 @@
 
 namespace kda {
 
-// waves on each 16 heads: what the heads leave of a work-group's four
-static int waves_per_tile(int H) { return H <= 16 ? 4 : H <= 32 ? 2 : 1; }
-static int head_groups(int H) {
-    const int tiles = (H + 15) / 16, ht = 4 / waves_per_tile(H);
-    return (tiles + ht - 1) / ht;
-}
+// Four waves on 16 heads or on 32, eight on 64 (float32, whose registers do not allow eight: 32).
+static int heads_per_group(const LatentLaunch &p) { return p.H <= 16 ? 16 : p.H <= 32 || p.fp32 ? 32 : 64; }
+static int head_groups(const LatentLaunch &p) { return (p.H + heads_per_group(p) - 1) / heads_per_group(p); }
 // Parts the keys are cut into: about three work-groups a CU, each with at least 64 keys of the longest
 // sequence that the table can hold (the lengths are on the device).
 static int splits(const LatentLaunch &p) {
-    const long long want = 768 / ((long long)p.B * head_groups(p.H)), most = ((long long)p.max_pages * p.page + 63) / 64;
+    const long long want = 768 / ((long long)p.B * head_groups(p)), most = ((long long)p.max_pages * p.page + 63) / 64;
     const long long n = want < most ? want : most;
     return n < 1 ? 1 : (n > 64 ? 64 : (int)n);
 }
@@ -24,13 +21,13 @@ size_t latent_decode_bytes(const LatentLaunch &p) {
     return n == 1 ? 0 : (size_t)p.B * n * p.H * (p.dc + 1) * 4;
 }
 
-template <int DC, bool F32, int WS>
+template <int DC, bool F32, int WS, int NW>
 static hipError_t run(const LatentLaunch &p) {
-    LatentDecodeArgs a{p.q, p.cache, p.table, p.lengths, p.B, p.H, p.pages, p.page, p.max_pages, splits(p), head_groups(p.H),
+    LatentDecodeArgs a{p.q, p.cache, p.table, p.lengths, p.B, p.H, p.pages, p.page, p.max_pages, splits(p), head_groups(p),
                        p.scale, p.out, p.lse, reinterpret_cast<float *>(p.workspace), nullptr};
     a.part_lse = a.part + (size_t)p.B * a.nsplit * p.H * DC;
     const unsigned grid = (unsigned)((p.B * a.nsplit + 7) / 8 * 8) * (unsigned)a.hgroups;
-    hipLaunchKernelGGL((latent_decode_kernel<DC, 64, F32, WS>), dim3(grid), dim3(256), 0, p.stream, a);
+    hipLaunchKernelGGL((latent_decode_kernel<DC, 64, F32, WS, NW>), dim3(grid), dim3(64 * NW), 0, p.stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.nsplit == 1) return e;
     hipLaunchKernelGGL((latent_join_kernel<DC, typename AttnOp<F32>::E>), dim3(p.H, p.B), dim3(DC / 4), 0, p.stream, a);
@@ -38,8 +35,11 @@ static hipError_t run(const LatentLaunch &p) {
 }
 template <int DC, bool F32>
 static hipError_t by_heads(const LatentLaunch &p) {
-    const int ws = waves_per_tile(p.H);
-    return ws == 4 ? run<DC, F32, 4>(p) : ws == 2 ? run<DC, F32, 2>(p) : run<DC, F32, 1>(p);
+    const int heads = heads_per_group(p);
+    if (heads == 16) return run<DC, F32, 4, 4>(p);
+    if constexpr (!F32)
+        if (heads == 64) return run<DC, F32, 2, 8>(p);
+    return run<DC, F32, 2, 4>(p);
 }
 hipError_t launch_latent_decode(const LatentLaunch &p) {
     if (p.dc == 256) return p.fp32 ? by_heads<256, true>(p) : by_heads<256, false>(p);

@@ -2,17 +2,17 @@
 // c = [latent (dc), rotary part (dr)]: s_j = scale q . c_j, o = sum p_j c_j[:dc].
 //
 // A row serves every head as key and as value, so the cache is read once for up to 64 heads: a
-// four-wave work-group takes one sequence, one part of its keys and 64 / WS heads, with WS waves on
-// each 16 heads.  32 keys at a time go through registers into LDS (36 KiB at 512 + 64, bf16); S^T is
-// C Q^T, and O^T = C^T P^T reads the same tile transposed.  WS = 1: a wave does both products for its
-// 16 heads alone.  WS > 1 (few heads): the waves split S by key tile (WS = 4: also by half of the
-// contraction), hand it round through LDS, and split the dc rows of O^T.
+// work-group of NW waves takes one sequence, one part of its keys and 16 NW / WS heads, with WS waves
+// on each 16 heads.  32 keys at a time go through registers into LDS (36 KiB at 512 + 64, bf16); S^T is
+// C Q^T, and O^T = C^T P^T reads the same tile transposed.  The waves on the same heads split S by key
+// tile (WS = 4: also by half of the contraction), hand it round through LDS, and split the dc rows of
+// O^T: one wave alone would need 128 registers for O^T and 72 for its queries, and spilled.
 //
 // Up to 16 heads the 2 * 16 * (576 + 512) flops a 1,152-byte row costs are far below what HBM lets
 // pass; at 128 heads (two work-groups on the same keys, side by side on one XCD) the 272 KiB of LDS
 // reads per tile and work-group take about the time HBM needs for the tile.  The keys are split
-// over work-groups until the chip has about three a CU; the parts are joined by their
-// log-sum-exps in a second kernel.
+// over work-groups until the chip has several a CU; the parts are joined by their log-sum-exps in a
+// second kernel.
 #pragma once
 #include "latent_common.h"
 
@@ -31,19 +31,19 @@ struct LatentDecodeArgs {
     float *part_lse;
 };
 
-template <int DC, int DR, bool F32, int WS>
-__global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const LatentDecodeArgs p) {
+template <int DC, int DR, bool F32, int WS, int NW>
+__global__ __launch_bounds__(64 * NW, F32 ? 1 : 2) void latent_decode_kernel(const LatentDecodeArgs p) {
     using Op = AttnOp<F32>;
     using E = typename Op::E;
     using V8 = typename Op::V8;
-    constexpr int D = DC + DR, NKB = D / 32, NC = D / 8, HT = 4 / WS;  // head tiles of the work-group
+    constexpr int D = DC + DR, NKB = D / 32, NC = D / 8, HT = NW / WS;  // head tiles of the work-group
     constexpr int NT = DC / 16 / WS;                                   // rows tiles of O^T per wave
     constexpr int KP = WS == 4 ? 2 : 1, NB = (NKB + KP - 1) / KP;      // parts of the contraction
-    constexpr int NST = 32 * NC / 256;
-    static_assert(32 * NC % 256 == 0, "whole pieces per thread");
+    constexpr int TPR = 2 * NW, NST = (NC + TPR - 1) / TPR;            // threads on a row, pieces a thread
+    static_assert(WS > 1 && TPR % 4 == 0, "S goes through LDS; a thread's pieces keep their place in a block");
     typedef __attribute__((address_space(3))) f32x4 lds_f4;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * NKB * Op::FB];
-    __shared__ __attribute__((aligned(16))) unsigned char sx[WS > 1 ? HT * KP * 2 * 1024 : 16];
+    __shared__ __attribute__((aligned(16))) unsigned char sx[HT * KP * 2 * 1024];
     __shared__ long long soff[2][32];
     lds_u8 *sc = lds_base(smem), *ss = lds_base(sx);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
@@ -65,19 +65,22 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
     for (int kb = 0; kb < NB; ++kb)
         qf[kb] = kb0 + kb < NKB ? Op::load(reinterpret_cast<const E *>(p.q) + ((size_t)b * p.H + hc) * D + 32 * (kb0 + kb) + 8 * g)
                                 : Op::zero();
-    // row of the cache that holds key j (past the last: the last); a page outside the cache is clipped
-    auto offset = [&](int tile) {
-        const int j = min(32 * tile + tid, len - 1);
-        int pg = p.table[(size_t)b * p.max_pages + j / p.page];
+    // Row r of a tile: key 32 tile + r (past the last: the last), on a page of the table; pages outside the
+    // cache are clipped.  The table is read two tiles before the rows, in front of the rows' loads: a
+    // wait for it is then no wait for them.
+    const int *table = p.table + (size_t)b * p.max_pages;
+    auto key_of = [&](int tile) { return min(32 * min(tile, last - 1) + (tid & 31), len - 1); };
+    auto put_row = [&](int tile, int pg) {
         pg = pg < 0 ? 0 : (pg >= p.pages ? p.pages - 1 : pg);
-        return ((long long)pg * p.page + j % p.page) * D;
+        if (tid < 32) soff[tile & 1][tid] = ((long long)pg * p.page + key_of(tile) % p.page) * D;
     };
     V8 st[NST];
     auto load = [&](int tile) {
+        const E *row = cache + soff[tile & 1][tid / TPR];
 #pragma unroll
         for (int i = 0; i < NST; ++i) {
-            const int x = i * 256 + tid;
-            st[i] = Op::load(cache + soff[tile & 1][x / NC] + 8 * (x % NC));
+            const int piece = tid % TPR + TPR * i;
+            st[i] = Op::load(row + 8 * (NC % TPR == 0 || piece < NC ? piece : NC - 1));
         }
     };
     f32x4 O[NT];
@@ -85,47 +88,40 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
 #pragma unroll
     for (int t = 0; t < NT; ++t) O[t] = zero;
     float m = -INFINITY, l = 0.f;
+    int pg = 0;  // this thread's page of the tile after next
     if (first < last) {
-        if (tid < 32) {
-            soff[first & 1][tid] = offset(first);
-            if (first + 1 < last) soff[(first + 1) & 1][tid] = offset(first + 1);
-        }
+        put_row(first, table[key_of(first) / p.page]);
+        put_row(first + 1, table[key_of(first + 1) / p.page]);
+        pg = table[key_of(first + 2) / p.page];
         __syncthreads();
         load(first);
     }
     for (int tile = first; tile < last; ++tile) {
         barrier_lds();  // the last tile has been read
+        const int r = tid / TPR, c0 = tid % TPR;
+        lds_u8 *to = sc + (perm_tile(r) * NKB + (c0 >> 2)) * Op::FB;
 #pragma unroll
-        for (int i = 0; i < NST; ++i) {
-            const int x = i * 256 + tid, r = x / NC, cc = x % NC;
-            Op::put(sc + (perm_tile(r) * NKB + (cc >> 2)) * Op::FB, cc >> 2, cc & 3, perm_m(r), st[i]);
-        }
+        for (int i = 0; i < NST; ++i)
+            if (NC % TPR == 0 || TPR * i + TPR <= NC || c0 + TPR * i < NC)
+                Op::put(to + TPR / 4 * i * Op::FB, TPR / 4 * i + (c0 >> 2), c0 & 3, perm_m(r), st[i]);
         barrier_lds();
-        if (tile + 1 < last) load(tile + 1);
-        if (tile + 2 < last && tid < 32) soff[tile & 1][tid] = offset(tile + 2);
+        put_row(tile + 2, pg);
+        pg = table[key_of(tile + 3) / p.page];
+        load(tile + 1);  // behind the last tile: its last rows again, not used
         f32x4 s[2];
-        if constexpr (WS == 1) {
+        f32x4 x = zero;
+        const int t = ws & 1;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                s[t] = zero;
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) s[t] = Op::mma(Op::get(sc + (t * NKB + kb) * Op::FB, kb, lane), qf[kb], s[t]);
-            }
-        } else {
-            f32x4 x = zero;
-            const int t = ws & 1;
-#pragma unroll
-            for (int kb = 0; kb < NB; ++kb)
-                if (kb0 + kb < NKB) x = Op::mma(Op::get(sc + (t * NKB + kb0 + kb) * Op::FB, kb0 + kb, lane), qf[kb], x);
-            lds_f4 *to = reinterpret_cast<lds_f4 *>(ss + (ht * KP * 2) * 1024);
-            to[(kpart * 2 + t) * 64 + lane] = x;
-            barrier_lds();
-            s[0] = to[lane];
-            s[1] = to[64 + lane];
-            if constexpr (KP == 2) {
-                s[0] += to[128 + lane];
-                s[1] += to[192 + lane];
-            }
+        for (int kb = 0; kb < NB; ++kb)
+            if (kb0 + kb < NKB) x = Op::mma(Op::get(sc + (t * NKB + kb0 + kb) * Op::FB, kb0 + kb, lane), qf[kb], x);
+        lds_f4 *sp = reinterpret_cast<lds_f4 *>(ss + (ht * KP * 2) * 1024);
+        sp[(kpart * 2 + t) * 64 + lane] = x;
+        barrier_lds();
+        s[0] = sp[lane];
+        s[1] = sp[64 + lane];
+        if constexpr (KP == 2) {
+            s[0] += sp[128 + lane];
+            s[1] += sp[192 + lane];
         }
         if (32 * tile + 32 > len) {
 #pragma unroll
@@ -160,6 +156,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
             const int tt = ws * NT + t;
             const lds_u8 *f0 = sc + (tt >> 1) * Op::FB;
             O[t] = Op::mma(Op::get_t(f0, f0 + NKB * Op::FB, tt, lane), pf, O[t]);
+            if (t % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // eight fragments in flight, not all
         }
     }
     l = col_sum(l);
@@ -171,6 +168,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
         for (int t = 0; t < NT; t += 2) {
             const f32x4 x = O[t] * inv, y = O[t + 1] * inv;
             Op::store8(o + 16 * (ws * NT + t) + 8 * g, x, y);
+            __builtin_amdgcn_sched_barrier(0);  // not all scaled copies at once: they would push Q into scratch
         }
         if (g == 0 && ws == 0) p.lse[(size_t)b * p.H + head] = lse2 * kLn2;
         return;
@@ -183,6 +181,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void latent_decode_kernel(const L
         float *o = p.part + row * DC + 16 * (ws * NT + t) + 8 * g;
         *reinterpret_cast<f32x4 *>(o) = O[t] * inv;
         *reinterpret_cast<f32x4 *>(o + 4) = O[t + 1] * inv;
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
