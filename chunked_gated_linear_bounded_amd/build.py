@@ -41,6 +41,7 @@ UNITS = [
     ("kda_kernels_gdr.hip", "kda_kernels_gdr.o", []),
     ("kda_kernels_gdr_bwd.hip", "kda_kernels_gdr_bwd.o", []),
     ("kda_kernels_latent.hip", "kda_kernels_latent.o", []),
+    ("kda_kernels_latent_bwd.hip", "kda_kernels_latent_bwd.o", []),
     ("kda_kernels_latent_decode.hip", "kda_kernels_latent_decode.o", []),
     ("kda_abi.cpp", "kda_abi.o", []),
     ("kda_abi_gdr.cpp", "kda_abi_gdr.o", []),
