@@ -24,7 +24,7 @@ size_t gdr_fwd_bytes(const GdrLaunch &p) {
 template <int DK, bool F32, int NCT>
 static hipError_t run_state(const GdrStateArgs &a, hipStream_t stream) {
     const int units = (a.seqs.N * a.H + 7) / 8 * 8;
-    hipLaunchKernelGGL((gdr_state_kernel<DK, F32, NCT, 0, F32 ? 2 : 1>), dim3(units * (a.dv / 16 / NCT)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((gdr_state_kernel<DK, F32, NCT, 0, F32 ? 2 : 1>), dim3(units * (a.dv / 16 / NCT)), dim3(512), 0, stream, a);
     return hipGetLastError();
 }
 
