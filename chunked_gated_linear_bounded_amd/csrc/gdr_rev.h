@@ -29,25 +29,31 @@ struct GdrRevArgs {
 };
 
 template <int DK, int NI, int NCT> struct GdrRevLds {
-    static constexpr int NKB = DK / 32;
-    // dP' [piece][kb][ct]; dO [piece < NI][kb 2][ct]; dU, H = scale e^G dO, F = b e^G dX [piece][kb 2][ct]
-    static constexpr int XP = 0, XO = XP + 2 * NKB * NCT * 1024, XU = XO + NI * 2 * NCT * 1024, XH = XU + 4 * NCT * 1024;
-    static constexpr int XF = XH + 4 * NCT * 1024, K = XF + 4 * NCT * 1024, Q = K + NI * 64 * DK * 2;
-    static constexpr int T = Q + NI * 64 * DK * 2, M = T + 2 * GdrLayout::kTri, BYTES = M + 2 * GdrLayout::kTri;
+    static constexpr int NKB = DK / 32, KB = NI * 64 * DK * 2;
+    // dP' [piece][kb][ct]; dU, F = b e^G dX, H = scale e^G dO [piece][kb 2][ct]; dO [piece < NI][kb 2][ct]
+    static constexpr int XP = 0, XU = XP + 2 * NKB * NCT * 1024, XF = XU + 4 * NCT * 1024, XH = XF + 4 * NCT * 1024;
+    static constexpr int XO = XH + 4 * NCT * 1024;
+    // float32 tiles from lane to lane: M^T dO and dX [wave][ct], Q^T H [wave][tile][ct]
+    static constexpr int D0 = XO + NI * 2 * NCT * 1024, DX = D0 + 4 * NCT * 1024, DQ = DX + 4 * NCT * 1024;
+    static constexpr int K = DQ + (DK / 16) * NCT * 1024, T = K + KB, Q = T + 2 * GdrLayout::kTri, M = Q + KB;
+    static constexpr int HEAD = M + 2 * GdrLayout::kTri, BYTES = HEAD + 2 * GdrLayout::kHead;
 };
 
 template <int DK, bool F32, int NCT>
-__global__ __launch_bounds__(256) void gdr_rev_kernel(const GdrRevArgs p) {
+__global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
     using E = typename std::conditional<F32, float, __bf16>::type;
     constexpr int NI = F32 ? 2 : 1, NKB = DK / 32, NTW = DK / 64;
     using S = GdrRevLds<DK, NI, NCT>;
     constexpr GdrLayout L{NI, DK, 2};
     constexpr GdrSave SV{NI, DK};
     typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
+    typedef __attribute__((address_space(3))) f32x4 lds_f4;
+    typedef __attribute__((address_space(3))) float lds_f1;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
-    __shared__ float sMax[16];  // per wave: max |dP'|, |dU|, |dO| of the next chunk
+    __shared__ float sMax[24];  // per wave: max |dP'|, |dU|, |F|, |dO|, |M^T dO|, |Q^T H|
+    __shared__ int sExp[2];     // exponents of dP's and of dX's pieces
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wid & 3;
     __builtin_assume(w >= 0 && w < 4);
     const int gh = p.dv / (16 * NCT), id = blockIdx.x;
     const int unit = id / (8 * gh) * 8 + (id & 7), slice = (id >> 3) % gh * NCT;
@@ -59,38 +65,258 @@ __global__ __launch_bounds__(256) void gdr_rev_kernel(const GdrRevArgs p) {
     const unsigned char *krec = p.keys + ((size_t)(b * nkey + h / p.r) * p.nslot + slot0) * L.key_bytes();
     const unsigned char *vrec = p.vals + ((size_t)(b * p.H + h) * p.nslot + slot0) * L.val_bytes();
     const int row0 = perm_row(w, 4 * g), fo = frag_slot(g, n);
-    const E *dop = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)start * p.sdo.t + col;
-    E *dvp = reinterpret_cast<E *>(p.dv_out) + ((size_t)(b * p.H + h) * p.seqs.T + start + row0) * p.dv + col;
-    unsigned char *save = p.save + (((size_t)(b * p.H + h) * p.nslot + slot0) * (p.dv / 16) + slice) * SV.bytes();
     lds_u8 *sx = lds_base(smem);
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    // rows of the transpose of a 64x64 lower triangle: column tile w, contraction block kb (>= w's own)
+    auto tri_t = [&](const lds_u8 *f, int kb) {
+        const lds_u8 *f0 = f + tri_frag(2 * kb, w >> 1) * 1024, *f1 = f + tri_frag(2 * kb + 1, w >> 1) * 1024;
+        return ld_frag_t(f0, f1, w, lane);
+    };
 
-    E vn[NCT][4];
-    auto load_do = [&](int c) {
+    if (wid >= 4) {  // ------------------------- loads, the terms without the state, outputs
+        const E *dop = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)start * p.sdo.t + col;
+        E *dvp = reinterpret_cast<E *>(p.dv_out) + ((size_t)(b * p.H + h) * p.seqs.T + start + row0) * p.dv + col;
+        unsigned char *save = p.save + (((size_t)(b * p.H + h) * p.nslot + slot0) * (p.dv / 16) + slice) * SV.bytes();
+        // a quarter of each; chunks before the first are loaded as the first and not used
+        f16x8 kf[NI][NKB], tf[3], qf[NI][NKB], mf[3];
+        E vn[NCT][4];
+        f32x4 eG;
+        float head;
+        int em, eq, at = 0;  // at: the chunk of qf, mf, vn
+        auto load_kt = [&](int c) {
+            c = max(c, 0);
+            const unsigned char *r = krec + (size_t)c * L.key_bytes() + w * NKB * 1024 + fo;
+            const unsigned char *t = vrec + (size_t)c * L.val_bytes() + 3 * w * 1024 + fo;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 64 * c + row0 + i, rc = row < len ? row : len - 1;
+            for (int x = 0; x < NI; ++x)
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) kf[x][kb] = *reinterpret_cast<const f16x8 *>(r + L.k_off(x) + kb * 1024);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) tf[i] = *reinterpret_cast<const f16x8 *>(t + L.t_off(0) + i * 1024);
+        };
+        auto load_head = [&](int c) {
+            head = *reinterpret_cast<const float *>(vrec + (size_t)max(c, 0) * L.val_bytes() + 4 * (64 * w + lane));
+        };
+        auto load_qm = [&](int c) {
+            at = c = max(c, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = min(64 * c + row0 + i, len - 1);
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) vn[ct][i] = dop[(long long)row * p.sdo.t + 16 * ct];
+            }
+            const unsigned char *r = krec + (size_t)c * L.key_bytes() + w * NKB * 1024 + fo;
+            const unsigned char *v = vrec + (size_t)c * L.val_bytes();
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) qf[x][kb] = *reinterpret_cast<const f16x8 *>(r + L.q_off(x) + kb * 1024);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) mf[i] = *reinterpret_cast<const f16x8 *>(v + L.m_off(0) + (3 * w + i) * 1024 + fo);
+            eG = *reinterpret_cast<const f32x4 *>(v + 4 * row0);
+            em = reinterpret_cast<const int *>(v)[194];
+            eq = reinterpret_cast<const int *>(v)[196];
+        };
+        auto grad_of = [&](int ct, int i) { return 64 * at + row0 + i < len ? to_f(vn[ct][i]) : 0.f; };  // none past the last row
+        auto publish_max = [&]() {
+            float m = 0.f;
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(grad_of(ct, i)));
+            m = wave_max(m);
+            if (lane == 0) sMax[12 + w] = m;
+        };
+        auto put_kt = [&]() {
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb)
+                    *reinterpret_cast<lds_f16x8 *>(sx + S::K + x * L.mat() + (w * NKB + kb) * 1024 + fo) = kf[x][kb];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<lds_f16x8 *>(sx + S::T + (3 * w + i) * 1024 + fo) = tf[i];
+        };
+        auto put_head = [&](int c) { *reinterpret_cast<lds_f1 *>(sx + S::HEAD + (c & 1) * L.kHead + 4 * (64 * w + lane)) = head; };
+        int eo = 0, eh = 0, em_ = 0, eq_ = 0;  // of what is in LDS
+        auto put_qm = [&]() {
+            const float omax = max4(sMax + 12);
+            eo = gdr_exp(omax);
+            eh = gdr_exp(fabsf(p.scale) * omax);
+            em_ = em;
+            eq_ = eq;
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb)
+                    *reinterpret_cast<lds_f16x8 *>(sx + S::Q + x * L.mat() + (w * NKB + kb) * 1024 + fo) = qf[x][kb];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<lds_f16x8 *>(sx + S::M + (3 * w + i) * 1024 + fo) = mf[i];
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                const E x = dop[(long long)rc * p.sdo.t + 16 * ct];
-                vn[ct][i] = row < len ? x : (E)0.f;  // rows past the last have no gradient
+                const f32x4 d = {grad_of(ct, 0), grad_of(ct, 1), grad_of(ct, 2), grad_of(ct, 3)};
+                f32x4 hd;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hd[i] = p.scale * eG[i] * d[i];
+                f16x4 hi, lo;
+                const int to = ((w >> 1) * NCT + ct) * 1024;
+                if constexpr (NI == 2) {
+                    split4(d, pow2f(eo), hi, lo);
+                    st_half_frag(sx + S::XO + 2 * NCT * 1024 + to, w & 1, g, n, lo);
+                } else {
+                    hi = round4(d, pow2f(eo));  // exact
+                }
+                st_half_frag(sx + S::XO + to, w & 1, g, n, hi);
+                split4(hd, pow2f(eh), hi, lo);
+                st_half_frag(sx + S::XH + to, w & 1, g, n, hi);
+                st_half_frag(sx + S::XH + 2 * NCT * 1024 + to, w & 1, g, n, lo);
+            }
+        };
+        f32x4 d0[NCT];
+        auto mul_m = [&]() {  // M^T dO
+            f32x4 y[NCT], y1[NCT];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) y[ct] = y1[ct] = zero;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb == 1 || w < 2) {
+                    const f16x8 mh = tri_t(sx + S::M, kb), ml = tri_t(sx + S::M + L.kTri, kb);
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        const f16x8 oh = ld_frag(sx + S::XO + (kb * NCT + ct) * 1024, lane);
+                        y[ct] = mma16(mh, oh, y[ct]);
+                        y1[ct] = mma16(ml, oh, y1[ct]);
+                        if constexpr (NI == 2) y1[ct] = mma16(mh, ld_frag(sx + S::XO + ((2 + kb) * NCT + ct) * 1024, lane), y1[ct]);
+                    }
+                }
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d0[ct][i] = scale_down(y[ct][i] + y1[ct][i], em_ + eo);
+        };
+        auto put_terms = [&]() {  // M^T dO, and Q^T (scale e^G dO)
+            float m0 = 0.f, mq = 0.f;
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                *reinterpret_cast<lds_f4 *>(sx + S::D0 + (w * NCT + ct) * 1024 + 16 * lane) = d0[ct];
+                m0 = max_abs4(d0[ct], m0);
+            }
+#pragma unroll
+            for (int t = 0; t < NTW; ++t) {
+                const int tile = NTW * w + t;
+                f32x4 a[NCT], a1[NCT];
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) a[ct] = a1[ct] = zero;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const lds_u8 *f0 = sx + S::Q + (2 * kb * NKB + (tile >> 1)) * 1024, *f1 = f0 + NKB * 1024;
+                    const f16x8 q = ld_frag_t(f0, f1, tile, lane);
+                    f16x8 q1 = q;
+                    if constexpr (NI == 2) q1 = ld_frag_t(f0 + L.mat(), f1 + L.mat(), tile, lane);
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        const f16x8 hh = ld_frag(sx + S::XH + (kb * NCT + ct) * 1024, lane);
+                        const f16x8 hl = ld_frag(sx + S::XH + ((2 + kb) * NCT + ct) * 1024, lane);
+                        a[ct] = mma16(q, hh, a[ct]);
+                        a1[ct] = mma16(q, hl, a1[ct]);
+                        if constexpr (NI == 2) a1[ct] = mma16(q1, hh, a1[ct]);
+                    }
+                }
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[ct][i] = scale_down(a[ct][i] + a1[ct][i], eq_ + eh);
+                    *reinterpret_cast<lds_f4 *>(sx + S::DQ + (tile * NCT + ct) * 1024 + 16 * lane) = a[ct];
+                    mq = max_abs4(a[ct], mq);
+                }
+            }
+            m0 = wave_max(m0);
+            mq = wave_max(mq);
+            if (lane == 0) {
+                sMax[16 + w] = m0;
+                sMax[20 + w] = mq;
+            }
+        };
+        if (nchunk > 0) {
+            load_qm(nchunk - 1);
+            load_head(nchunk - 1);
+            publish_max();
+            barrier_lds();  // (a)
+            put_qm();
+            load_qm(nchunk - 2);
+            barrier_lds();  // (b)
+            mul_m();
+            put_terms();
+            put_head(nchunk - 1);
+            load_head(nchunk - 2);
+            publish_max();
+            barrier_lds();  // (c)
+            put_qm();
+            load_qm(nchunk - 3);
+            load_kt(nchunk - 1);
+        }
+        // chunk c's K and T, c - 1's terms and header, c - 2's Q, M and dO go to LDS
+        for (int c = nchunk - 1; c >= 0; --c) {
+            barrier_lds();  // (1)
+            const int ep = sExp[0];
+            put_kt();
+            mul_m();
+            if (w < NKB)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    const f16x8 ph = ld_frag(sx + S::XP + (w * NCT + ct) * 1024, lane);
+                    const f16x8 pl = ld_frag(sx + S::XP + ((NKB + w) * NCT + ct) * 1024, lane);
+                    unsigned char *sv = save + ((size_t)c * (p.dv / 16) + ct) * SV.bytes() + w * 1024 + fo;
+                    if constexpr (NI == 2) {
+                        *reinterpret_cast<f16x8 *>(sv + SV.p_off(0)) = ph;
+                        *reinterpret_cast<f16x8 *>(sv + SV.p_off(1)) = pl;
+                    } else {
+                        *reinterpret_cast<f16x8 *>(sv + SV.p_off(0)) = ph + pl;  // both pieces together round to one
+                    }
+                }
+            barrier_lds();  // (2)
+            load_kt(c - 1);
+            put_terms();
+            put_head(c - 1);
+            load_head(c - 2);
+            publish_max();
+            barrier_lds();  // (3)
+            const int ex = sExp[1];
+            f32x4 dX[NCT];
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) dX[ct] = *reinterpret_cast<const lds_f4 *>(sx + S::DX + (w * NCT + ct) * 1024 + 16 * lane);
+            const f32x4 be = *reinterpret_cast<const lds_f4 *>(sx + S::HEAD + (c & 1) * L.kHead + 512 + 4 * row0);
+            put_qm();
+            load_qm(c - 3);
+            unsigned char *sv = save + (size_t)c * (p.dv / 16) * SV.bytes();
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                f16x4 hi, lo;
+                if constexpr (NI == 2) split4(dX[ct], pow2f(ex), hi, lo);
+                else hi = round4(dX[ct], pow2f(ex));
+                unsigned char *to = sv + ct * SV.bytes() + (w >> 1) * 1024 + fo + 8 * (w & 1);
+                *reinterpret_cast<f16x4 *>(to + SV.u_off(0)) = hi;
+                if constexpr (NI == 2) *reinterpret_cast<f16x4 *>(to + SV.u_off(1)) = lo;
+                if (w == 0 && lane == 0) {
+                    reinterpret_cast<int *>(sv + ct * SV.bytes())[0] = ep;
+                    reinterpret_cast<int *>(sv + ct * SV.bytes())[1] = ex;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (64 * c + row0 + i < len) dvp[(size_t)(64 * c + i) * p.dv + 16 * ct] = from_f<E>(be[i] * dX[ct][i]);
             }
         }
-    };
-    auto max_do = [&]() {
-        float m = 0.f;
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(to_f(vn[ct][i])));
-        return wave_max(m);
-    };
+        return;
+    }
+
+    // ------------------------------------------ the chain
+    __builtin_amdgcn_s_setprio(3);
     f32x4 P[NTW][NCT];  // dP
     const size_t state0 = ((size_t)(seq * p.H + h) * p.dv + col) * DK;
 #pragma unroll
     for (int t = 0; t < NTW; ++t)
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct)
-            P[t][ct] = p.dfinal == nullptr ? f32x4{0.f, 0.f, 0.f, 0.f}
+            P[t][ct] = p.dfinal == nullptr ? zero
                            : *reinterpret_cast<const f32x4 *>(p.dfinal + state0 + (size_t)16 * ct * DK + perm_row(NTW * w + t, 4 * g));
     auto max_p = [&]() {
         float m = 0.f;
@@ -114,107 +340,59 @@ __global__ __launch_bounds__(256) void gdr_rev_kernel(const GdrRevArgs p) {
                 st_half_frag(f + NKB * NCT * 1024, tile & 1, g, n, lo);
             }
     };
-    f16x8 kf[NI][NKB], qf[NI][NKB], tf[2][2], mf[2][2];
-    f32x4 eG, eL, be;
-    float last_, bm_, cl_;
-    int et_, em_, ek_, eq_;
-    const int tri0 = w < 2 ? w : 2 * w - 2, tri1 = w < 2 ? 0 : 1024;  // waves 0, 1: one causal fragment
-    auto load_rec = [&](int c) {
-        const unsigned char *r = krec + (size_t)c * L.key_bytes() + w * NKB * 1024 + fo;
-        const unsigned char *v = vrec + (size_t)c * L.val_bytes(), *t = v + tri0 * 1024 + fo;
+    f16x8 kf[NI][NKB];
+    f32x4 eG, eL, be, h0, h1, D0[NCT], DQ[NTW][NCT];
+    float cl_, ks_, d0max, dqmax;
+    auto load_k = [&](int c) {
+        const unsigned char *r = krec + (size_t)max(c, 0) * L.key_bytes() + w * NKB * 1024 + fo;
 #pragma unroll
         for (int x = 0; x < NI; ++x)
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-                kf[x][kb] = *reinterpret_cast<const f16x8 *>(r + L.k_off(x) + kb * 1024);
-                qf[x][kb] = *reinterpret_cast<const f16x8 *>(r + L.q_off(x) + kb * 1024);
-            }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                tf[x][o] = *reinterpret_cast<const f16x8 *>(t + L.t_off(x) + o * tri1);
-                mf[x][o] = *reinterpret_cast<const f16x8 *>(t + L.m_off(x) + o * tri1);
-            }
-        const float *f = reinterpret_cast<const float *>(v);
-        const int *e = reinterpret_cast<const int *>(v);
-        eG = *reinterpret_cast<const f32x4 *>(f + row0);
-        eL = *reinterpret_cast<const f32x4 *>(f + 64 + row0);
-        be = *reinterpret_cast<const f32x4 *>(f + 128 + row0);
-        last_ = f[192];
-        et_ = e[193];
-        em_ = e[194];
-        ek_ = e[195];
-        eq_ = e[196];
-        bm_ = f[198];
-        cl_ = f[201];
+            for (int kb = 0; kb < NKB; ++kb) kf[x][kb] = *reinterpret_cast<const f16x8 *>(r + L.k_off(x) + kb * 1024);
     };
-    // rows of the transpose of a 64x64 lower triangle: column tile w, contraction block kb (>= w's own)
-    auto tri_t = [&](const lds_u8 *f, int kb) {
-        const lds_u8 *f0 = f + tri_frag(2 * kb, w >> 1) * 1024, *f1 = f + tri_frag(2 * kb + 1, w >> 1) * 1024;
-        return ld_frag_t(f0, f1, w, lane);
+    // what the other waves have laid out for chunk c
+    auto get = [&](int c) {
+        const lds_u8 *hd = sx + S::HEAD + (c & 1) * L.kHead;
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            D0[ct] = *reinterpret_cast<const lds_f4 *>(sx + S::D0 + (w * NCT + ct) * 1024 + 16 * lane);
+#pragma unroll
+            for (int t = 0; t < NTW; ++t)
+                DQ[t][ct] = *reinterpret_cast<const lds_f4 *>(sx + S::DQ + ((NTW * w + t) * NCT + ct) * 1024 + 16 * lane);
+        }
+        eG = *reinterpret_cast<const lds_f4 *>(hd + 4 * row0);
+        eL = *reinterpret_cast<const lds_f4 *>(hd + 256 + 4 * row0);
+        be = *reinterpret_cast<const lds_f4 *>(hd + 512 + 4 * row0);
+        h0 = *reinterpret_cast<const lds_f4 *>(hd + 768);
+        h1 = *reinterpret_cast<const lds_f4 *>(hd + 784);
+        cl_ = *reinterpret_cast<const lds_f1 *>(hd + 804);
+        ks_ = *reinterpret_cast<const lds_f1 *>(hd + 808);
+        d0max = max4(sMax + 16);
+        dqmax = max4(sMax + 20);
     };
     int ep = 0;
     if (nchunk > 0) {
-        load_rec(nchunk - 1);
-        load_do(nchunk - 1);
-        const float mp = max_p(), mo = max_do();
-        if (lane == 0) {
-            sMax[w] = mp;
-            sMax[8 + w] = mo;
-        }
-        barrier_lds();
+        load_k(nchunk - 1);
+        const float mp = max_p();
+        if (lane == 0) sMax[w] = mp;
+        barrier_lds();  // (a)
         ep = gdr_exp(max4(sMax));
         put_p(ep);
+        if (threadIdx.x == 0) sExp[0] = ep;
+        barrier_lds();  // (b)
+        barrier_lds();  // (c)
+        get(nchunk - 1);
     }
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     for (int c = nchunk - 1; c >= 0; --c) {
-        const int next = c > 0 ? c - 1 : 0;
-        barrier_lds();  // dP' is there; the last chunk's LDS has been read
-        const float pmax = max4(sMax), omax = max4(sMax + 8), last = last_, bm = bm_, cl = cl_;
-        const int et = et_, em = em_, ek = ek_, eq = eq_;
-        const f32x4 eL0 = eL, eG0 = eG, be0 = be;
-        const int eo = gdr_exp(omax), eh = gdr_exp(fabsf(p.scale) * omax);
-#pragma unroll
-        for (int x = 0; x < NI; ++x)
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-                *reinterpret_cast<lds_f16x8 *>(sx + S::K + x * L.mat() + (w * NKB + kb) * 1024 + fo) = kf[x][kb];
-                *reinterpret_cast<lds_f16x8 *>(sx + S::Q + x * L.mat() + (w * NKB + kb) * 1024 + fo) = qf[x][kb];
-            }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-                if (o == 0 || w >= 2) {
-                    *reinterpret_cast<lds_f16x8 *>(sx + S::T + x * GdrLayout::kTri + (tri0 + o) * 1024 + fo) = tf[x][o];
-                    *reinterpret_cast<lds_f16x8 *>(sx + S::M + x * GdrLayout::kTri + (tri0 + o) * 1024 + fo) = mf[x][o];
-                }
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-            const f32x4 d = {to_f(vn[ct][0]), to_f(vn[ct][1]), to_f(vn[ct][2]), to_f(vn[ct][3])};
-            f32x4 hd;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hd[i] = p.scale * eG0[i] * d[i];
-            f16x4 hi, lo;
-            const int at = ((w >> 1) * NCT + ct) * 1024;
-            if constexpr (NI == 2) {
-                split4(d, pow2f(eo), hi, lo);
-                st_half_frag(sx + S::XO + 2 * NCT * 1024 + at, w & 1, g, n, lo);
-            } else {
-                hi = round4(d, pow2f(eo));  // exact
-            }
-            st_half_frag(sx + S::XO + at, w & 1, g, n, hi);
-            split4(hd, pow2f(eh), hi, lo);
-            st_half_frag(sx + S::XH + at, w & 1, g, n, hi);
-            st_half_frag(sx + S::XH + 2 * NCT * 1024 + at, w & 1, g, n, lo);
-        }
-        barrier_lds();
+        barrier_lds();  // (1)
+        const float et_ = h0[1], ek_ = h0[3];
+        const int et = __builtin_bit_cast(int, et_), ek = __builtin_bit_cast(int, ek_);
+        const float pmax = max4(sMax), last = h0[0], bm = h1[2], cl = cl_, ksum = ks_;
 
         // ---- 1. dU = M^T dO + e^{G_last - G} K dP'
-        f32x4 Z[NCT], Z1[NCT], Y[NCT], Y1[NCT];
+        f32x4 Z[NCT], Z1[NCT];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) Z[ct] = Z1[ct] = Y[ct] = Y1[ct] = zero;
+        for (int ct = 0; ct < NCT; ++ct) Z[ct] = Z1[ct] = zero;
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
@@ -224,36 +402,14 @@ __global__ __launch_bounds__(256) void gdr_rev_kernel(const GdrRevArgs p) {
                 Z[ct] = mma16(kf[0][kb], ph, Z[ct]);
                 Z1[ct] = mma16(kf[0][kb], pl, Z1[ct]);
                 if constexpr (NI == 2) Z1[ct] = mma16(kf[1][kb], ph, Z1[ct]);
-                if (kb == w && NKB == 4 || kb == w >> 1 && NKB == 2 && (w & 1) == 0) {
-                    unsigned char *sv = save + ((size_t)c * (p.dv / 16) + ct) * SV.bytes() + kb * 1024 + fo;
-                    if constexpr (NI == 2) {
-                        *reinterpret_cast<f16x8 *>(sv + SV.p_off(0)) = ph;
-                        *reinterpret_cast<f16x8 *>(sv + SV.p_off(1)) = pl;
-                    } else {
-                        *reinterpret_cast<f16x8 *>(sv + SV.p_off(0)) = ph + pl;
-                    }
-                }
             }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-            if (kb == 1 || w < 2) {
-                const f16x8 mh = tri_t(sx + S::M, kb), ml = tri_t(sx + S::M + GdrLayout::kTri, kb);
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    const f16x8 oh = ld_frag(sx + S::XO + (kb * NCT + ct) * 1024, lane);
-                    Y[ct] = mma16(mh, oh, Y[ct]);
-                    Y1[ct] = mma16(ml, oh, Y1[ct]);
-                    if constexpr (NI == 2) Y1[ct] = mma16(mh, ld_frag(sx + S::XO + ((2 + kb) * NCT + ct) * 1024, lane), Y1[ct]);
-                }
-            }
-        const int eu = gdr_exp(64.f * ldexp2(1.f, 14 - em) * omax + cl * pmax);
+        const int eu = gdr_exp(d0max + cl * pmax);
         float um = 0.f;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 dU;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                dU[i] = scale_down(Y[ct][i] + Y1[ct][i], em + eo) + eL0[i] * scale_down(Z[ct][i] + Z1[ct][i], ek + ep);
+            for (int i = 0; i < 4; ++i) dU[i] = D0[ct][i] + eL[i] * scale_down(Z[ct][i] + Z1[ct][i], ek + ep);
             um = max_abs4(dU, um);
             f16x4 hi, lo;
             split4(dU, pow2f(eu), hi, lo);
@@ -263,109 +419,96 @@ __global__ __launch_bounds__(256) void gdr_rev_kernel(const GdrRevArgs p) {
         }
         um = wave_max(um);
         if (lane == 0) sMax[4 + w] = um;
-        load_rec(next);
-        load_do(next);
-        barrier_lds();
+        load_k(c - 1);
+        barrier_lds();  // (2)
 
-        // ---- 2. dX = T^T dU, dV = b dX, F = b e^G dX
+        // ---- 2. dX = T^T dU, F = b e^G dX
         const float xbound = 64.f * ldexp2(1.f, 14 - et) * max4(sMax + 4);
         const int ex = gdr_exp(xbound), ef = gdr_exp(bm * xbound);
-        f32x4 dX[NCT];
+        float fm = 0.f;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 z = zero, z1 = zero;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
                 if (kb == 1 || w < 2) {
-                    const f16x8 th = tri_t(sx + S::T, kb), tl = tri_t(sx + S::T + GdrLayout::kTri, kb);
+                    const f16x8 th = tri_t(sx + S::T, kb), tl = tri_t(sx + S::T + L.kTri, kb);
                     const f16x8 uh = ld_frag(sx + S::XU + (kb * NCT + ct) * 1024, lane);
                     const f16x8 ul = ld_frag(sx + S::XU + ((2 + kb) * NCT + ct) * 1024, lane);
                     z = mma16(th, uh, z);
                     z1 = mma16(tl, uh, mma16(th, ul, z1));
                 }
-            f32x4 F;
+            f32x4 dX, F;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                dX[ct][i] = scale_down(z[i] + z1[i], et + eu);
-                F[i] = be0[i] * eG0[i] * dX[ct][i];
+                dX[i] = scale_down(z[i] + z1[i], et + eu);
+                F[i] = be[i] * eG[i] * dX[i];
             }
+            fm = max_abs4(F, fm);
             f16x4 hi, lo;
             split4(F, pow2f(ef), hi, lo);
             lds_u8 *f = sx + S::XF + ((w >> 1) * NCT + ct) * 1024;
             st_half_frag(f, w & 1, g, n, hi);
             st_half_frag(f + 2 * NCT * 1024, w & 1, g, n, lo);
+            *reinterpret_cast<lds_f4 *>(sx + S::DX + (w * NCT + ct) * 1024 + 16 * lane) = dX;
         }
-        barrier_lds();
+        fm = wave_max(fm);
+        if (lane == 0) sMax[8 + w] = fm;
+        if (threadIdx.x == 0) sExp[1] = ex;
+        barrier_lds();  // (3)
 
-        // ---- 3. dP = e^{G_last} dP' + Q^T (scale e^G dO) - K^T F
+        // ---- 3. dP = e^{G_last} dP' + Q^T H - K^T F
+        f16x8 fh[2][NCT], fl[2][NCT], kt[NI][NTW][2];
 #pragma unroll
-        for (int t = 0; t < NTW; ++t) {
-            const int tile = NTW * w + t;
-            f32x4 a[NCT], a1[NCT], d[NCT], d1[NCT];
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) a[ct] = a1[ct] = d[ct] = d1[ct] = zero;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const int at = (2 * kb * NKB + (tile >> 1)) * 1024;
-                const f16x8 q = ld_frag_t(sx + S::Q + at, sx + S::Q + at + NKB * 1024, tile, lane);
-                const f16x8 k = ld_frag_t(sx + S::K + at, sx + S::K + at + NKB * 1024, tile, lane);
-                f16x8 q1 = q, k1 = k;
-                if constexpr (NI == 2) {
-                    q1 = ld_frag_t(sx + S::Q + L.mat() + at, sx + S::Q + L.mat() + at + NKB * 1024, tile, lane);
-                    k1 = ld_frag_t(sx + S::K + L.mat() + at, sx + S::K + L.mat() + at + NKB * 1024, tile, lane);
-                }
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    const f16x8 hh = ld_frag(sx + S::XH + (kb * NCT + ct) * 1024, lane);
-                    const f16x8 hl = ld_frag(sx + S::XH + ((2 + kb) * NCT + ct) * 1024, lane);
-                    const f16x8 fh = ld_frag(sx + S::XF + (kb * NCT + ct) * 1024, lane);
-                    const f16x8 fl = ld_frag(sx + S::XF + ((2 + kb) * NCT + ct) * 1024, lane);
-                    a[ct] = mma16(q, hh, a[ct]);
-                    a1[ct] = mma16(q, hl, a1[ct]);
-                    d[ct] = mma16(k, fh, d[ct]);
-                    d1[ct] = mma16(k, fl, d1[ct]);
-                    if constexpr (NI == 2) {
-                        a1[ct] = mma16(q1, hh, a1[ct]);
-                        d1[ct] = mma16(k1, fh, d1[ct]);
-                    }
-                }
+            for (int ct = 0; ct < NCT; ++ct) {
+                fh[kb][ct] = ld_frag(sx + S::XF + (kb * NCT + ct) * 1024, lane);
+                fl[kb][ct] = ld_frag(sx + S::XF + ((2 + kb) * NCT + ct) * 1024, lane);
             }
+#pragma unroll
+            for (int t = 0; t < NTW; ++t) {
+                const int tile = NTW * w + t;
+                const lds_u8 *f0 = sx + S::K + (2 * kb * NKB + (tile >> 1)) * 1024, *f1 = f0 + NKB * 1024;
+#pragma unroll
+                for (int x = 0; x < NI; ++x) kt[x][t][kb] = ld_frag_t(f0 + x * L.mat(), f1 + x * L.mat(), tile, lane);
+            }
+        }
+        const float fmax = max4(sMax + 8);
+        f32x4 base[NTW][NCT];
+#pragma unroll
+        for (int t = 0; t < NTW; ++t)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    P[t][ct][i] = fmaf(P[t][ct][i], last, scale_down(a[ct][i] + a1[ct][i], eq + eh)) -
-                                  scale_down(d[ct][i] + d1[ct][i], ek + ef);
-        }
-        // the state's bound needs the next maximum, so it is taken, not bounded: one more barrier
-        const float mp = max_p(), mo = max_do();
-        if (lane == 0) {
-            sMax[12 + w] = mp;
-            sMax[8 + w] = mo;
-        }
-        // outputs of this chunk meanwhile
-        unsigned char *sv = save + (size_t)c * (p.dv / 16) * SV.bytes();
+                for (int i = 0; i < 4; ++i) base[t][ct][i] = fmaf(P[t][ct][i], last, DQ[t][ct][i]);
+        const float qmax = dqmax;
+        __builtin_amdgcn_sched_barrier(0);
+        get(c - 1);  // behind the reads that are waited for
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-            f16x4 hi, lo;
-            if constexpr (NI == 2) split4(dX[ct], pow2f(ex), hi, lo);
-            else hi = round4(dX[ct], pow2f(ex));
-            unsigned char *to = sv + ct * SV.bytes() + (w >> 1) * 1024 + fo + 8 * (w & 1);
-            *reinterpret_cast<f16x4 *>(to + SV.u_off(0)) = hi;
-            if constexpr (NI == 2) *reinterpret_cast<f16x4 *>(to + SV.u_off(1)) = lo;
-            if (threadIdx.x == 0) {
-                reinterpret_cast<int *>(sv + ct * SV.bytes())[0] = ep;
-                reinterpret_cast<int *>(sv + ct * SV.bytes())[1] = ex;
-            }
+        for (int t = 0; t < NTW; ++t) {
+            f32x4 d[NCT], d1[NCT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (64 * c + row0 + i < len) dvp[(size_t)(64 * c + i) * p.dv + 16 * ct] = from_f<E>(be0[i] * dX[ct][i]);
+            for (int ct = 0; ct < NCT; ++ct) d[ct] = d1[ct] = zero;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    d[ct] = mma16(kt[0][t][kb], fh[kb][ct], d[ct]);
+                    d1[ct] = mma16(kt[0][t][kb], fl[kb][ct], d1[ct]);
+                    if constexpr (NI == 2) d1[ct] = mma16(kt[1][t][kb], fh[kb][ct], d1[ct]);
+                }
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) P[t][ct][i] = base[t][ct][i] - scale_down(d[ct][i] + d1[ct][i], ek + ef);
         }
-        barrier_lds();
-        const float newmax = max4(sMax + 12);
-        if (threadIdx.x < 4) sMax[threadIdx.x] = sMax[12 + threadIdx.x];
-        ep = gdr_exp(newmax);
+        ep = gdr_exp(last * pmax + qmax + ksum * fmax);
         put_p(ep);
+        const float mp = max_p();
+        if (lane == 0) sMax[w] = mp;
+        if (threadIdx.x == 0) sExp[0] = ep;
     }
     if (p.dinit != nullptr)
 #pragma unroll

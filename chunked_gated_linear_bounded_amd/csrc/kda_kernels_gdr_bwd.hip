@@ -32,11 +32,12 @@ size_t gdr_bwd_bytes(const GdrLaunch &p) { return plan(p).total; }
 
 template <int DK, bool F32, int NCT>
 static hipError_t passes(const GdrLaunch &p, const GdrStateArgs &a, const GdrRevArgs &c) {
-    const dim3 grid((p.N * p.H + 7) / 8 * 8 * (p.dv / 16 / NCT));
-    hipLaunchKernelGGL((gdr_state_kernel<DK, F32, NCT, 1, 2>), grid, dim3(512), 0, p.stream, a);
+    constexpr int NR = F32 && DK == 128 ? 1 : NCT;  // two float32 tiles would need 170 KiB of LDS
+    const int units = (p.N * p.H + 7) / 8 * 8;
+    hipLaunchKernelGGL((gdr_state_kernel<DK, F32, NCT, 1, 2>), dim3(units * (p.dv / 16 / NCT)), dim3(512), 0, p.stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdr_rev_kernel<DK, F32, NCT>), grid, dim3(256), 0, p.stream, c);
+    hipLaunchKernelGGL((gdr_rev_kernel<DK, F32, NR>), dim3(units * (p.dv / 16 / NR)), dim3(512), 0, p.stream, c);
     return hipGetLastError();
 }
 
