@@ -26,12 +26,12 @@ static hipError_t bwd_t(const LatentLaunch &p) {
     hipError_t e = hipSuccess;
     if (p.T > 0) {
         a.ntile = AttnSeqs::tiles(packed, p.N, p.T, BT);
-        hipLaunchKernelGGL((latent_dq_kernel<DN, DR, F32>), dim3(grid_of(p.B * p.H, a.ntile)), dim3(256), 0, p.stream, a);
+        hipLaunchKernelGGL((latent_dq_kernel<DN, DR, F32>), dim3(grid_of(p.B * p.H, a.ntile)), dim3(512), 0, p.stream, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (p.S > 0) {
         a.ntile = AttnSeqs::tiles(packed, p.N, p.S, BT);
-        hipLaunchKernelGGL((latent_dkv_kernel<DN, DR, F32>), dim3(grid_of(p.B * p.H, a.ntile)), dim3(256), 0, p.stream, a);
+        hipLaunchKernelGGL((latent_dkv_kernel<DN, DR, F32>), dim3(grid_of(p.B * p.H, a.ntile)), dim3(512), 0, p.stream, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL((latent_dkr_kernel<E>), dim3((unsigned)(((long long)p.S * DR / 4 + 255) / 256), p.B), dim3(256), 0,
                            p.stream, part, seqs, p.H, DR, (E *)p.dkr);

@@ -5,10 +5,13 @@
 // key_j = [k_j, k_rope_j]; k_rope's gradient is summed over the heads.
 //
 // Two kernels, so that no sum needs atomics: one walks the keys of 128 queries (dq, and delta on the
-// way), one the queries of 128 keys (dk, dv), seven products for five.  Both hold their own side's
-// operands and their accumulators in registers (up to 340 a lane, one wave per SIMD, bf16) and stage
-// the other side 64 rows at a time through 40 KiB of LDS.  The rotary part's gradient goes to a
-// float32 partial per head, which a third kernel sums.
+// way), one the queries of 128 keys (dk, dv), seven products for five.  The other side comes in tiles
+// of 32 rows through LDS.  Four waves hold their own side's operands and make p and ds, four others
+// hold the accumulators and take p and ds as operands, a tile behind: by themselves the operands (80
+// registers a lane) and the accumulators (160) leave two waves a SIMD, which fill each other's waits,
+// where one wave with both (340) spent 9,900 cycles on a 64 x 128 tile whose matrix work is 2,560.
+// What is handed over is rounded to the inputs' type as the MFMA takes it in either case.  The rotary
+// part's gradient goes to a float32 partial per head, which a third kernel sums.
 #pragma once
 #include "latent_common.h"
 
@@ -27,16 +30,22 @@ struct LatentBwdArgs {
     float *dkr;                // [B][H][S][dr] partials
 };
 
+// LDS of a 512-thread work-group: three tiles, and what the four makers hand over, twice
+template <bool F32, int FRAGS, int HAND> struct LatentBwdLds {
+    static constexpr int TILE = FRAGS * AttnOp<F32>::FB, EX = 3 * TILE, EXB = 4 * HAND * AttnOp<F32>::FB, BYTES = EX + 2 * EXB;
+};
+
 template <int DN, int DR, bool F32>
-__global__ __launch_bounds__(256, 1) void latent_dq_kernel(const LatentBwdArgs p) {
+__global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
     using Op = AttnOp<F32>;
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = (DN + DR) / 16, NQ = F32 ? 1 : 2, BM = 64 * NQ;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[(4 * NKB + 4 * NDB) * Op::FB];
-    lds_u8 *sk = lds_base(smem), *sv = sk + 4 * NKB * Op::FB;
+    using S = LatentBwdLds<F32, 2 * NKB + 2 * NDB, NQ>;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
+    lds_u8 *sx = lds_base(smem);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), w = wid & 3;
     const int unit = (blockIdx.x >> 3) / p.ntile * 8 + (blockIdx.x & 7);
     const int slot = p.ntile - 1 - (blockIdx.x >> 3) % p.ntile;
     if (unit >= p.NB * p.H) return;
@@ -50,101 +59,126 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(const LatentBwdArgs p
     const E *kp = reinterpret_cast<const E *>(p.k) + b * p.sk.b + h * p.sk.h + (long long)k0 * p.sk.t;
     const E *rp = reinterpret_cast<const E *>(p.kr) + b * p.skr.b + (long long)k0 * p.skr.t;
     const E *vp = reinterpret_cast<const E *>(p.v) + b * p.sv.b + h * p.sv.h + (long long)k0 * p.sv.t;
-    const E *qp = reinterpret_cast<const E *>(p.q) + b * p.sq.b + h * p.sq.h + (long long)q0 * p.sq.t + 8 * g;
-    const E *dp_ = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)q0 * p.sdo.t + 8 * g;
     const size_t row0 = (size_t)(b * p.H + h) * p.seqs.T + q0;
-    const E *op = reinterpret_cast<const E *>(p.out) + row0 * DN + 8 * g;
-    const int nkey = max(0, min(nk, min(tile * BM + BM - 1, nq - 1) + shift + 1)), ntk = (nkey + 63) / 64;
-    const float c = p.scale * kLog2e;
+    const int nkey = max(0, min(nk, min(tile * BM + BM - 1, nq - 1) + shift + 1)), ntk = (nkey + 31) / 32;
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    V8 qf[NQ][NKB], df[NQ][NDB];
-    float lse[NQ], delta[NQ];
+    TileStage<F32, DN / 8, 32, 512> stk, stv;
+    TileStage<F32, DR / 8, 32, 512> str;
+    auto load = [&](int kt) {  // behind the last tile it loads nothing
+        stk.load(kp, p.sk.t, 32 * kt, nk, tid);
+        str.load(rp, p.skr.t, 32 * kt, nk, tid);
+        stv.load(vp, p.sv.t, 32 * kt, nk, tid);
+    };
+    auto store = [&](int buf) {
+        lds_u8 *to = sx + buf * S::TILE;
+        stk.store(to, NKB, 0, tid);
+        str.store(to, NKB, NDB, tid);
+        stv.store(to + 2 * NKB * Op::FB, NDB, 0, tid);
+    };
+    load(0);
+    store(0);
+    load(1);
+
+    // step kt: tile kt + 1 to LDS; p and ds of tile kt; the products of tile kt - 1
+    if (wid < 4) {
+        const E *qp = reinterpret_cast<const E *>(p.q) + b * p.sq.b + h * p.sq.h + (long long)q0 * p.sq.t + 8 * g;
+        const E *dp_ = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)q0 * p.sdo.t + 8 * g;
+        const E *op = reinterpret_cast<const E *>(p.out) + row0 * DN + 8 * g;
+        const float c = p.scale * kLog2e;
+        V8 qf[NQ][NKB], df[NQ][NDB];
+        float lse[NQ], delta[NQ];
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        const int r = min(qw + 16 * x + n, nq - 1);
+        for (int x = 0; x < NQ; ++x) {
+            const int r = min(qw + 16 * x + n, nq - 1);
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) qf[x][kb] = Op::load(qp + (long long)r * p.sq.t + 32 * kb);
-        float d = 0.f;
+            for (int kb = 0; kb < NKB; ++kb) qf[x][kb] = Op::load(qp + (long long)r * p.sq.t + 32 * kb);
+            float d = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < NDB; ++kb) {
-            df[x][kb] = Op::load(dp_ + (long long)r * p.sdo.t + 32 * kb);
-            float a[8], o[8];
-            ld8(dp_ + (long long)r * p.sdo.t + 32 * kb, a);
-            ld8(op + (size_t)r * DN + 32 * kb, o);
+            for (int kb = 0; kb < NDB; ++kb) {
+                df[x][kb] = Op::load(dp_ + (long long)r * p.sdo.t + 32 * kb);
+                float a[8], o[8];
+                ld8(dp_ + (long long)r * p.sdo.t + 32 * kb, a);
+                ld8(op + (size_t)r * DN + 32 * kb, o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d = fmaf(a[j], o[j], d);
+                for (int j = 0; j < 8; ++j) d = fmaf(a[j], o[j], d);
+            }
+            delta[x] = col_sum(d);
+            const float e = p.lse[row0 + r];
+            lse[x] = e == -INFINITY ? 0.f : e * kLog2e;  // nothing seen: no key below the mask either
+            if (g == 0 && qw + 16 * x + n < nq) p.delta[row0 + r] = delta[x];
         }
-        delta[x] = col_sum(d);
-        const float e = p.lse[row0 + r];
-        lse[x] = e == -INFINITY ? 0.f : e * kLog2e;  // nothing seen: no key below the mask either
-        if (g == 0 && qw + 16 * x + n < nq) p.delta[row0 + r] = delta[x];
+        int buf = 0;
+        for (int kt = 0; kt <= ntk; ++kt) {
+            barrier_lds();
+            const int nb = buf == 2 ? 0 : buf + 1;
+            store(nb);
+            load(kt + 2);
+            if (kt < ntk) {
+                const lds_u8 *sk = sx + buf * S::TILE, *sv = sk + 2 * NKB * Op::FB;
+                const int first = 32 * kt;
+                const bool edge = first + 32 > nk || first + 31 > qw + shift;
+                f32x4 s[2][NQ], d[2][NQ];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int x = 0; x < NQ; ++x) s[t][x] = d[t][x] = zero;
+#pragma unroll
+                    for (int kb = 0; kb < NKB; ++kb) {
+                        const V8 kf = Op::get(sk + (t * NKB + kb) * Op::FB, kb, lane);
+#pragma unroll
+                        for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf, qf[x][kb], s[t][x]);
+                    }
+#pragma unroll
+                    for (int kb = 0; kb < NDB; ++kb) {
+                        const V8 vf = Op::get(sv + (t * NDB + kb) * Op::FB, kb, lane);
+#pragma unroll
+                        for (int x = 0; x < NQ; ++x) d[t][x] = Op::mma(vf, df[x][kb], d[t][x]);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (edge && perm_row(t, i) > see) s[t][x][i] = -INFINITY;
+                            const float pr = ex2(fmaf(s[t][x][i], c, -lse[x]));
+                            s[t][x][i] = pr * (d[t][x][i] - delta[x]);
+                        }
+                    Op::put_lane(sx + S::EX + (kt & 1) * S::EXB + (w * NQ + x) * Op::FB, lane, Op::pair(s[0][x], s[1][x]));
+                }
+            }
+            buf = nb;
+        }
+        return;
     }
     f32x4 dq[NT][NQ];
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int x = 0; x < NQ; ++x) dq[t][x] = zero;
-    TileStage<F32, DN / 8> stk, stv;
-    TileStage<F32, DR / 8> str;
-    if (ntk > 0) {
-        stk.load(kp, p.sk.t, 0, nk, tid);
-        str.load(rp, p.skr.t, 0, nk, tid);
-        stv.load(vp, p.sv.t, 0, nk, tid);
-    }
-    for (int kt = 0; kt < ntk; ++kt) {
+    int buf = 0;
+    for (int kt = 0; kt <= ntk; ++kt) {
         barrier_lds();
-        stk.store(sk, NKB, 0, tid);
-        str.store(sk, NKB, NDB, tid);
-        stv.store(sv, NDB, 0, tid);
-        barrier_lds();
-        stk.load(kp, p.sk.t, 64 * kt + 64, nk, tid);  // behind the last tile it loads nothing
-        str.load(rp, p.skr.t, 64 * kt + 64, nk, tid);
-        stv.load(vp, p.sv.t, 64 * kt + 64, nk, tid);
-        const int first = 64 * kt;
-        const bool edge = first + 64 > nk || first + 63 > qw + shift;
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {  // 32 keys: the k of one MFMA
-            f32x4 s[2][NQ], d[2][NQ];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) s[t][x] = d[t][x] = zero;
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const V8 kf = Op::get(sk + ((2 * hb + t) * NKB + kb) * Op::FB, kb, lane);
-#pragma unroll
-                    for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf, qf[x][kb], s[t][x]);
-                }
-#pragma unroll
-                for (int kb = 0; kb < NDB; ++kb) {
-                    const V8 vf = Op::get(sv + ((2 * hb + t) * NDB + kb) * Op::FB, kb, lane);
-#pragma unroll
-                    for (int x = 0; x < NQ; ++x) d[t][x] = Op::mma(vf, df[x][kb], d[t][x]);
-                }
-            }
+        const int nb = buf == 2 ? 0 : buf + 1, pb = buf == 0 ? 2 : buf - 1;
+        store(nb);
+        load(kt + 2);
+        if (kt > 0) {
+            const lds_u8 *sk = sx + pb * S::TILE;
             V8 sf[NQ];
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-                const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (edge && perm_row(2 * hb + t, i) > see) s[t][x][i] = -INFINITY;
-                        const float pr = ex2(fmaf(s[t][x][i], c, -lse[x]));
-                        s[t][x][i] = pr * (d[t][x][i] - delta[x]);
-                    }
-                sf[x] = Op::pair(s[0][x], s[1][x]);
-            }
+            for (int x = 0; x < NQ; ++x) sf[x] = Op::get_lane(sx + S::EX + ((kt - 1) & 1) * S::EXB + (w * NQ + x) * Op::FB, lane);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const lds_u8 *f0 = sk + (2 * hb * NKB + (t >> 1)) * Op::FB;
+                const lds_u8 *f0 = sk + (t >> 1) * Op::FB;
                 const V8 kf = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
 #pragma unroll
                 for (int x = 0; x < NQ; ++x) dq[t][x] = Op::mma(kf, sf[x], dq[t][x]);
             }
         }
+        buf = nb;
     }
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
@@ -164,16 +198,17 @@ __global__ __launch_bounds__(256, 1) void latent_dq_kernel(const LatentBwdArgs p
 }
 
 template <int DN, int DR, bool F32>
-__global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs p) {
+__global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) {
     using Op = AttnOp<F32>;
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = (DN + DR) / 16, NV = DN / 16, NK = F32 ? 1 : 2, BN = 64 * NK;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[(4 * NKB + 4 * NDB) * Op::FB];
-    __shared__ __attribute__((aligned(16))) float sl[64], sd[64];
-    lds_u8 *sq = lds_base(smem), *so = sq + 4 * NKB * Op::FB;
+    using S = LatentBwdLds<F32, 2 * NKB + 2 * NDB, 2 * NK>;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
+    __shared__ __attribute__((aligned(16))) float sl[3][32], sd[3][32];
+    lds_u8 *sx = lds_base(smem);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6), w = wid & 3;
     const int unit = (blockIdx.x >> 3) / p.ntile * 8 + (blockIdx.x & 7), slot = (blockIdx.x >> 3) % p.ntile;
     if (unit >= p.NB * p.H) return;
     const int b = unit / p.H, h = unit % p.H;
@@ -183,30 +218,112 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs 
     AttnSeqs::range(p.seqs.cu_k, seq, p.seqs.S, k0, nk);
     if (tile * BN >= nk) return;
     const int kw = tile * BN + 16 * NK * w, shift = nk - nq;
-    const E *kp = reinterpret_cast<const E *>(p.k) + b * p.sk.b + h * p.sk.h + (long long)k0 * p.sk.t + 8 * g;
-    const E *rp = reinterpret_cast<const E *>(p.kr) + b * p.skr.b + (long long)k0 * p.skr.t + 8 * g;
-    const E *vp = reinterpret_cast<const E *>(p.v) + b * p.sv.b + h * p.sv.h + (long long)k0 * p.sv.t + 8 * g;
     const E *qp = reinterpret_cast<const E *>(p.q) + b * p.sq.b + h * p.sq.h + (long long)q0 * p.sq.t;
     const E *dp_ = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)q0 * p.sdo.t;
     const size_t qrow = (size_t)(b * p.H + h) * p.seqs.T + q0;
-    const float c = p.scale * kLog2e;
     // queries that see the tile's first key stand at its index minus shift, or later
-    const int t_first = max(0, tile * BN - shift) / 64, t_end = (nq + 63) / 64;
+    const int t_first = max(0, tile * BN - shift) / 32, ntq = max(0, (nq + 31) / 32 - t_first);
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    V8 kf[NK][NKB], vf[NK][NDB];
-#pragma unroll
-    for (int x = 0; x < NK; ++x) {
-        const int r = min(kw + 16 * x + n, nk - 1);
-#pragma unroll
-        for (int kb = 0; kb < NDB; ++kb) {
-            kf[x][kb] = Op::load(kp + (long long)r * p.sk.t + 32 * kb);
-            vf[x][kb] = Op::load(vp + (long long)r * p.sv.t + 32 * kb);
+    TileStage<F32, DN / 8, 32, 512> stq, sto;
+    TileStage<F32, DR / 8, 32, 512> str;
+    float rl = 0.f, rd = 0.f;
+    auto load = [&](int i) {  // behind the last tile it loads nothing
+        const int row = 32 * (t_first + i);
+        stq.load(qp, p.sq.t, row, nq, tid);
+        str.load(qp + DN, p.sq.t, row, nq, tid);
+        sto.load(dp_, p.sdo.t, row, nq, tid);
+        if (tid < 32 && nq > 0) {
+            const int r = min(row + tid, nq - 1);
+            rl = p.lse[qrow + r];
+            rd = p.delta[qrow + r];
         }
+    };
+    auto store = [&](int buf) {
+        lds_u8 *to = sx + buf * S::TILE;
+        stq.store(to, NKB, 0, tid);
+        str.store(to, NKB, NDB, tid);
+        sto.store(to + 2 * NKB * Op::FB, NDB, 0, tid);
+        if (tid < 32) {
+            sl[buf][tid] = rl == -INFINITY ? 0.f : rl * kLog2e;
+            sd[buf][tid] = rd;
+        }
+    };
+    load(0);
+    store(0);
+    load(1);
+
+    // step i: tile i + 1 to LDS; p and ds of tile i; the products of tile i - 1
+    if (wid < 4) {
+        const E *kp = reinterpret_cast<const E *>(p.k) + b * p.sk.b + h * p.sk.h + (long long)k0 * p.sk.t + 8 * g;
+        const E *rp = reinterpret_cast<const E *>(p.kr) + b * p.skr.b + (long long)k0 * p.skr.t + 8 * g;
+        const E *vp = reinterpret_cast<const E *>(p.v) + b * p.sv.b + h * p.sv.h + (long long)k0 * p.sv.t + 8 * g;
+        const float c = p.scale * kLog2e;
+        V8 kf[NK][NKB], vf[NK][NDB];
 #pragma unroll
-        for (int kb = NDB; kb < NKB; ++kb) kf[x][kb] = Op::load(rp + (long long)r * p.skr.t + 32 * (kb - NDB));
+        for (int x = 0; x < NK; ++x) {
+            const int r = min(kw + 16 * x + n, nk - 1);
+#pragma unroll
+            for (int kb = 0; kb < NDB; ++kb) {
+                kf[x][kb] = Op::load(kp + (long long)r * p.sk.t + 32 * kb);
+                vf[x][kb] = Op::load(vp + (long long)r * p.sv.t + 32 * kb);
+            }
+#pragma unroll
+            for (int kb = NDB; kb < NKB; ++kb) kf[x][kb] = Op::load(rp + (long long)r * p.skr.t + 32 * (kb - NDB));
+        }
+        int buf = 0;
+        for (int it = 0; it <= ntq; ++it) {
+            barrier_lds();
+            const int nb = buf == 2 ? 0 : buf + 1;
+            store(nb);
+            load(it + 2);
+            if (it < ntq) {
+                const lds_u8 *sq = sx + buf * S::TILE, *so = sq + 2 * NKB * Op::FB;
+                const int first = 32 * (t_first + it);
+                const bool edge = first + 32 > nq || first + shift < kw + 16 * NK - 1;
+                f32x4 s[2][NK], d[2][NK], l4[2], d4[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    l4[t] = *reinterpret_cast<const f32x4 *>(sl[buf] + perm_row(t, 4 * g));
+                    d4[t] = *reinterpret_cast<const f32x4 *>(sd[buf] + perm_row(t, 4 * g));
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) s[t][x] = d[t][x] = zero;
+#pragma unroll
+                    for (int kb = 0; kb < NKB; ++kb) {
+                        const V8 qf = Op::get(sq + (t * NKB + kb) * Op::FB, kb, lane);
+#pragma unroll
+                        for (int x = 0; x < NK; ++x) s[t][x] = Op::mma(qf, kf[x][kb], s[t][x]);
+                    }
+#pragma unroll
+                    for (int kb = 0; kb < NDB; ++kb) {
+                        const V8 of = Op::get(so + (t * NDB + kb) * Op::FB, kb, lane);
+#pragma unroll
+                        for (int x = 0; x < NK; ++x) d[t][x] = Op::mma(of, vf[x][kb], d[t][x]);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < NK; ++x) {
+                    const int seen = kw + 16 * x + n - shift - first - 8 * g, none = nq - first - 8 * g;  // rows seen .. none - 1
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = perm_row(t, i);
+                            if (edge && (row >= none || row < seen)) s[t][x][i] = -INFINITY;
+                            const float pr = ex2(fmaf(s[t][x][i], c, -l4[t][i]));
+                            s[t][x][i] = pr;
+                            d[t][x][i] = pr * (d[t][x][i] - d4[t][i]);
+                        }
+                    lds_u8 *to = sx + S::EX + (it & 1) * S::EXB + (w * NK + x) * 2 * Op::FB;
+                    Op::put_lane(to, lane, Op::pair(s[0][x], s[1][x]));
+                    Op::put_lane(to + Op::FB, lane, Op::pair(d[0][x], d[1][x]));
+                }
+            }
+            buf = nb;
+        }
+        return;
     }
     f32x4 dk[NT][NK], dv[NV][NK];
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < NK; ++x) {
 #pragma unroll
@@ -214,92 +331,37 @@ __global__ __launch_bounds__(256, 1) void latent_dkv_kernel(const LatentBwdArgs 
 #pragma unroll
         for (int t = 0; t < NV; ++t) dv[t][x] = zero;
     }
-    TileStage<F32, DN / 8> stq, sto;
-    TileStage<F32, DR / 8> str;
-    float rl = 0.f, rd = 0.f;
-    auto load = [&](int qt) {
-        stq.load(qp, p.sq.t, 64 * qt, nq, tid);
-        str.load(qp + DN, p.sq.t, 64 * qt, nq, tid);
-        sto.load(dp_, p.sdo.t, 64 * qt, nq, tid);
-        if (tid < 64) {
-            const int r = min(64 * qt + tid, nq - 1);
-            const float e = p.lse[qrow + r];
-            rl = e == -INFINITY ? 0.f : e * kLog2e;
-            rd = p.delta[qrow + r];
-        }
-    };
-    if (t_first < t_end) load(t_first);
-    for (int qt = t_first; qt < t_end; ++qt) {
+    int buf = 0;
+    for (int it = 0; it <= ntq; ++it) {
         barrier_lds();
-        stq.store(sq, NKB, 0, tid);
-        str.store(sq, NKB, NDB, tid);
-        sto.store(so, NDB, 0, tid);
-        if (tid < 64) {
-            sl[tid] = rl;
-            sd[tid] = rd;
-        }
-        barrier_lds();
-        load(qt + 1);  // behind the last tile it loads nothing
-        const int first = 64 * qt;
-        const bool edge = first + 64 > nq || first + shift < kw + 16 * NK - 1;
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-            f32x4 s[2][NK], d[2][NK];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int x = 0; x < NK; ++x) s[t][x] = d[t][x] = zero;
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const V8 qf = Op::get(sq + ((2 * hb + t) * NKB + kb) * Op::FB, kb, lane);
-#pragma unroll
-                    for (int x = 0; x < NK; ++x) s[t][x] = Op::mma(qf, kf[x][kb], s[t][x]);
-                }
-#pragma unroll
-                for (int kb = 0; kb < NDB; ++kb) {
-                    const V8 of = Op::get(so + ((2 * hb + t) * NDB + kb) * Op::FB, kb, lane);
-#pragma unroll
-                    for (int x = 0; x < NK; ++x) d[t][x] = Op::mma(of, vf[x][kb], d[t][x]);
-                }
-            }
+        const int nb = buf == 2 ? 0 : buf + 1, pb = buf == 0 ? 2 : buf - 1;
+        store(nb);
+        load(it + 2);
+        if (it > 0) {
+            const lds_u8 *sq = sx + pb * S::TILE, *so = sq + 2 * NKB * Op::FB;
             V8 pf[NK], sf[NK];
-            f32x4 l4[2], d4[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                l4[t] = *reinterpret_cast<const f32x4 *>(sl + perm_row(2 * hb + t, 4 * g));
-                d4[t] = *reinterpret_cast<const f32x4 *>(sd + perm_row(2 * hb + t, 4 * g));
-            }
 #pragma unroll
             for (int x = 0; x < NK; ++x) {
-                const int seen = kw + 16 * x + n - shift - first - 8 * g, none = nq - first - 8 * g;  // rows seen .. none - 1
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = perm_row(2 * hb + t, i);
-                        if (edge && (row >= none || row < seen)) s[t][x][i] = -INFINITY;
-                        const float pr = ex2(fmaf(s[t][x][i], c, -l4[t][i]));
-                        s[t][x][i] = pr;
-                        d[t][x][i] = pr * (d[t][x][i] - d4[t][i]);
-                    }
-                pf[x] = Op::pair(s[0][x], s[1][x]);
-                sf[x] = Op::pair(d[0][x], d[1][x]);
+                const lds_u8 *from = sx + S::EX + ((it - 1) & 1) * S::EXB + (w * NK + x) * 2 * Op::FB;
+                pf[x] = Op::get_lane(from, lane);
+                sf[x] = Op::get_lane(from + Op::FB, lane);
             }
 #pragma unroll
             for (int t = 0; t < NV; ++t) {
-                const lds_u8 *f0 = so + (2 * hb * NDB + (t >> 1)) * Op::FB;
+                const lds_u8 *f0 = so + (t >> 1) * Op::FB;
                 const V8 of = Op::get_t(f0, f0 + NDB * Op::FB, t, lane);
 #pragma unroll
                 for (int x = 0; x < NK; ++x) dv[t][x] = Op::mma(of, pf[x], dv[t][x]);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const lds_u8 *f0 = sq + (2 * hb * NKB + (t >> 1)) * Op::FB;
+                const lds_u8 *f0 = sq + (t >> 1) * Op::FB;
                 const V8 qf = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
 #pragma unroll
                 for (int x = 0; x < NK; ++x) dk[t][x] = Op::mma(qf, sf[x], dk[t][x]);
             }
         }
+        buf = nb;
     }
 #pragma unroll
     for (int x = 0; x < NK; ++x) {

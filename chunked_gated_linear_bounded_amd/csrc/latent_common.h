@@ -46,6 +46,7 @@ template <> struct AttnOp<false> {
         return r;
     }
     typedef __attribute__((address_space(3))) bf16x4 lds_b4;
+    typedef __attribute__((address_space(3))) bf16x8 lds_b8;
     __device__ __forceinline__ static int slot(int kb, int g, int m) { return 8 * (16 * g + (m ^ (8 * (g >> 1)) ^ (2 * (kb & 3)))); }
     // f: the fragment; kb: its column block
     __device__ __forceinline__ static void put(lds_u8 *f, int kb, int g, int m, const V8 &x) {
@@ -58,6 +59,9 @@ template <> struct AttnOp<false> {
         const bf16x4 a = *reinterpret_cast<const lds_b4 *>(p), b = *reinterpret_cast<const lds_b4 *>(p + 512);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
+    // an operand handed to the same lane of another wave
+    __device__ __forceinline__ static void put_lane(lds_u8 *f, int lane, const V8 &x) { *reinterpret_cast<lds_b8 *>(f + 16 * lane) = x; }
+    __device__ __forceinline__ static V8 get_lane(const lds_u8 *f, int lane) { return *reinterpret_cast<const lds_b8 *>(f + 16 * lane); }
     // transposed: rows = columns perm_row(tile, .), k = rows of the fragments f0 (row tile 2 kb), f1 (2 kb
     // + 1) of column block tile / 2
     __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int tile, int lane) {
@@ -95,6 +99,13 @@ template <> struct AttnOp<true> {
     __device__ __forceinline__ static V8 get(const lds_u8 *f, int, int lane) {
         const lds_f4 *p = reinterpret_cast<const lds_f4 *>(f + 2 * frag_slot(lane >> 4, lane & 15));
         return V8{p[0], p[1]};
+    }
+    __device__ __forceinline__ static void put_lane(lds_u8 *f, int lane, const V8 &x) {
+        *reinterpret_cast<lds_f4 *>(f + 16 * lane) = x.a;
+        *reinterpret_cast<lds_f4 *>(f + 1024 + 16 * lane) = x.b;
+    }
+    __device__ __forceinline__ static V8 get_lane(const lds_u8 *f, int lane) {
+        return V8{*reinterpret_cast<const lds_f4 *>(f + 16 * lane), *reinterpret_cast<const lds_f4 *>(f + 1024 + 16 * lane)};
     }
     __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int tile, int lane) {
         const int g = lane >> 4, m = lane & 15, e = 4 * (4 * (tile & 1) + (m & 3));
@@ -174,22 +185,23 @@ struct AttnSeqs {
 };
 
 // One operand tile of ROWS rows and 8 NC columns into LDS: 16-byte pieces through registers, in
-// fragment order; 256 threads, piece p = i 256 + tid: row p / NC.  Loads go through a buffer
+// fragment order; NTH threads, piece p = i NTH + tid: row p / NC.  Loads go through a buffer
 // resource that starts at the tile's first row and ends behind the sequence's last: one 32-bit
 // offset a thread in place of an address a piece, and rows past the last arrive as zeros.
-template <bool F32, int NC, int ROWS = 64> struct TileStage {
+template <bool F32, int NC, int ROWS = 64, int NTH = 256> struct TileStage {
     using Op = AttnOp<F32>;
     using E = typename Op::E;
-    static constexpr int N = (ROWS * NC + 255) / 256;
-    static constexpr bool ALL = ROWS * NC >= 256;  // every thread has a piece
-    static_assert(ROWS * NC % 256 == 0 || !ALL, "whole pieces per thread");
+    static constexpr int N = (ROWS * NC + NTH - 1) / NTH, STEP = NTH / NC;  // STEP: rows from piece to piece
+    static constexpr bool ALL = ROWS * NC >= NTH;  // every thread has a piece
+    static_assert(ROWS * NC % NTH == 0 || !ALL, "whole pieces per thread");
+    static_assert(STEP % 16 == 0, "whole row tiles from piece to piece");
     typename Op::V8 x[N];
     // rows row0 .. of the nrow rows at base; `stride` in elements, a tile of it below 2^31 bytes
     __device__ __forceinline__ void load(const E *base, long long stride, int row0, int nrow, int tid) {
         const int st = (int)stride * (int)sizeof(E), left = min(max(nrow - row0, 0), ROWS);
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<E *>(base + (long long)row0 * stride), 0, left > 0 ? (left - 1) * st + 8 * NC * (int)sizeof(E) : 0, 0x00027000);
-        const int step = (256 / NC) * st;
+        const int step = STEP * st;
         int off = (tid / NC) * st + (tid % NC) * 8 * (int)sizeof(E);
         asm volatile("" : "+v"(off));  // or all N offsets would be kept in registers across the tiles
 #pragma unroll
@@ -208,8 +220,8 @@ template <bool F32, int NC, int ROWS = 64> struct TileStage {
         }
     }
     // fragments [row tile][nb blocks], this tile's columns from block b0 on.  Rows of later pieces are
-    // 16 (NC = 16) or 32 behind, which moves the fragment by a constant and flips at most one address
-    // bit: a few addresses and immediate offsets.
+    // 16 or a multiple of 32 behind, which moves the fragment by a constant and flips at most one
+    // address bit: a few addresses and immediate offsets.
     __device__ __forceinline__ void store(lds_u8 *f, int nb, int b0, int tid) const {
         static_assert(NC == 4 || NC == 8 || NC == 16, "32, 64 or 128 columns");
         const int r = tid / NC, c = tid % NC, kb = b0 + (c >> 2);
@@ -217,7 +229,7 @@ template <bool F32, int NC, int ROWS = 64> struct TileStage {
         if (!ALL && tid >= ROWS * NC) return;
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            Op::put(to + (NC == 16 ? i >> 1 : i) * 2 * nb * Op::FB, kb, c & 3, perm_m(r) ^ (NC == 16 ? 8 * (i & 1) : 0), x[i]);
+            Op::put(to + i * STEP / 32 * 2 * nb * Op::FB, kb, c & 3, perm_m(r) ^ (STEP % 32 ? 8 * (i & 1) : 0), x[i]);
     }
 };
 
