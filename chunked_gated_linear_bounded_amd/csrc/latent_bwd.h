@@ -1,5 +1,5 @@
 // Expanded latent attention, backward.  With p_ij recomputed from the kept log-sum-exp and
-// delta_i = dout_i . out_i:
+// delta_i = sum_j p_ij (dout_i . v_j) = dout_i . out_i:
 //   dp_ij = dout_i . v_j,  ds_ij = p_ij (dp_ij - delta_i),
 //   dq_i = scale sum_j ds_ij key_j,  dkey_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
 // key_j = [k_j, k_rope_j]; k_rope's gradient is summed over the heads.
@@ -10,12 +10,25 @@
 // hold the accumulators and take p and ds as operands, a tile behind: by themselves the operands (80
 // registers a lane) and the accumulators (160) leave two waves a SIMD, which fill each other's waits,
 // where one wave with both (340) spent 9,900 cycles on a 64 x 128 tile whose matrix work is 2,560.
+//
+// delta from the kept output carries the output's rounding, 2^-9 of |dout| |out|, and ds is what is left
+// of p (dp - delta): little where a query sees few keys or one of them has most of p.  (One key: ds = 0.
+// 8 keys, bf16: dq off by 2.7e-3 from this alone, where rounding ds costs 1.4e-3.)  So a tile of queries
+// that see at most kExactKeys keys walks them once more, first, for the sum itself; and every tile adds
+// up its ds, whose sum would be 0, so that the delta left for dk and dv is the sum in float32 in any
+// case.  At 256 keys the rounding has fallen to a tenth of ds's own and a second walk would be 60 % of
+// the kernel's work.
+//
 // What is handed over is rounded to the inputs' type as the MFMA takes it in either case.  The rotary
-// part's gradient goes to a float32 partial per head, which a third kernel sums.
+// part's gradient goes to a float32 partial per head, which a third kernel sums.  16 heads x 4096
+// queries and keys, 128 + 64 channels: dq 180 us, dk and dv 215 us, matrix units busy 41 and 39 % of
+// the time, the LDS 50 and 47 %; one kind of wave, 64-row tiles: 270 and 325 us.
 #pragma once
 #include "latent_common.h"
 
 namespace kda {
+
+constexpr int kExactKeys = 256;
 
 struct LatentBwdArgs {
     const void *q, *k, *kr, *v, *out, *dout;
@@ -34,6 +47,40 @@ struct LatentBwdArgs {
 template <bool F32, int FRAGS, int HAND> struct LatentBwdLds {
     static constexpr int TILE = FRAGS * AttnOp<F32>::FB, EX = 3 * TILE, EXB = 4 * HAND * AttnOp<F32>::FB, BYTES = EX + 2 * EXB;
 };
+
+// s = X a, d = Y c: rows 0 .. 31 of a tile (X: NA column blocks from f on, Y: NC from e on) against NX
+// operand columns a lane.  A group's fragments are read while the group before is multiplied; left to
+// itself the compiler waits for each one it reads.
+template <typename Op, int NA, int NC, int NX>
+__device__ __forceinline__ void tile_products(const lds_u8 *f, const lds_u8 *e, int lane, const typename Op::V8 (&a)[NX][NA],
+                                              const typename Op::V8 (&c)[NX][NC], f32x4 (&s)[2][NX], f32x4 (&d)[2][NX]) {
+    typename Op::V8 fa[2][NA], fc[2][NC];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int x = 0; x < NX; ++x) s[t][x] = d[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < NA; ++kb) fa[0][kb] = Op::get(f + kb * Op::FB, kb, lane);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int kb = 0; kb < NC; ++kb) fc[t][kb] = Op::get(e + (t * NC + kb) * Op::FB, kb, lane);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kb = 0; kb < NA; ++kb)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) s[t][x] = Op::mma(fa[t][kb], a[x][kb], s[t][x]);
+        if (t == 0) {
+#pragma unroll
+            for (int kb = 0; kb < NA; ++kb) fa[1][kb] = Op::get(f + (NA + kb) * Op::FB, kb, lane);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kb = 0; kb < NC; ++kb)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) d[t][x] = Op::mma(fc[t][kb], c[x][kb], d[t][x]);
+    }
+}
 
 template <int DN, int DR, bool F32>
 __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
@@ -76,9 +123,7 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
         str.store(to, NKB, NDB, tid);
         stv.store(to + 2 * NKB * Op::FB, NDB, 0, tid);
     };
-    load(0);
-    store(0);
-    load(1);
+    const int pass0 = nkey <= kExactKeys ? 0 : 1;  // pass 0: delta alone
 
     // step kt: tile kt + 1 to LDS; p and ds of tile kt; the products of tile kt - 1
     if (wid < 4) {
@@ -87,7 +132,7 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
         const E *op = reinterpret_cast<const E *>(p.out) + row0 * DN + 8 * g;
         const float c = p.scale * kLog2e;
         V8 qf[NQ][NKB], df[NQ][NDB];
-        float lse[NQ], delta[NQ];
+        float lse[NQ], delta[NQ], rest[NQ];  // rest: sum of ds over the keys
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             const int r = min(qw + 16 * x + n, nq - 1);
@@ -103,55 +148,59 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d = fmaf(a[j], o[j], d);
             }
-            delta[x] = col_sum(d);
+            delta[x] = pass0 == 0 ? 0.f : col_sum(d);
             const float e = p.lse[row0 + r];
             lse[x] = e == -INFINITY ? 0.f : e * kLog2e;  // nothing seen: no key below the mask either
-            if (g == 0 && qw + 16 * x + n < nq) p.delta[row0 + r] = delta[x];
         }
-        int buf = 0;
-        for (int kt = 0; kt <= ntk; ++kt) {
-            barrier_lds();
-            const int nb = buf == 2 ? 0 : buf + 1;
-            store(nb);
-            load(kt + 2);
-            if (kt < ntk) {
-                const lds_u8 *sk = sx + buf * S::TILE, *sv = sk + 2 * NKB * Op::FB;
-                const int first = 32 * kt;
-                const bool edge = first + 32 > nk || first + 31 > qw + shift;
-                f32x4 s[2][NQ], d[2][NQ];
+        for (int pass = pass0; pass < 2; ++pass) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+            for (int x = 0; x < NQ; ++x) rest[x] = 0.f;
+            barrier_lds();  // the pass before has read its tiles
+            load(0);
+            store(0);
+            load(1);
+            int buf = 0;
+            for (int kt = 0; kt <= ntk; ++kt) {
+                barrier_lds();
+                const int nb = buf == 2 ? 0 : buf + 1;
+                store(nb);
+                load(kt + 2);
+                if (kt < ntk) {
+                    const lds_u8 *sk = sx + buf * S::TILE, *sv = sk + 2 * NKB * Op::FB;
+                    const int first = 32 * kt;
+                    const bool edge = first + 32 > nk || first + 31 > qw + shift;
+                    f32x4 s[2][NQ], d[2][NQ];
+                    tile_products<Op>(sk, sv, lane, qf, df, s, d);
+                    if (edge)  // one branch a tile, not one an element
 #pragma unroll
-                    for (int x = 0; x < NQ; ++x) s[t][x] = d[t][x] = zero;
+                        for (int x = 0; x < NQ; ++x) {
+                            const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;
 #pragma unroll
-                    for (int kb = 0; kb < NKB; ++kb) {
-                        const V8 kf = Op::get(sk + (t * NKB + kb) * Op::FB, kb, lane);
+                            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int x = 0; x < NQ; ++x) s[t][x] = Op::mma(kf, qf[x][kb], s[t][x]);
-                    }
-#pragma unroll
-                    for (int kb = 0; kb < NDB; ++kb) {
-                        const V8 vf = Op::get(sv + (t * NDB + kb) * Op::FB, kb, lane);
-#pragma unroll
-                        for (int x = 0; x < NQ; ++x) d[t][x] = Op::mma(vf, df[x][kb], d[t][x]);
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) {
-                    const int see = min(nk - 1, qw + 16 * x + n + shift) - first - 8 * g;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (edge && perm_row(t, i) > see) s[t][x][i] = -INFINITY;
-                            const float pr = ex2(fmaf(s[t][x][i], c, -lse[x]));
-                            s[t][x][i] = pr * (d[t][x][i] - delta[x]);
+                                for (int i = 0; i < 4; ++i) s[t][x][i] = perm_row(t, i) > see ? -INFINITY : s[t][x][i];
                         }
-                    Op::put_lane(sx + S::EX + (kt & 1) * S::EXB + (w * NQ + x) * Op::FB, lane, Op::pair(s[0][x], s[1][x]));
+#pragma unroll
+                    for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float pr = ex2(fmaf(s[t][x][i], c, -lse[x]));
+                                s[t][x][i] = pr * (d[t][x][i] - delta[x]);
+                                rest[x] += s[t][x][i];
+                            }
+                        Op::put_lane(sx + S::EX + (kt & 1) * S::EXB + (w * NQ + x) * Op::FB, lane, Op::pair(s[0][x], s[1][x]));
+                    }
                 }
+                buf = nb;
             }
-            buf = nb;
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) delta[x] += col_sum(rest[x]);
         }
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+            if (g == 0 && qw + 16 * x + n < nq) p.delta[row0 + qw + 16 * x + n] = delta[x];
         return;
     }
     f32x4 dq[NT][NQ];
@@ -159,26 +208,44 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int x = 0; x < NQ; ++x) dq[t][x] = zero;
-    int buf = 0;
-    for (int kt = 0; kt <= ntk; ++kt) {
+    for (int pass = pass0; pass < 2; ++pass) {
         barrier_lds();
-        const int nb = buf == 2 ? 0 : buf + 1, pb = buf == 0 ? 2 : buf - 1;
-        store(nb);
-        load(kt + 2);
-        if (kt > 0) {
-            const lds_u8 *sk = sx + pb * S::TILE;
-            V8 sf[NQ];
+        load(0);
+        store(0);
+        load(1);
+        int buf = 0;
+        for (int kt = 0; kt <= ntk; ++kt) {
+            barrier_lds();
+            const int nb = buf == 2 ? 0 : buf + 1, pb = buf == 0 ? 2 : buf - 1;
+            store(nb);
+            load(kt + 2);
+            if (kt > 0 && pass > 0) {
+                const lds_u8 *sk = sx + pb * S::TILE;
+                V8 sf[NQ];
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) sf[x] = Op::get_lane(sx + S::EX + ((kt - 1) & 1) * S::EXB + (w * NQ + x) * Op::FB, lane);
+                for (int x = 0; x < NQ; ++x) sf[x] = Op::get_lane(sx + S::EX + ((kt - 1) & 1) * S::EXB + (w * NQ + x) * Op::FB, lane);
+                // four column tiles' fragments are read while the four before are multiplied
+                V8 f4[2][4];
+                auto read = [&](int j) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const lds_u8 *f0 = sk + (t >> 1) * Op::FB;
-                const V8 kf = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
+                    for (int t = 4 * j; t < min(4 * j + 4, NT); ++t) {
+                        const lds_u8 *f0 = sk + (t >> 1) * Op::FB;
+                        f4[j & 1][t & 3] = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
+                    }
+                };
+                read(0);
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) dq[t][x] = Op::mma(kf, sf[x], dq[t][x]);
+                for (int j = 0; j < (NT + 3) / 4; ++j) {
+                    read(j + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int t = 4 * j; t < min(4 * j + 4, NT); ++t)
+#pragma unroll
+                        for (int x = 0; x < NQ; ++x) dq[t][x] = Op::mma(f4[j & 1][t & 3], sf[x], dq[t][x]);
+                }
             }
+            buf = nb;
         }
-        buf = nb;
     }
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
@@ -301,15 +368,22 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
                         for (int x = 0; x < NK; ++x) d[t][x] = Op::mma(of, vf[x][kb], d[t][x]);
                     }
                 }
+                if (edge)  // one branch a tile, not one an element
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) {
+                        const int seen = kw + 16 * x + n - shift - first - 8 * g, none = nq - first - 8 * g;  // rows seen .. none - 1
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s[t][x][i] = (perm_row(t, i) >= none) | (perm_row(t, i) < seen) ? -INFINITY : s[t][x][i];
+                    }
 #pragma unroll
                 for (int x = 0; x < NK; ++x) {
-                    const int seen = kw + 16 * x + n - shift - first - 8 * g, none = nq - first - 8 * g;  // rows seen .. none - 1
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int row = perm_row(t, i);
-                            if (edge && (row >= none || row < seen)) s[t][x][i] = -INFINITY;
                             const float pr = ex2(fmaf(s[t][x][i], c, -l4[t][i]));
                             s[t][x][i] = pr;
                             d[t][x][i] = pr * (d[t][x][i] - d4[t][i]);
