@@ -51,6 +51,17 @@ def test_waves_per_work_group(dtype):
         _check_fwd(x, out, fs, 1.0, None, "%d " % (B * H))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,T", [(128, 200), (64, 129), (128, 5)])
+def test_two_column_tiles(dk, T, dtype):
+    """More than 256 slices of 16 value columns: 32 a work-group, with a start state."""
+    B, H, dv = 3, 12, 128
+    x = inputs(B, 4, H, T, dk, dv, dtype, dk + T)
+    S0 = _state(B, H, dv, dk, T)
+    out, fs = kda.gdr_chunk_fwd(*(t.cuda() for t in x), scale=dk ** -0.5, return_final_state=True, initial_state=S0.cuda())
+    _check_fwd(x, out, fs, dk ** -0.5, S0)
+
+
 def test_strided_views():
     """Projections as a model leaves them: [B,T,H,d] seen as [B,H,T,d], g and beta interleaved."""
     x = inputs(2, 2, 4, 77, 128, 64, BF, 3)

@@ -56,7 +56,7 @@ def compare(got, ref, dtype, what):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("B,Hk,H,T,dk,dv", [
     (1, 1, 1, 1, 64, 64), (1, 1, 2, 3, 128, 64), (2, 2, 2, 63, 64, 128), (1, 2, 4, 64, 128, 128), (1, 1, 3, 65, 128, 128),
-    (1, 2, 2, 127, 64, 64), (2, 1, 4, 150, 128, 128), (3, 4, 16, 70, 128, 128),
+    (1, 2, 2, 127, 64, 64), (2, 1, 4, 150, 128, 128), (3, 4, 16, 70, 128, 128), (3, 4, 12, 195, 64, 128),
 ])
 def test_gradients(B, Hk, H, T, dk, dv, dtype):
     x = inputs(B, Hk, H, T, dk, dv, dtype, 7 + T)
@@ -69,6 +69,19 @@ def test_gradients(B, Hk, H, T, dk, dv, dtype):
                             dfinal_state=None if dfin is None else dfin.cuda())
     for name, ref in zip(NAMES, reference(x, dout, dk ** -0.5, S0, dfin)):
         compare(got[name], ref, dtype, name)
+
+
+@pytest.mark.parametrize("what", ["keys", "queries", "values", "dout"])
+def test_zeros(what):
+    """An operand that is zero throughout the middle chunk: the bounds that the others' exponents come
+    from hold there too, and the initial state's gradient keeps its 22 bits."""
+    x = list(inputs(1, 1, 2, 192, 128, 64, F32, 31, rate=-5.0))
+    gen = torch.Generator().manual_seed(2)
+    dout, S0, dfin = (torch.randn(1, 2, *s, generator=gen) for s in ((192, 64), (64, 128), (64, 128)))
+    {"keys": x[1], "queries": x[0], "values": x[2], "dout": dout}[what][:, :, 64:128] = 0.0
+    got = kda.gdr_chunk_bwd(*(t.cuda() for t in x), dout.cuda(), scale=128 ** -0.5, initial_state=S0.cuda(), dfinal_state=dfin.cuda())
+    for name, ref in zip(NAMES, reference(x, dout, 128 ** -0.5, S0, dfin)):
+        compare(got[name], ref, F32, name)
 
 
 def test_differences():

@@ -133,6 +133,51 @@ def test_packed(dtype, lens):
                    {"dq": g["dq"][:, i0:i1], "dk": g["dk"][:, j0:j1], "dv": g["dv"][:, j0:j1], "dk_rope": g["dk_rope"][j0:j1]}, "seq %d " % i)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_short_sequences(dtype):
+    """More work-groups than two a CU: the forward's form without wave groups, beside long sequences."""
+    dn, dr, H = 64, 32, 2
+    lens = [(1 + i % 3, 1 + i % 3 + i % 2) for i in range(300)] + [(140, 300), (1, 257), (0, 5)]
+    a = [sum(t for t, _ in lens[:i]) for i in range(len(lens) + 1)]
+    c = [sum(s for _, s in lens[:i]) for i in range(len(lens) + 1)]
+    q, kv, r, do = inputs((), H, a[-1], c[-1], dn, dr, dtype, 17)
+    k, v = split(kv, dn)
+    x = (q.cuda(), *split(kv.cuda(), dn), r.cuda())
+    cu = [torch.tensor(t, dtype=torch.int32).cuda() for t in (a, c)]
+    out, lse = kda.latent_attn_fwd_varlen(*x, *cu, return_lse=True)
+    g = kda.latent_attn_bwd_varlen(*x, out, lse, do.cuda(), *cu)
+    torch.cuda.synchronize()
+    g = {n: t.cpu() for n, t in g.items()}
+    out, lse = out.cpu(), lse.cpu()
+    for i in list(range(0, 300, 23)) + [300, 301]:
+        i0, i1, j0, j1 = a[i], a[i + 1], c[i], c[i + 1]
+        _check_all(q[:, i0:i1], k[:, j0:j1], v[:, j0:j1], r[j0:j1], do[:, i0:i1], (dn + dr) ** -0.5, dtype, out[:, i0:i1], lse[:, i0:i1],
+                   {"dq": g["dq"][:, i0:i1], "dk": g["dk"][:, j0:j1], "dv": g["dv"][:, j0:j1], "dk_rope": g["dk_rope"][j0:j1]}, "seq %d " % i)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_visible_key_has_no_gradient(dtype):
+    """With one key p is 1 and ds = 0 whatever dout is.  p comes from two float32 score sums that differ
+    by 2^-24 of the largest score's 2 * 192 terms at most, and ds = p dp - p p dp, so |ds| is at most that
+    share of |dp|, with the exponential's 2^-21, twice (p and the sum), and dp's float32 sums."""
+    dn, dr, H, N = 128, 64, 2, 40
+    q, kv, r, do = inputs((), H, N, N, dn, dr, dtype, 23)
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    x = (q.cuda(), *split(kv.cuda(), dn), r.cuda())
+    out, lse = kda.latent_attn_fwd_varlen(*x, cu, cu, return_lse=True)
+    g = kda.latent_attn_bwd_varlen(*x, out, lse, do.cuda(), cu, cu)
+    k, v = split(kv, dn)
+    scale = 192 ** -0.5
+    for h in range(H):
+        key = torch.cat([k[h], r], -1).double().abs()
+        qa = q[h].double().abs()
+        size = scale * (qa * key).sum(-1, keepdim=True)
+        dp = (do[h].double().abs() * v[h].double().abs()).sum(-1, keepdim=True)
+        ds = dp * 4 * (2 * 192 * 2.0 ** -24 * size + 2.0 ** -21 + 128 * 2.0 ** -24)
+        assert (g["dq"][h].double().cpu().abs() <= 1.01 * scale * ds * key).all()
+        assert (g["dk"][h].double().cpu().abs() <= 1.01 * scale * ds * qa[:, :dn]).all()
+
+
 def test_bad_boundaries_stay_inside():
     q, kv, r, _ = inputs((), 1, 150, 150, 64, 32, BF, 3)
     k, v = split(kv.cuda(), 64)
