@@ -37,6 +37,11 @@ bool set_strides(long long (&s)[3], const kda_strides *given, long long H, long 
     return s[0] % unit == 0 && s[1] % unit == 0 && s[2] % unit == 0;
 }
 
+// the kernels step through 64 rows with 32-bit offsets, forwards
+bool far_rows(const long long (&s)[3], long long rows, bool fp32) {
+    return rows > 1 && (s[2] < 0 || s[2] > 2147483647LL / 64 / (fp32 ? 4 : 2));
+}
+
 kda::LatentLaunch shape(bool packed, int N, int H, int T, int S, int dn, int dr, int io) {
     kda::LatentLaunch p{};
     p.N = N; p.B = packed ? 1 : N; p.H = H; p.T = T; p.S = S; p.dn = dn; p.dr = dr;
@@ -55,6 +60,8 @@ int inputs(kda::LatentLaunch &p, const void *q, const kda_strides *qs, const voi
     if (!set_strides(p.sq, qs, p.H, p.T, p.dn + p.dr, unit) || !set_strides(p.sk, ks, p.H, p.S, p.dn, unit) ||
         !set_strides(p.sv, vs, p.H, p.S, p.dn, unit) || !set_strides(p.skr, krs, 0, p.S, p.dr, unit))
         return KDA_ERR_ALIGN;
+    if (far_rows(p.sq, p.T, p.fp32) || far_rows(p.sk, p.S, p.fp32) || far_rows(p.sv, p.S, p.fp32) || far_rows(p.skr, p.S, p.fp32))
+        return KDA_ERR_SHAPE;
     p.q = q; p.k = k; p.v = v; p.kr = kr;
     p.cu_q = cu_q; p.cu_k = cu_k;
     p.scale = scale;
@@ -119,6 +126,7 @@ int kda_latent_attn_bwd(const void *q, const kda_strides *q_strides, const void 
         return KDA_ERR_ALIGN;
     st = inputs(p, q, q_strides, k, k_strides, v, v_strides, k_rope, k_rope_strides, cu_seqlens_q, cu_seqlens_k, scale);
     if (st != KDA_OK) return st;
+    if (far_rows(p.sdo, T, p.fp32)) return KDA_ERR_SHAPE;
     const size_t need = kda::latent_bwd_bytes(p);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return KDA_ERR_ALIGN;

@@ -357,7 +357,8 @@ int kda_gdr_decode_step(const void *q, const void *k, const void *v, const void 
  * query i sees keys 0 .. i + S - T.  A query that sees no key gets zeros and a log-sum-exp of -inf.
  *  - q : [B][H][T][dn + dr]   k, v : [B][H][S][dn]   k_rope : [B][S][dr]   in io_dtype, each with
  *    element strides (NULL: contiguous; k_rope's h is unused); the last dimension is contiguous and
- *    every row starts at a multiple of 16 bytes.
+ *    every row starts at a multiple of 16 bytes; t is not negative, and 64 t elements take less than
+ *    2^31 bytes (KDA_ERR_SHAPE otherwise).
  *  - cu_seqlens_q and cu_seqlens_k both NULL: a batch of N sequences.  Otherwise packed streams of T
  *    queries and S keys ([H][T][..], [H][S][..], [S][dr], strides b unused) with N + 1 int32
  *    boundaries each, on the device; they are clipped to the streams there, and rows that no

@@ -18,7 +18,9 @@ S3 = ctypes.c_longlong * 3
     (dict(N=70000), E_SHAPE), (dict(N=1 << 30, cq=FAKE, ck=FAKE), E_SHAPE), (dict(scale=0.0), E_SCALE),
     (dict(scale=-1.0), E_SCALE), (dict(scale=float("nan")), E_SCALE), (dict(scale=float("inf")), E_SCALE),
     (dict(q=FAKE + 8), E_ALIGN), (dict(lse=FAKE + 2), E_ALIGN), (dict(ks=S3(0, 0, 132)), E_ALIGN),
-    (dict(krs=S3(0, 0, 68)), E_ALIGN), (dict(io=1, vs=S3(0, 2, 128)), E_ALIGN), (dict(T=0, q=None, out=None, lse=None), OK),
+    (dict(krs=S3(0, 0, 68)), E_ALIGN), (dict(io=1, vs=S3(0, 2, 128)), E_ALIGN),
+    (dict(ks=S3(0, 0, 1 << 24)), E_SHAPE), (dict(io=1, qs=S3(0, 0, 1 << 23)), E_SHAPE), (dict(vs=S3(0, 0, -128)), E_SHAPE),
+    (dict(krs=S3(0, 0, 1 << 40)), E_SHAPE), (dict(T=0, q=None, out=None, lse=None), OK),
 ])
 def test_forward_refusals(kw, want):
     a = dict(q=FAKE, qs=None, k=FAKE, ks=None, v=FAKE, vs=None, kr=FAKE, krs=None, cq=None, ck=None, N=2, H=4, T=100, S=120,
@@ -32,7 +34,7 @@ def test_forward_refusals(kw, want):
     (dict(out=None), E_NULL), (dict(lse=None), E_NULL), (dict(do=None), E_NULL), (dict(dkr=None), E_NULL), (dict(io=5), E_DTYPE),
     (dict(dr=48), E_SHAPE), (dict(scale=0.0), E_SCALE), (dict(do=FAKE + 4), E_ALIGN), (dict(dos=S3(0, 0, 129)), E_ALIGN),
     (dict(dq=FAKE + 8), E_ALIGN), (dict(ws=None), E_WS), (dict(wsb=1000), E_WS), (dict(ws=FAKE + 4), E_ALIGN),
-    (dict(T=0, S=0, ws=None, wsb=0), OK),
+    (dict(dos=S3(0, 0, 1 << 24)), E_SHAPE), (dict(dos=S3(0, 0, -128)), E_SHAPE), (dict(T=0, S=0, ws=None, wsb=0), OK),
 ])
 def test_backward_refusals(kw, want):
     a = dict(q=FAKE, qs=None, k=FAKE, ks=None, v=FAKE, vs=None, kr=FAKE, krs=None, out=FAKE, lse=FAKE, do=FAKE, dos=None, cq=None,
