@@ -138,8 +138,8 @@ def _stream(stream):
 
 def _stream_of(stream, device):
     """The stream a call on `device` launches on, as the integer ctypes passes on: the given one, else
-    that device's current stream."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    that device's current stream, read without making a Stream object (1.8 of a small call's 13 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _on_device(device):

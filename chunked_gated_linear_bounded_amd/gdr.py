@@ -36,15 +36,15 @@ def _plain(t, name, dtype, dev, shape):
     """Checks a contiguous tensor of a given shape (or None); returns its pointer."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device != dev or t.dtype != dtype:
         raise ValueError("%s must be %s on %s, is %s on %s" % (name, dtype, dev, t.dtype, t.device))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _shapes(q, k, v, g, beta, cu_seqlens):
