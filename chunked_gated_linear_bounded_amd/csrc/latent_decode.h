@@ -11,8 +11,9 @@
 // Up to 16 heads the 2 * 16 * (576 + 512) flops a 1,152-byte row costs are far below what HBM lets
 // pass; at 128 heads (two work-groups on the same keys, side by side on one XCD) the 272 KiB of LDS
 // reads per tile and work-group take about the time HBM needs for the tile.  The keys are split
-// over work-groups until the chip has several a CU; the parts are joined by their log-sum-exps in a
-// second kernel.
+// over work-groups until there are two a CU; the parts are joined by their log-sum-exps in a second
+// kernel.  48 sequences of 6,000 to 12,000 rows, 128 heads: 313 us and 14 for the join (three
+// work-groups a CU: 345 and 24).
 #pragma once
 #include "latent_common.h"
 
