@@ -36,4 +36,16 @@ hipError_t launch_gdr_fwd(const GdrLaunch &p);
 hipError_t launch_gdr_bwd(const GdrLaunch &p);
 hipError_t launch_gdr_decode(const GdrLaunch &p);
 
+// The sequential stages take 32 columns a work-group in place of 16 once those of 16 outnumber the
+// places for them: one a CU, or two where two fit (dk = 64, bf16).  Packed documents are ragged, a short
+// one's place is soon free, and two a CU still run faster than fewer, longer steps.  Microseconds of the
+// state stage and the reverse pass, 16 columns / 32: 5 sequences of 1024 x 12 heads (480 work-groups of
+// 16), dk = 128: 51 and 80 / 42 and 60, dk = 64: 36 and 53 / 36 and 50; 11 documents of 5000 tokens x 4
+// heads (352), dk = 128: 37 and 60 / 59 and 82, dk = 64: 23 and 36 / 33 and 47; 32 documents of 12,000
+// tokens x 8 heads (2048), dk = 128: 99 and 161 / 79 and 119.
+inline bool gdr_two_tiles(const GdrLaunch &p) {
+    const long long places = p.cu != nullptr || (p.dk == 64 && !p.fp32) ? 512 : 256;
+    return (long long)p.N * p.H * (p.dv / 16) > places;
+}
+
 }  // namespace kda

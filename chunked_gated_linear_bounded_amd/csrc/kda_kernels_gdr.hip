@@ -44,8 +44,7 @@ static hipError_t fwd_t(const GdrLaunch &p) {
     }
     const GdrStateArgs a{p.workspace, vals, p.v, st3(p.sv), seqs, p.H, r, nslot, p.dv, p.scale,
                          p.final_state, p.init_state, p.out, nullptr};
-    // 32 columns a work-group as soon as 16 would need more than one a CU
-    if ((long long)p.N * p.H * (p.dv / 16) > 256) return run_state<DK, F32, 2>(a, p.stream);
+    if (gdr_two_tiles(p)) return run_state<DK, F32, 2>(a, p.stream);
     return run_state<DK, F32, 1>(a, p.stream);
 }
 

@@ -57,7 +57,7 @@ static hipError_t bwd_t(const GdrLaunch &p) {
     }
     const GdrStateArgs a{keys, vals, p.v, st3(p.sv), seqs, p.H, r, nslot, p.dv, p.scale, nullptr, p.init_state, nullptr, fwd};
     const GdrRevArgs c{keys, vals, p.dout, st3(p.sdo), seqs, p.H, r, nslot, p.dv, p.scale, p.dfinal, p.dinit, p.dv_, rev};
-    e = (long long)p.N * p.H * (p.dv / 16) > 256 ? passes<DK, F32, 2>(p, a, c) : passes<DK, F32, 1>(p, a, c);
+    e = gdr_two_tiles(p) ? passes<DK, F32, 2>(p, a, c) : passes<DK, F32, 1>(p, a, c);
     if (e != hipSuccess || p.T == 0) return e;
     const GdrGradArgs d{keys, vals, p.v, p.g, p.dout, st3(p.sv), st3(p.sg), st3(p.sdo), seqs, p.Hk, r, nslot, p.scale,
                         fwd, rev, p.dq, p.dk_, p.dg, p.dbeta};

@@ -54,7 +54,7 @@ def test_waves_per_work_group(dtype):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("dk,T", [(128, 200), (64, 129), (128, 5)])
 def test_two_column_tiles(dk, T, dtype):
-    """More than 256 slices of 16 value columns: 32 a work-group, with a start state."""
+    """More than 256 slices of 16 value columns, 32 a work-group but for dk = 64 in bf16; a start state."""
     B, H, dv = 3, 12, 128
     x = inputs(B, 4, H, T, dk, dv, dtype, dk + T)
     S0 = _state(B, H, dv, dk, T)

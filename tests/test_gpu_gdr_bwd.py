@@ -57,6 +57,7 @@ def compare(got, ref, dtype, what):
 @pytest.mark.parametrize("B,Hk,H,T,dk,dv", [
     (1, 1, 1, 1, 64, 64), (1, 1, 2, 3, 128, 64), (2, 2, 2, 63, 64, 128), (1, 2, 4, 64, 128, 128), (1, 1, 3, 65, 128, 128),
     (1, 2, 2, 127, 64, 64), (2, 1, 4, 150, 128, 128), (3, 4, 16, 70, 128, 128), (3, 4, 12, 195, 64, 128),
+    (5, 7, 14, 66, 64, 128),
 ])
 def test_gradients(B, Hk, H, T, dk, dv, dtype):
     x = inputs(B, Hk, H, T, dk, dv, dtype, 7 + T)
