@@ -101,7 +101,6 @@ struct GdrSeqs {
 };
 
 // ---------------------------------------------------------------- fp16 pieces
-typedef __attribute__((ext_vector_type(2))) __fp16 pkh2;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 
 // x = hi + lo to 22 bits: hi is x cut off (not rounded) to fp16, so what is left is exact in
@@ -163,12 +162,6 @@ __device__ __forceinline__ f16x8 ld_frag_t(const lds_u8 *f0, const lds_u8 *f1, i
     const int off = frag_slot(cg, m) + 8 * (tile & 1);
     const f16x4 a = ld_tr16<f16x4>(f0 + off), b = ld_tr16<f16x4>(f1 + off);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// 16 bytes per lane from global memory straight to LDS: lane l of the wave lands at lds + 16 l.
-// `lds` is wave-uniform.
-__device__ __forceinline__ void load_lds16(const void *g, lds_u8 *lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g, (lds_void *)lds, 16, 0, 0);
 }
 
 }  // namespace kda

@@ -55,6 +55,8 @@ static hipError_t dispatch(const LatentLaunch &p) {
     if (p.dn == 64) return p.dr == 32 ? bwd_t<64, 32, F32>(p) : bwd_t<64, 64, F32>(p);
     return p.dr == 32 ? bwd_t<128, 32, F32>(p) : bwd_t<128, 64, F32>(p);
 }
-hipError_t launch_latent_bwd(const LatentLaunch &p) { return p.fp32 ? dispatch<true>(p) : dispatch<false>(p); }
+hipError_t launch_latent_bwd(const LatentLaunch &p) {
+    return p.fp32 ? dispatch<true>(p) : dispatch<false>(p);
+}
 
 }  // namespace kda

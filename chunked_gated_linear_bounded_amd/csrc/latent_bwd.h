@@ -19,9 +19,12 @@
 // case.  At 256 keys the rounding has fallen to a tenth of ds's own and a second walk would be 60 % of
 // the kernel's work.
 //
-// What is handed over is rounded to the inputs' type as the MFMA takes it in either case.  The rotary
+// What is handed over is rounded to the inputs' type as the MFMA takes it in either case.  Sums of a few
+// terms keep all of a term's rounding (dk 2.8e-3 off where the outputs' own rounding leaves 1.8e-3), so
+// the ds of a sequence of up to kExactKeys keys are two bf16 pieces, with a second product, which costs
+// so short a sequence nothing (and a long one, whose waves branch around it, 1 to 3 %).  The rotary
 // part's gradient goes to a float32 partial per head, which a third kernel sums.  16 heads x 4096
-// queries and keys, 128 + 64 channels: dq 180 us, dk and dv 215 us, matrix units busy 41 and 39 % of
+// queries and keys, 128 + 64 channels: dq 182 us, dk and dv 217 us, matrix units busy 41 and 39 % of
 // the time, the LDS 50 and 47 %; one kind of wave, 64-row tiles: 270 and 325 us.
 #pragma once
 #include "latent_common.h"
@@ -88,7 +91,8 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = (DN + DR) / 16, NQ = F32 ? 1 : 2, BM = 64 * NQ;
-    using S = LatentBwdLds<F32, 2 * NKB + 2 * NDB, NQ>;
+    constexpr int HAND = F32 ? NQ : 2 * NQ;  // ds, and what rounding left of it
+    using S = LatentBwdLds<F32, 2 * NKB + 2 * NDB, HAND>;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
     lds_u8 *sx = lds_base(smem);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
@@ -123,6 +127,7 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
         str.store(to, NKB, NDB, tid);
         stv.store(to + 2 * NKB * Op::FB, NDB, 0, tid);
     };
+    const bool exact = nk <= kExactKeys;
     const int pass0 = nkey <= kExactKeys ? 0 : 1;  // pass 0: delta alone
 
     // step kt: tile kt + 1 to LDS; p and ds of tile kt; the products of tile kt - 1
@@ -193,7 +198,11 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
                                 s[t][x][i] = pr * (d[t][x][i] - delta[x]);
                                 rest[x] += s[t][x][i];
                             }
-                        Op::put_lane(sx + S::EX + (kt & 1) * S::EXB + (w * NQ + x) * Op::FB, lane, Op::pair(s[0][x], s[1][x]));
+                        lds_u8 *to = sx + S::EX + (kt & 1) * S::EXB + (w * HAND + x) * Op::FB;
+                        const V8 r = Op::pair(s[0][x], s[1][x]);
+                        Op::put_lane(to, lane, r);
+                        if constexpr (!F32)
+                            if (exact) Op::put_lane(to + NQ * Op::FB, lane, Op::rest(s[0][x], s[1][x], r));
                     }
                 }
                 buf = nb;
@@ -224,28 +233,34 @@ __global__ __launch_bounds__(512) void latent_dq_kernel(const LatentBwdArgs p) {
             load(kt + 2);
             if (kt > 0 && pass > 0) {
                 const lds_u8 *sk = sx + pb * S::TILE;
-                V8 sf[NQ];
+                auto add = [&](const lds_u8 *from) {
+                    V8 sf[NQ];
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) sf[x] = Op::get_lane(sx + S::EX + ((kt - 1) & 1) * S::EXB + (w * NQ + x) * Op::FB, lane);
-                // four column tiles' fragments are read while the four before are multiplied
-                V8 f4[2][4];
-                auto read = [&](int j) {
+                    for (int x = 0; x < NQ; ++x) sf[x] = Op::get_lane(from + (w * HAND + x) * Op::FB, lane);
+                    // four column tiles' fragments are read while the four before are multiplied
+                    V8 f4[2][4];
+                    auto read = [&](int j) {
 #pragma unroll
-                    for (int t = 4 * j; t < min(4 * j + 4, NT); ++t) {
-                        const lds_u8 *f0 = sk + (t >> 1) * Op::FB;
-                        f4[j & 1][t & 3] = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
+                        for (int t = 4 * j; t < min(4 * j + 4, NT); ++t) {
+                            const lds_u8 *f0 = sk + (t >> 1) * Op::FB;
+                            f4[j & 1][t & 3] = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
+                        }
+                    };
+                    read(0);
+#pragma unroll
+                    for (int j = 0; j < (NT + 3) / 4; ++j) {
+                        read(j + 1);
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int t = 4 * j; t < min(4 * j + 4, NT); ++t)
+#pragma unroll
+                            for (int x = 0; x < NQ; ++x) dq[t][x] = Op::mma(f4[j & 1][t & 3], sf[x], dq[t][x]);
                     }
                 };
-                read(0);
-#pragma unroll
-                for (int j = 0; j < (NT + 3) / 4; ++j) {
-                    read(j + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int t = 4 * j; t < min(4 * j + 4, NT); ++t)
-#pragma unroll
-                        for (int x = 0; x < NQ; ++x) dq[t][x] = Op::mma(f4[j & 1][t & 3], sf[x], dq[t][x]);
-                }
+                const lds_u8 *ex = sx + S::EX + ((kt - 1) & 1) * S::EXB;
+                add(ex);
+                if constexpr (!F32)
+                    if (exact) add(ex + NQ * Op::FB);
             }
             buf = nb;
         }
@@ -273,7 +288,8 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int NKB = (DN + DR) / 32, NDB = DN / 32, NT = (DN + DR) / 16, NV = DN / 16, NK = F32 ? 1 : 2, BN = 64 * NK;
-    using S = LatentBwdLds<F32, 2 * NKB + 2 * NDB, 2 * NK>;
+    constexpr int HAND = F32 ? 2 * NK : 3 * NK;  // p, ds, and what rounding left of ds
+    using S = LatentBwdLds<F32, 2 * NKB + 2 * NDB, HAND>;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
     __shared__ __attribute__((aligned(16))) float sl[3][32], sd[3][32];
     lds_u8 *sx = lds_base(smem);
@@ -291,6 +307,7 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
     const E *qp = reinterpret_cast<const E *>(p.q) + b * p.sq.b + h * p.sq.h + (long long)q0 * p.sq.t;
     const E *dp_ = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)q0 * p.sdo.t;
     const size_t qrow = (size_t)(b * p.H + h) * p.seqs.T + q0;
+    const bool exact = nk <= kExactKeys;
     // queries that see the tile's first key stand at its index minus shift, or later
     const int t_first = max(0, tile * BN - shift) / 32, ntq = max(0, (nq + 31) / 32 - t_first);
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -394,9 +411,12 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
                             s[t][x][i] = pr;
                             d[t][x][i] = pr * (d[t][x][i] - d4[t][i]);
                         }
-                    lds_u8 *to = sx + S::EX + (it & 1) * S::EXB + (w * NK + x) * 2 * Op::FB;
+                    lds_u8 *to = sx + S::EX + (it & 1) * S::EXB + (w * HAND + x) * Op::FB;
+                    const V8 r = Op::pair(d[0][x], d[1][x]);
                     Op::put_lane(to, lane, Op::pair(s[0][x], s[1][x]));
-                    Op::put_lane(to + Op::FB, lane, Op::pair(d[0][x], d[1][x]));
+                    Op::put_lane(to + NK * Op::FB, lane, r);
+                    if constexpr (!F32)
+                        if (exact) Op::put_lane(to + 2 * NK * Op::FB, lane, Op::rest(d[0][x], d[1][x], r));
                 }
             }
             buf = nb;
@@ -419,13 +439,10 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
         load(it + 2);
         if (it > 0) {
             const lds_u8 *sq = sx + pb * S::TILE, *so = sq + 2 * NKB * Op::FB;
-            V8 pf[NK], sf[NK];
+            const lds_u8 *ex = sx + S::EX + ((it - 1) & 1) * S::EXB + w * HAND * Op::FB;
+            V8 pf[NK];
 #pragma unroll
-            for (int x = 0; x < NK; ++x) {
-                const lds_u8 *from = sx + S::EX + ((it - 1) & 1) * S::EXB + (w * NK + x) * 2 * Op::FB;
-                pf[x] = Op::get_lane(from, lane);
-                sf[x] = Op::get_lane(from + Op::FB, lane);
-            }
+            for (int x = 0; x < NK; ++x) pf[x] = Op::get_lane(ex + x * Op::FB, lane);
 #pragma unroll
             for (int t = 0; t < NV; ++t) {
                 const lds_u8 *f0 = so + (t >> 1) * Op::FB;
@@ -433,13 +450,21 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
 #pragma unroll
                 for (int x = 0; x < NK; ++x) dv[t][x] = Op::mma(of, pf[x], dv[t][x]);
             }
+            auto add = [&](const lds_u8 *from) {
+                V8 sf[NK];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const lds_u8 *f0 = sq + (t >> 1) * Op::FB;
-                const V8 qf = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
+                for (int x = 0; x < NK; ++x) sf[x] = Op::get_lane(from + x * Op::FB, lane);
 #pragma unroll
-                for (int x = 0; x < NK; ++x) dk[t][x] = Op::mma(qf, sf[x], dk[t][x]);
-            }
+                for (int t = 0; t < NT; ++t) {
+                    const lds_u8 *f0 = sq + (t >> 1) * Op::FB;
+                    const V8 qf = Op::get_t(f0, f0 + NKB * Op::FB, t, lane);
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) dk[t][x] = Op::mma(qf, sf[x], dk[t][x]);
+                }
+            };
+            add(ex + NK * Op::FB);
+            if constexpr (!F32)
+                if (exact) add(ex + 2 * NK * Op::FB);
         }
         buf = nb;
     }

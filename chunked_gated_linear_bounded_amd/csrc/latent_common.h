@@ -45,6 +45,13 @@ template <> struct AttnOp<false> {
         for (int i = 0; i < 4; ++i) { r[i] = (__bf16)x[i]; r[4 + i] = (__bf16)y[i]; }
         return r;
     }
+    // what pair(x, y) = r left of x and y
+    __device__ __forceinline__ static V8 rest(const f32x4 &x, const f32x4 &y, const V8 &r) {
+        V8 l;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { l[i] = (__bf16)(x[i] - (float)r[i]); l[4 + i] = (__bf16)(y[i] - (float)r[4 + i]); }
+        return l;
+    }
     typedef __attribute__((address_space(3))) bf16x4 lds_b4;
     typedef __attribute__((address_space(3))) bf16x8 lds_b8;
     __device__ __forceinline__ static int slot(int kb, int g, int m) { return 8 * (16 * g + (m ^ (8 * (g >> 1)) ^ (2 * (kb & 3)))); }
