@@ -4,7 +4,7 @@
 // full batch and the launch bounds a single user.  A wave takes 4 value rows, 16 bytes of a row per
 // lane, with every load issued before the first use; a work-group takes 16 rows, so one user's 32
 // heads already make 256 work-groups.  256 users x 32 heads: 190 us for 1.08 GB, 5.7 TB/s; one user
-// 4 us, less than the call's way through the host.
+// 3 us, less than the call's way through the host.
 #pragma once
 #include "gdr_common.h"
 #include "kda_decode.h"

@@ -16,7 +16,7 @@
 // max|k|) max|U|.  A bound that is 2^10 too large still leaves two pieces their 22 bits.
 //
 // The chain of chunks is what bounds the stage, three exchanges through LDS one behind the other.
-// 65,536 tokens x 32 heads (16 columns a work-group, one work-group a CU): 1.53 us a chunk; the chain's
+// 65,536 tokens x 32 heads (16 columns a work-group, one work-group a CU): 1.48 us a chunk; the chain's
 // waves with the loads and outputs on them 1.78 us, 215 of their vector instructions and the LDS reads
 // of 100 KiB a chunk being left; one wave on its own columns, no barriers, 6.3 us.
 //

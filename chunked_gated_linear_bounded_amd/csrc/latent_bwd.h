@@ -24,8 +24,8 @@
 // the ds of a sequence of up to kExactKeys keys are two bf16 pieces, with a second product, which costs
 // so short a sequence nothing (and a long one, whose waves branch around it, 1 to 3 %).  The rotary
 // part's gradient goes to a float32 partial per head, which a third kernel sums.  16 heads x 4096
-// queries and keys, 128 + 64 channels: dq 182 us, dk and dv 217 us, matrix units busy 41 and 39 % of
-// the time, the LDS 50 and 47 %; one kind of wave, 64-row tiles: 270 and 325 us.
+// queries and keys, 128 + 64 channels: dq 179 us, dk and dv 212 us, matrix units busy 38 and 41 % of
+// the time, the LDS 47 and 49 %; one kind of wave, 64-row tiles: 270 and 325 us.
 #pragma once
 #include "latent_common.h"
 
