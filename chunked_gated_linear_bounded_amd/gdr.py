@@ -20,16 +20,16 @@ def _view(t, name, dtype, dev, inner=True):
     """Checks a strided input; returns (pointer, element strides of all but the last dimension)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != dev or t.device.type != "cuda":
+    if dev.type != "cuda" or t.device != dev:
         raise ValueError("%s must be a GPU tensor on %s, is on %s" % (name, dev, t.device))
     if t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     s = t.stride()
     if inner:
-        if t.shape[-1] > 1 and s[-1] != 1 and t.numel() > 0:
+        if s[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0:
             raise ValueError("the last dimension of %s must be contiguous" % name)
         s = s[:-1]
-    return t.data_ptr(), _S3(*((0,) * (3 - len(s)) + tuple(s)))
+    return t.data_ptr(), _S3(*s) if len(s) == 3 else _S3(*((0,) * (3 - len(s)) + s))
 
 
 def _plain(t, name, dtype, dev, shape):
