@@ -174,6 +174,55 @@ def test_one_visible_key_has_no_gradient(dtype):
     assert torch.isfinite(g["dv"]).all() and g["dv"][:, alone].any()
 
 
+def test_bad_boundaries_stay_inside():
+    q, kv, r, _ = inputs((), 1, 150, 150, 64, 32, BF, 3)
+    k, v = split(kv.cuda(), 64)
+    for a, c in (([-5, 70, 900], [0, 70, 150]), ([100, 20, 150], [-9, 500, 2]), ([0, 75, 150], [2 ** 31 - 1, -2 ** 31, 64])):
+        out = kda.latent_attn_fwd_varlen(q.cuda(), k, v, r.cuda(), *(torch.tensor(t, dtype=torch.int32).cuda() for t in (a, c)))
+        torch.cuda.synchronize()
+        assert out.shape == (1, 150, 64)
+
+
+def test_large_scores():
+    """Scores of a few thousand: the running maximum keeps every exponential in range."""
+    q, kv, r, do = inputs((1,), 2, 200, 200, 128, 64, F32, 5)
+    q = q * 40
+    k, v = split(kv, 128)
+    out, lse = kda.latent_attn_fwd(q.cuda(), *split(kv.cuda(), 128), r.cuda(), return_lse=True)
+    for h in range(2):
+        ref = one(q[0, h], torch.cat([k[0, h], r[0]], -1), v[0, h], 192 ** -0.5, F32)
+        _check(out[0, h], *ref["out"], "out")
+        _check(lse[0, h], *ref["lse"], "lse")
+
+
+def test_autograd_and_differences():
+    """loss.backward() through LatentAttnFunction on the up-projection's output gives the entry point's
+    gradients, and those agree with central differences of the float64 formula (error h^2, h = 1e-4)."""
+    dn, dr, H, T = 64, 32, 2, 70
+    q, kv, r, do = inputs((1,), H, T, T, dn, dr, F32, 9)
+    leaf = [t.cuda().requires_grad_() for t in (q, kv, r)]
+    out = kda.LatentAttnFunction.apply(leaf[0], *split(leaf[1], dn), leaf[2])
+    (out * do.cuda()).sum().backward()
+    k, v = split(kv.cuda(), dn)
+    o, lse = kda.latent_attn_fwd(q.cuda(), k, v, r.cuda(), return_lse=True)
+    g = kda.latent_attn_bwd(q.cuda(), k, v, r.cuda(), o, lse, do.cuda())
+    assert torch.equal(leaf[0].grad, g["dq"]) and torch.equal(leaf[2].grad, g["dk_rope"])
+    assert torch.equal(leaf[1].grad, torch.cat([g["dk"], g["dv"]], -1).transpose(1, 2))
+
+    def loss(q, kv, r):
+        k, v = split(kv[0], dn)
+        return sum(float((one(q[0, h], torch.cat([k[h], r[0]], -1), v[h], (dn + dr) ** -0.5, F32)["out"][0] * do[0, h].double()).sum())
+                   for h in range(H))
+
+    args, gen = [t.double() for t in (q, kv, r)], torch.Generator().manual_seed(4)
+    for i in range(3):
+        u = torch.randn(args[i].shape, generator=gen, dtype=torch.float64)
+        u /= u.norm()
+        up, down = (loss(*[a + s * 1e-4 * u if j == i else a for j, a in enumerate(args)]) for s in (1, -1))
+        grad = leaf[i].grad.double().cpu()
+        assert abs((up - down) / 2e-4 - float((grad * u).sum())) <= 1e-5 * float(grad.norm()) + 1e-6
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("H,dc,page,lens", [
     (1, 512, 64, [1]), (16, 512, 64, [64, 65, 1, 0]), (5, 256, 16, [31, 32, 33, 500]), (17, 512, 7, [100, 3]), (32, 256, 128, [700, 20]),
