@@ -18,8 +18,8 @@
 // Lane (g, m) of column block kb has slot 16 g + (m ^ 8 (g / 2) ^ 2 (kb % 4)): all 32 lanes of a half
 // wave fall on different banks in the plain read, in the transposed one, and when rows are stored.
 //
-// bf16 inputs use 16x16x32 bf16 MFMAs, P and dS rounded to bf16; float32 inputs use float32 MFMAs
-// (eight 16x16x4 steps).  Softmax statistics and all sums are float32.
+// bf16 inputs use 16x16x32 bf16 MFMAs, P and dS rounded to bf16 (dS of few keys to two pieces);
+// float32 inputs use float32 MFMAs (eight 16x16x4 steps).  Softmax statistics and all sums are float32.
 #pragma once
 #include "gdr_common.h"
 
