@@ -189,21 +189,17 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         // what the state stage bounds its operands with (GdrLayout)
         const float ck = wave_max(fabsf(bv) * ex2((float)G) * sK1[lane]), bm = wave_max(fabsf(bv));
         const float cl = wave_max(ex2((float)(last - G)) * sK1[lane]);
-        float ks = in ? sKm[lane] : 0.f, kc = ks * ex2((float)(last - G));
+        float ks = in ? sKm[lane] : 0.f;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            kc += __shfl_xor(kc, d, 64);
-            ks += __shfl_xor(ks, d, 64);
-        }
+        for (int d = 1; d < 64; d <<= 1) ks += __shfl_xor(ks, d, 64);
         if (lane == 0) {
             hd[192] = ex2((float)last);
             reinterpret_cast<int *>(vrec)[195] = ek;
             reinterpret_cast<int *>(vrec)[196] = eq;
             hd[197] = ck;
             hd[198] = bm;
-            hd[200] = kc;
+            hd[200] = ks;
             hd[201] = cl;
-            hd[202] = ks;
         }
     }
     __syncthreads();

@@ -373,7 +373,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         h0 = *reinterpret_cast<const lds_f4 *>(hd + 768);
         h1 = *reinterpret_cast<const lds_f4 *>(hd + 784);
         cl_ = *reinterpret_cast<const lds_f1 *>(hd + 804);
-        ks_ = *reinterpret_cast<const lds_f1 *>(hd + 808);
+        ks_ = *reinterpret_cast<const lds_f1 *>(hd + 800);
         d0max = max4(sMax + 16);
         dqmax = max4(sMax + 20);
     };

@@ -12,8 +12,10 @@
 //
 // The exponents of the fp16 pieces have to be the same in all four waves.  They come from a bound,
 // one norm away from a maximum that was published with the operand before: |X| <= max b max|V| +
-// max(b e^G |k|_1) max|P|, |U| <= |T|_inf max|X|, |P'| <= e^{G_last} max|P| + sum(e^{G_last - G}
-// max|k|) max|U|.  A bound that is 2^10 too large still leaves two pieces their 22 bits.
+// max(b e^G |k|_1) max|P|, |U| <= |T|_inf max|X|, |P'| <= e^{G_last} max|P| + sum(max|k|) max|e^{G_last - G}
+// U|: the maximum is that of the decayed U, so the sum is not decayed again (keys that end before the
+// chunk does would leave it far below P').  A bound that is 2^10 too large still leaves two pieces their
+// 22 bits.
 //
 // The chain of chunks is what bounds the stage, three exchanges through LDS one behind the other.
 // 65,536 tokens x 32 heads (16 columns a work-group, one work-group a CU): 1.48 us a chunk; the chain's
@@ -312,7 +314,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     f16x8 kf[NI][NKB], tf[2][2];
     E4 v[NCT];
     f32x4 eG, eL, be, h0, h1;
-    float cc_;
+    float ks_;
     // what the other waves have laid out for chunk c
     auto get = [&](int c) {
         const lds_u8 *in = sx + S::IN + (c & 1) * S::INB;
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
         be = *reinterpret_cast<const lds_f4 *>(hd + 512 + 4 * row0);
         h0 = *reinterpret_cast<const lds_f4 *>(hd + 768);
         h1 = *reinterpret_cast<const lds_f4 *>(hd + 784);
-        cc_ = *reinterpret_cast<const __attribute__((address_space(3))) float *>(hd + 800);
+        ks_ = *reinterpret_cast<const __attribute__((address_space(3))) float *>(hd + 800);
     };
     int ep = 0;
     if (nchunk > 0) {
@@ -347,7 +349,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     }
     for (int c = 0; c < nchunk; ++c) {
         barrier_lds();  // (1)
-        const float pmax = max4(sMax), last = h0[0], kbound = h1[1], bbound = h1[2], tbound = h1[3], kcol = cc_;
+        const float pmax = max4(sMax), last = h0[0], kbound = h1[1], bbound = h1[2], tbound = h1[3], ksum = ks_;
         const float et_ = h0[1], ek_ = h0[3];
         const int et = __builtin_bit_cast(int, et_), ek = __builtin_bit_cast(int, ek_);
 
@@ -466,7 +468,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
                 for (int i = 0; i < 4; ++i)
                     P[t][ct][i] = fmaf(P[t][ct][i], last, scale_down(z[ct][i] + z1[ct][i], ek + eu));
         }
-        ep = gdr_exp(last * pmax + kcol * emax);
+        ep = gdr_exp(last * pmax + ksum * emax);
         put_p(ep);
         const float mp = max_p();
         if (lane == 0) sMax[w] = mp;
