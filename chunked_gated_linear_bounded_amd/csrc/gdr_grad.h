@@ -12,11 +12,12 @@
 //
 // Wave (rw, ch) owns token tile rw and one half of the key channels.  Operands are fp16 with one
 // exponent per block (float32 inputs: two pieces); what the passes kept with an exponent per 16
-// columns is brought to the smallest of them on its way into LDS.  The stage reads about 200 KiB a
-// chunk and value head at d = 128 (bf16) and writes 32 KiB a key head; its 656 MFMAs a head are a
-// tenth of that traffic's time (4096 tokens x 32 heads: 166 us, most of it the four phases' barriers
-// with one work-group of eight waves a CU), so the four phases share one 64 KiB buffer (P, then dP', then K and
-// Q; dX, then X1 and X2).
+// columns is brought to the smallest of them on its way into LDS.  diag(b) X2 takes b times the power of
+// two that brings max |b| below 1: X2 itself sits at 2^13 .. 2^14, and a beta of 4 would reach fp16's end.
+// The stage reads about 200 KiB a chunk and value head at d = 128 (bf16) and writes 32 KiB a key head;
+// its 656 MFMAs a head are a tenth of that traffic's time (4096 tokens x 32 heads: 166 us, most of it
+// the four phases' barriers with one work-group of eight waves a CU), so the four phases share one 64
+// KiB buffer (P, then dP', then K and Q; dX, then X1 and X2).
 #pragma once
 #include "gdr_state.h"
 
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
     constexpr int BA = NI * (PP > 2 * L.mat() ? PP : 2 * L.mat()), BU = NI * PU, BX = NI * (PU > 16384 ? PU : 16384);
     __shared__ __attribute__((aligned(1024))) unsigned char smem[BA + BU + BX];
     __shared__ double sG[64];
-    __shared__ __attribute__((aligned(16))) _Float16 sBh[64];
+    __shared__ __attribute__((aligned(16))) _Float16 sBh[64];  // b 2^eb
     __shared__ float sGi[2][64], sBe[2][64], sRed[4][8];  // per half: dG, dbeta; per wave: max X1, X2, <P, dP'>, sum for dG_last
     lds_u8 *sa = lds_base(smem), *su = sa + BA, *sxx = su + BU;
     const int slot = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, H = p.Hk * p.r;
@@ -95,6 +96,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
         const f32x4 be = *reinterpret_cast<const f32x4 *>(hd + 128 + row0);
         const float last = hd[192];
         const int ek = reinterpret_cast<const int *>(vrec)[195], eq = reinterpret_cast<const int *>(vrec)[196];
+        const int eb = max(gdr_exp(hd[198]) - 14, -126);  // max |b| 2^eb in [0.5, 1)
         // the smallest exponents over the slices
         int ep = 1 << 20, eu = ep, epr = ep, ex = ep;
 #pragma unroll
@@ -143,7 +145,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
                 if (lane >= d) G += y;
             }
             sG[lane] = G;
-            sBh[lane] = (_Float16)hd[128 + lane];
+            sBh[lane] = (_Float16)(hd[128 + lane] * pow2f(eb));
         }
         // dO and V rows of this wave's tile, lane (g, n): token perm_row(rw, n)
         const int tok = perm_row(rw, n), tokc = tok < nrow ? tok : nrow - 1;
@@ -372,8 +374,8 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
                         const float *bb = hd + 128 + 32 * kb + 8 * g;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            lo4[j] = ((float)c[0][j] + (float)c[NI - 1][j]) * bb[j];
-                            hi4[j] = ((float)c[0][4 + j] + (float)c[NI - 1][4 + j]) * bb[4 + j];
+                            lo4[j] = ((float)c[0][j] + (float)c[NI - 1][j]) * (bb[j] * pow2f(eb));
+                            hi4[j] = ((float)c[0][4 + j] + (float)c[NI - 1][4 + j]) * (bb[4 + j] * pow2f(eb));
                         }
                         split_pair(lo4, hi4, 1.f, c[0], c[NI - 1]);
                     } else {
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
                 kv = scale_down(kv, ek);
                 qv = scale_down(qv, eq);
                 const float dqh = E1[t][i] + scale_down(q1[i], e1 + ek);
-                const float x1 = scale_down(k1[i], e1 + eq), rr_ = scale_down(r[i], e2 + ek), ss = scale_down(s[i], e2 + ek);
+                const float x1 = scale_down(k1[i], e1 + eq), rr_ = scale_down(r[i], e2 + ek), ss = scale_down(s[i], e2 + ek + eb);
                 dq[t][i] += dqh;
                 dk[t][i] += x1 + E3[t][i] - be[i] * E2[t][i] + be[i] * rr_ + ss;
                 aG[i] += qv * dqh - kv * (x1 + E3[t][i] + be[i] * E2[t][i] - be[i] * rr_ + ss);

@@ -60,3 +60,14 @@ def _tail(sizes, dtype, decay):
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_keys_end_before_the_chunk(dtype, sizes, decay):
     _fwd_and_grads(*_tail(sizes, dtype, decay), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("norm", [0.3, 1e-3, 300.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_beta_far_from_one(dtype, norm):
+    """Keys of another norm, and betas that keep beta |k|^2 below one: up to 10, to 9e5, to 1e-5."""
+    x = list(inputs(2, 2, 4, 150, 128, 64, dtype, 81))
+    x[1] = (x[1].double() * norm).to(dtype)
+    x[4] = (x[4].double() * 0.9 / norm ** 2).to(dtype)
+    dout = torch.randn(2, 4, 150, 64, generator=torch.Generator().manual_seed(4)).to(dtype)
+    _fwd_and_grads(x, dout, 128 ** -0.5)
