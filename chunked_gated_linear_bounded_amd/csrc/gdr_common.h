@@ -130,10 +130,11 @@ __device__ __forceinline__ f32x4 mma16(const f16x8 &a, const f16x8 &b, f32x4 c) 
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// exponent that puts magnitudes up to m at 2^13 .. 2^14; 0 for a block of zeros, and kept where
-// 2^e and 2^-e are normal floats (an infinite or NaN block passes through as such)
+// exponent that puts magnitudes up to m at 2^13 .. 2^14, kept where 2^e and 2^-e are normal floats (an
+// infinite or NaN block passes through as such).  A block of zeros has the largest, so that it does not
+// count where several blocks are brought to the smallest of their exponents.
 __device__ __forceinline__ int gdr_exp(float m) {
-    if (!(m > 0.f)) return 0;
+    if (!(m > 0.f)) return 120;
     const int e = pow2_scale(m);
     return e > 120 ? 120 : (e < -120 ? -120 : e);
 }

@@ -71,3 +71,17 @@ def test_beta_far_from_one(dtype, norm):
     x[4] = (x[4].double() * 0.9 / norm ** 2).to(dtype)
     dout = torch.randn(2, 4, 150, 64, generator=torch.Generator().manual_seed(4)).to(dtype)
     _fwd_and_grads(x, dout, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_zero_channels(dtype, sizes):
+    """Heads padded with zero channels (values and gradients of 16 or 32 columns), beside small values
+    and small gradients."""
+    B, Hk, H, dv = sizes
+    x = inputs(B, Hk, H, 150, 128, dv, dtype, 91)
+    dout = torch.randn(B, H, 150, dv, generator=torch.Generator().manual_seed(5)).to(dtype)
+    for t in (x[2], dout):
+        t *= 2.0 ** -20
+        t[..., -32:] = 0.0
+    _fwd_and_grads(x, dout, 128 ** -0.5)
