@@ -62,7 +62,8 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
     __shared__ __attribute__((aligned(16))) unsigned char smem[kBuf];
     __shared__ double sG[64];
     __shared__ float sBeta[64], sK1[64], sKm[64];  // beta; sum and maximum of |k| per token
-    __shared__ float red[20];
+    __shared__ __attribute__((aligned(16))) float sGf[64];  // G in float32, for a bound
+    __shared__ float red[24];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x, h = blockIdx.y, b = blockIdx.z, H = p.Hk * p.r, kh = h / p.r;
@@ -181,6 +182,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         }
         const double last = __shfl(G, 63, 64);
         sG[lane] = G;
+        sGf[lane] = (float)G;
         sBeta[lane] = bv;
         float *hd = reinterpret_cast<float *>(vrec);
         hd[lane] = ex2((float)G);
@@ -188,7 +190,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         hd[128 + lane] = bv;
         // what the state stage bounds its operands with (GdrLayout)
         const float ck = wave_max(fabsf(bv) * ex2((float)G) * sK1[lane]), bm = wave_max(fabsf(bv));
-        const float cl = wave_max(ex2((float)(last - G)) * sK1[lane]);
+        const float cl = wave_max(ex2((float)(last - G)) * sK1[lane]), k1 = wave_max(sK1[lane]);
         float ks = in ? sKm[lane] : 0.f;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) ks += __shfl_xor(ks, d, 64);
@@ -200,6 +202,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
             hd[198] = bm;
             hd[200] = ks;
             hd[201] = cl;
+            hd[203] = k1;
         }
     }
     __syncthreads();
@@ -294,7 +297,8 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         }
     __syncthreads();
     f32x4 ft[2][2], fm[2][2];
-    float mt = 0.f, mm = 0.f, rs = 0.f;
+    float mt = 0.f, mm = 0.f, rs = 0.f, rt = 0.f;
+    const float gi = sGf[perm_row(w, m)];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
         if (kb == 0 || w >= 2) {
@@ -307,8 +311,14 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
                 mm = max_abs4(fm[kb][o], mm);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rs += fabsf(ft[kb][o][i]);
+                const f32x4 gj = *reinterpret_cast<const f32x4 *>(sGf + 32 * kb + 8 * g + 4 * o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rt = fmaf(fabsf(ft[kb][o][i]), ex2(fminf(gj[i] - gi, 126.f)), rt);
             }
         }
+    rt += __shfl_xor(rt, 16, 64);
+    rt += __shfl_xor(rt, 32, 64);
+    rt = block_max4(rt, red + 20);
     rs += __shfl_xor(rs, 16, 64);
     rs += __shfl_xor(rs, 32, 64);
     rs = block_max4(rs, red + 16);
@@ -317,6 +327,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         reinterpret_cast<int *>(vrec)[193] = et;
         reinterpret_cast<int *>(vrec)[194] = em;
         reinterpret_cast<float *>(vrec)[199] = rs;
+        reinterpret_cast<float *>(vrec)[202] = rt;
     }
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)

@@ -49,8 +49,8 @@ struct GdrLayout {
     __host__ __device__ constexpr size_t key_bytes() const { return 256 + 2 * (size_t)ni * mat(); }
     // value record, one per (batch, value head, chunk): header, T hi, T lo, M hi (, M lo)
     // header: float eG[64], eL[64] (e^{G_last - G}), beta[64]; then at float 192: e^{G_last}; int
-    // exponents of T, M, K, Q; and five norms, max b e^G |k|_1, max b, max row sum of |T|, sum over
-    // the tokens of max |k|, max e^{G_last - G} |k|_1
+    // exponents of T, M, K, Q; and seven norms, max b e^G |k|_1, max b, max row sum of |T|, sum over
+    // the tokens of max |k|, max e^{G_last - G} |k|_1, max row sum of |T_ij| e^{G_j - G_i}, max |k|_1
     static constexpr int kTri = 6 * 1024;  // six causal 16x32 fragments of a 64x64 lower triangle
     static constexpr int kHead = 1024;
     __host__ __device__ constexpr int t_off(int piece) const { return kHead + piece * kTri; }

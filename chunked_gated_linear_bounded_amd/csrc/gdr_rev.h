@@ -12,8 +12,10 @@
 // intervals before it is read, Q, M and dO two chunks ahead, K and T in the chunk itself.  The
 // exponents of the pieces come from bounds as in gdr_state.h, |dU| <= max|M^T dO| + max(e^{G_last - G}
 // |k|_1) max|dP'|, |dX| <= 64 max|T| max|dU|, |dP| <= e^{G_last} max|dP'| + max|Q^T H| + sum(max|k|)
-// max|F|.  A state gradient that a caller asks for (dinitial_state, float32) is exact to the same 22
-// bits as the final state.
+// max|F|.  H and F have their own, of the decayed values, F_j = b_j sum_i (T_ij e^{G_j - G_i}) e^{G_i} dU_i
+// with |e^G dU| <= max|e^G M^T dO| + e^{G_last} max|k|_1 max|dP'|: where the chunk's first tokens have no gradient, both are as small as the decay over them.  A state
+// gradient that a caller asks for (dinitial_state, float32) is exact to the same 22 bits as the final
+// state.
 //
 // 4096 tokens x 32 heads: 2.4 us a chunk, 157 us; with everything on the chain's four waves, and a
 // fourth barrier for dP's maximum, 3.2 us, 204 us.
@@ -57,7 +59,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
     typedef __attribute__((address_space(3))) f32x4 lds_f4;
     typedef __attribute__((address_space(3))) float lds_f1;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
-    __shared__ float sMax[24];  // per wave: max |dP'|, |dU|, |F|, |dO|, |M^T dO|, |Q^T H|
+    __shared__ __attribute__((aligned(16))) float sMax[32];  // per wave: max |dP'|, |dU|, |F|, |dO|, |M^T dO|, |Q^T H|, |e^G M^T dO|, |e^G dO|
     __shared__ int sExp[2];     // exponents of dP's and of dX's pieces
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wid & 3;
@@ -114,25 +116,34 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
             }
             const unsigned char *r = krec + (size_t)c * L.key_bytes() + w * NKB * 1024 + fo;
             const unsigned char *v = vrec + (size_t)c * L.val_bytes();
+            eG = *reinterpret_cast<const f32x4 *>(v + 4 * row0);
 #pragma unroll
             for (int x = 0; x < NI; ++x)
 #pragma unroll
                 for (int kb = 0; kb < NKB; ++kb) qf[x][kb] = *reinterpret_cast<const f16x8 *>(r + L.q_off(x) + kb * 1024);
 #pragma unroll
             for (int i = 0; i < 3; ++i) mf[i] = *reinterpret_cast<const f16x8 *>(v + L.m_off(0) + (3 * w + i) * 1024 + fo);
-            eG = *reinterpret_cast<const f32x4 *>(v + 4 * row0);
             em = reinterpret_cast<const int *>(v)[194];
             eq = reinterpret_cast<const int *>(v)[196];
         };
         auto grad_of = [&](int ct, int i) { return 64 * at + row0 + i < len ? to_f(vn[ct][i]) : 0.f; };  // none past the last row
         auto publish_max = [&]() {
-            float m = 0.f;
+            __builtin_amdgcn_sched_barrier(0);  // mixed in with what stands before, 2 % slower
+            float m = 0.f, mh = 0.f;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(grad_of(ct, i)));
+                for (int i = 0; i < 4; ++i) {
+                    const float d = grad_of(ct, i);
+                    m = fmaxf(m, fabsf(d));
+                    mh = fmaxf(mh, fabsf(eG[i] * d));
+                }
             m = wave_max(m);
-            if (lane == 0) sMax[12 + w] = m;
+            mh = wave_max(mh);
+            if (lane == 0) {
+                sMax[12 + w] = m;
+                sMax[28 + w] = mh;
+            }
         };
         auto put_kt = [&]() {
 #pragma unroll
@@ -145,12 +156,13 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         };
         auto put_head = [&](int c) { *reinterpret_cast<lds_f1 *>(sx + S::HEAD + (c & 1) * L.kHead + 4 * (64 * w + lane)) = head; };
         int eo = 0, eh = 0, em_ = 0, eq_ = 0;  // of what is in LDS
+        f32x4 eG_ = zero;
         auto put_qm = [&]() {
-            const float omax = max4(sMax + 12);
-            eo = gdr_exp(omax);
-            eh = gdr_exp(fabsf(p.scale) * omax);
+            eo = gdr_exp(max4(sMax + 12));
+            eh = gdr_exp(fabsf(p.scale) * max4(sMax + 28));
             em_ = em;
             eq_ = eq;
+            eG_ = eG;
 #pragma unroll
             for (int x = 0; x < NI; ++x)
 #pragma unroll
@@ -201,11 +213,12 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
                 for (int i = 0; i < 4; ++i) d0[ct][i] = scale_down(y[ct][i] + y1[ct][i], em_ + eo);
         };
         auto put_terms = [&]() {  // M^T dO, and Q^T (scale e^G dO)
-            float m0 = 0.f, mq = 0.f;
+            float m0 = 0.f, mg = 0.f, mq = 0.f;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 *reinterpret_cast<lds_f4 *>(sx + S::D0 + (w * NCT + ct) * 1024 + 16 * lane) = d0[ct];
                 m0 = max_abs4(d0[ct], m0);
+                mg = max_abs4(eG_ * d0[ct], mg);
             }
 #pragma unroll
             for (int t = 0; t < NTW; ++t) {
@@ -237,9 +250,11 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
                 }
             }
             m0 = wave_max(m0);
+            mg = wave_max(mg);
             mq = wave_max(mq);
             if (lane == 0) {
                 sMax[16 + w] = m0;
+                sMax[24 + w] = mg;
                 sMax[20 + w] = mq;
             }
         };
@@ -348,8 +363,8 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
             }
     };
     f16x8 kf[NI][NKB];
-    f32x4 eG, eL, be, h0, h1, D0[NCT], DQ[NTW][NCT];
-    float cl_, ks_, d0max, dqmax;
+    f32x4 eG, eL, be, h0, h1, h2, D0[NCT], DQ[NTW][NCT];
+    f32x4 md, mdg, mq;
     auto load_k = [&](int c) {
         const unsigned char *r = krec + (size_t)max(c, 0) * L.key_bytes() + w * NKB * 1024 + fo;
 #pragma unroll
@@ -372,10 +387,10 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         be = *reinterpret_cast<const lds_f4 *>(hd + 512 + 4 * row0);
         h0 = *reinterpret_cast<const lds_f4 *>(hd + 768);
         h1 = *reinterpret_cast<const lds_f4 *>(hd + 784);
-        cl_ = *reinterpret_cast<const lds_f1 *>(hd + 804);
-        ks_ = *reinterpret_cast<const lds_f1 *>(hd + 800);
-        d0max = max4(sMax + 16);
-        dqmax = max4(sMax + 20);
+        h2 = *reinterpret_cast<const lds_f4 *>(hd + 800);
+        md = *reinterpret_cast<const f32x4 *>(sMax + 16);  // their maxima where they are used
+        mdg = *reinterpret_cast<const f32x4 *>(sMax + 24);
+        mq = *reinterpret_cast<const f32x4 *>(sMax + 20);
     };
     int ep = 0;
     if (nchunk > 0) {
@@ -394,7 +409,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         barrier_lds();  // (1)
         const float et_ = h0[1], ek_ = h0[3];
         const int et = __builtin_bit_cast(int, et_), ek = __builtin_bit_cast(int, ek_);
-        const float pmax = max4(sMax), last = h0[0], bm = h1[2], cl = cl_, ksum = ks_;
+        const float pmax = max4(sMax), last = h0[0], bm = h1[2], ksum = h2[0], cl = h2[1], ubound = h2[2], k1 = h2[3];
 
         // ---- 1. dU = M^T dO + e^{G_last - G} K dP'
         f32x4 Z[NCT], Z1[NCT];
@@ -410,7 +425,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
                 Z1[ct] = mma16(kf[0][kb], pl, Z1[ct]);
                 if constexpr (NI == 2) Z1[ct] = mma16(kf[1][kb], ph, Z1[ct]);
             }
-        const int eu = gdr_exp(d0max + cl * pmax);
+        const int eu = gdr_exp(max_abs4(md, 0.f) + cl * pmax);
         float um = 0.f;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
@@ -426,12 +441,13 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         }
         um = wave_max(um);
         if (lane == 0) sMax[4 + w] = um;
+        const float gbound = 64.f * ubound * (max_abs4(mdg, 0.f) + last * k1 * pmax);  // of e^G dX
         load_k(c - 1);
         barrier_lds();  // (2)
 
         // ---- 2. dX = T^T dU, F = b e^G dX
         const float xbound = 64.f * ldexp2(1.f, 14 - et) * max4(sMax + 4);
-        const int ex = gdr_exp(xbound), ef = gdr_exp(bm * xbound);
+        const int ex = gdr_exp(xbound), ef = gdr_exp(bm * fminf(xbound, gbound));
         float fm = 0.f;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
@@ -489,7 +505,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) base[t][ct][i] = fmaf(P[t][ct][i], last, DQ[t][ct][i]);
-        const float qmax = dqmax;
+        const float qmax = max_abs4(mq, 0.f);
         __builtin_amdgcn_sched_barrier(0);
         get(c - 1);  // behind the reads that are waited for
         __builtin_amdgcn_sched_barrier(0);

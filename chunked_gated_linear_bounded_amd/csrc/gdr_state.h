@@ -14,8 +14,11 @@
 // one norm away from a maximum that was published with the operand before: |X| <= max b max|V| +
 // max(b e^G |k|_1) max|P|, |U| <= |T|_inf max|X|, |P'| <= e^{G_last} max|P| + sum(max|k|) max|e^{G_last - G}
 // U|: the maximum is that of the decayed U, so the sum is not decayed again (keys that end before the
-// chunk does would leave it far below P').  A bound that is 2^10 too large still leaves two pieces their
-// 22 bits.
+// chunk does would leave it far below P').  The decayed U has a bound of its own, e^{G_last - G_i} U_i =
+// sum_j (T_ij e^{G_j - G_i}) e^{G_last - G_j} X_j with |e^{G_last - G} X| <= max(b e^{G_last - G} |V|) +
+// e^{G_last} max b max|k|_1 max|P|: where the chunk's last tokens write nothing, all of it
+// is as small as the decay over them, and U's exponent would leave its pieces no bits.  A bound that is
+// 2^10 too large still leaves two pieces their 22 bits.
 //
 // The chain of chunks is what bounds the stage, three exchanges through LDS one behind the other.
 // 65,536 tokens x 32 heads (16 columns a work-group, one work-group a CU): 1.48 us a chunk; the chain's
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     constexpr GdrLayout L{NI, DK, MP};
     constexpr GdrSave SV{NI, DK};
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
-    __shared__ float sMax[20];  // per wave: max |P|, |X|, |e^{G_last-G} U|, |V| of two chunks
+    __shared__ __attribute__((aligned(16))) float sMax[28];  // per wave: max |P|, |X|, |e^{G_last-G} U|; |V| of two chunks; b e^{G_last-G} |V| of two
     __shared__ int sExp[2];     // exponents of P and of U's pieces
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wid & 3;
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
         unsigned char *save = p.save + (((size_t)(b * p.H + h) * p.nslot + slot0) * (p.dv / 16) + slice) * SV.bytes();
         E vn[NCT][4];  // a vector would be put together, and waited for, where it is loaded
         f16x8 kf[NI][NKB], tf[3], qf[SAVE ? 1 : NI][NKB], mf[SAVE ? 1 : NI][2];
-        f32x4 eG;
+        f32x4 eG, el, bl;
         float head;
         int em, eq;
         // a quarter of K's and T's fragments, of the header and of V
@@ -135,6 +138,8 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
 #pragma unroll
             for (int i = 0; i < 3; ++i) tf[i] = *reinterpret_cast<const f16x8 *>(t + L.t_off(0) + (3 * w + i) * 1024 + fo);
             head = *reinterpret_cast<const float *>(t + 4 * (64 * w + lane));
+            el = *reinterpret_cast<const f32x4 *>(t + 256 + 4 * row0);
+            bl = *reinterpret_cast<const f32x4 *>(t + 512 + 4 * row0);
         };
         auto load_v = [&](int c) {
 #pragma unroll
@@ -154,15 +159,23 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
 #pragma unroll
             for (int i = 0; i < 3; ++i) *reinterpret_cast<lds_f16x8 *>(to + S::T + (3 * w + i) * 1024 + fo) = tf[i];
             *reinterpret_cast<__attribute__((address_space(3))) float *>(to + S::HEAD + 4 * (64 * w + lane)) = head;
-            float m = 0.f;
+            __builtin_amdgcn_sched_barrier(0);  // mixed in with what stands before, 2 % slower
+            float m = 0.f, ml = 0.f;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 *reinterpret_cast<lds_e4 *>(to + S::V + ct * NI * 2048 + (w * 64 + lane) * 4 * (int)sizeof(E)) = E4{vn[ct][0], vn[ct][1], vn[ct][2], vn[ct][3]};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf((float)vn[ct][i]));
+                for (int i = 0; i < 4; ++i) {
+                    m = fmaxf(m, fabsf((float)vn[ct][i]));
+                    ml = fmaxf(ml, fabsf(bl[i] * el[i] * (float)vn[ct][i]));
+                }
             }
             m = wave_max(m);
-            if (lane == 0) sMax[12 + 4 * (c & 1) + w] = m;
+            ml = wave_max(ml);
+            if (lane == 0) {
+                sMax[12 + 4 * (c & 1) + w] = m;
+                sMax[20 + 4 * (c & 1) + w] = ml;
+            }
         };
         auto load_q = [&](int c) {
             const unsigned char *r = krec + (size_t)min(c, nchunk - 1) * L.key_bytes() + w * NKB * 1024 + fo;
@@ -313,8 +326,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     };
     f16x8 kf[NI][NKB], tf[2][2];
     E4 v[NCT];
-    f32x4 eG, eL, be, h0, h1;
-    float ks_;
+    f32x4 eG, eL, be, h0, h1, h2, mv, ml;
     // what the other waves have laid out for chunk c
     auto get = [&](int c) {
         const lds_u8 *in = sx + S::IN + (c & 1) * S::INB;
@@ -335,7 +347,9 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
         be = *reinterpret_cast<const lds_f4 *>(hd + 512 + 4 * row0);
         h0 = *reinterpret_cast<const lds_f4 *>(hd + 768);
         h1 = *reinterpret_cast<const lds_f4 *>(hd + 784);
-        ks_ = *reinterpret_cast<const __attribute__((address_space(3))) float *>(hd + 800);
+        h2 = *reinterpret_cast<const lds_f4 *>(hd + 800);
+        mv = *reinterpret_cast<const f32x4 *>(sMax + 12 + 4 * (c & 1));  // their maxima where they are used
+        ml = *reinterpret_cast<const f32x4 *>(sMax + 20 + 4 * (c & 1));
     };
     int ep = 0;
     if (nchunk > 0) {
@@ -349,7 +363,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     }
     for (int c = 0; c < nchunk; ++c) {
         barrier_lds();  // (1)
-        const float pmax = max4(sMax), last = h0[0], kbound = h1[1], bbound = h1[2], tbound = h1[3], ksum = ks_;
+        const float pmax = max4(sMax), last = h0[0], kbound = h1[1], bbound = h1[2], tbound = h1[3], ksum = h2[0], ubound = h2[2], k1 = h2[3];
         const float et_ = h0[1], ek_ = h0[3];
         const int et = __builtin_bit_cast(int, et_), ek = __builtin_bit_cast(int, ek_);
 
@@ -367,7 +381,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
                 Z1[ct] = mma16(kf[0][kb], pl, Z1[ct]);
                 if constexpr (NI == 2) Z1[ct] = mma16(kf[1][kb], ph, Z1[ct]);
             }
-        const int ex = gdr_exp(bbound * max4(sMax + 12 + 4 * (c & 1)) + kbound * pmax);
+        const int ex = gdr_exp(bbound * max_abs4(mv, 0.f) + kbound * pmax);
         f32x4 X[NCT];
         float xm = 0.f;
 #pragma unroll
@@ -387,10 +401,12 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
         }
         xm = wave_max(xm);
         if (lane == 0) sMax[4 + w] = xm;
+        const float lbound = ubound * (max_abs4(ml, 0.f) + last * bbound * k1 * pmax);  // of e^{G_last - G} U
         barrier_lds();  // (2)
 
         // ---- 2. U = T X
-        const int eu = gdr_exp(tbound * max4(sMax + 4));
+        const float umost = tbound * max4(sMax + 4);
+        const int eu = gdr_exp(umost), ee = gdr_exp(fminf(umost, lbound));
         float um = 0.f;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
@@ -411,7 +427,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
             }
             um = max_abs4(EU, um);
             f16x4 hi, lo;
-            split4(EU, pow2f(eu), hi, lo);
+            split4(EU, pow2f(ee), hi, lo);
             lds_u8 *f = sx + S::XE + ((w >> 1) * NCT + ct) * 1024;
             st_half_frag(f, w & 1, g, n, hi);
             st_half_frag(f + 2 * NCT * 1024, w & 1, g, n, lo);
@@ -466,7 +482,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    P[t][ct][i] = fmaf(P[t][ct][i], last, scale_down(z[ct][i] + z1[ct][i], ek + eu));
+                    P[t][ct][i] = fmaf(P[t][ct][i], last, scale_down(z[ct][i] + z1[ct][i], ek + ee));
         }
         ep = gdr_exp(last * pmax + ksum * emax);
         put_p(ep);

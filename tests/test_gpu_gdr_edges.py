@@ -20,12 +20,35 @@ def _gpu():
     kda.lib()
 
 
+def _floor(q, k, v, g, beta, scale):
+    """Besides their 11 or 22 bits the fp16 pieces of a block are multiples of 2^-24, with the block's
+    bound at 2^13 or above: a value is off by up to 2^-37 of that bound.  For out = M U + ... that is
+    2^-37 (max|M| sum_j |U_j| + (|T|_inf max|X|) sum_j |M_ij|), which counts where a token's own decays
+    from its chunk's largest are below 2^-13; the inputs of one sequence, [H,T,dv]."""
+    q, k, v, g, beta = (t.double() for t in (q, k, v, g, beta))
+    r = v.shape[0] // k.shape[0]
+    q, k = q.repeat_interleave(r, 0), k.repeat_interleave(r, 0)
+    P, floor = torch.zeros(v.shape[0], k.shape[-1], v.shape[-1], dtype=torch.float64), torch.zeros_like(v)
+    for t in range(0, v.shape[1], 64):
+        s = slice(t, min(v.shape[1], t + 64))
+        kc, G = k[:, s], g[:, s].cumsum(-1)
+        D = torch.exp((G[:, :, None] - G[:, None]).tril()).tril()
+        T = torch.linalg.inv(torch.eye(G.shape[-1], dtype=torch.float64) + (beta[:, s, None] * (kc @ kc.mT) * D).tril(-1))
+        X = beta[:, s, None] * (v[:, s] - torch.exp(G)[..., None] * (kc @ P))
+        U, M = T @ X, scale * (q[:, s] @ kc.mT) * D
+        most = T.abs().sum(-1).amax(-1) * X.abs().amax((-1, -2))
+        floor[:, s] = 2.0 ** -37 * (M.abs().amax((-1, -2))[:, None, None] * U.abs().sum(1, keepdim=True)
+                                    + most[:, None, None] * M.abs().sum(-1, keepdim=True))
+        P = torch.exp(G[:, -1])[:, None, None] * P + kc.mT @ (torch.exp(G[:, -1:] - G)[..., None] * U)
+    return floor
+
+
 def _check_fwd(x, out, fs, scale, channels=slice(None)):
     """`channels`: the value channels that are compared."""
     ref, S = recurrent(*x, scale)
     for b in range(ref.shape[0]):
         inter, intra, size = chunk_terms(*(t[b] for t in x), scale)
-        bound = out_bound(ref[b], inter, intra, x[0].dtype)
+        bound = out_bound(ref[b], inter, intra, x[0].dtype) + _floor(*(t[b] for t in x), scale)
         check(out[b][..., channels], ref[b][..., channels], bound[..., channels], "out %d" % b)
         check(fs[b][:, channels], S[b][:, channels], state_bound(size)[:, channels], "state %d" % b)
 
@@ -55,11 +78,32 @@ def _tail(sizes, dtype, decay):
     return x, dout
 
 
-@pytest.mark.parametrize("decay", [-0.1, -0.2])
+@pytest.mark.parametrize("decay", [-0.1, -0.2, -0.5, -1.0])
 @pytest.mark.parametrize("sizes", SIZES)
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_keys_end_before_the_chunk(dtype, sizes, decay):
     _fwd_and_grads(*_tail(sizes, dtype, decay), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("T", [64, 150])
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradients_begin_inside_the_chunk(dtype, sizes, T):
+    """The mirror image: no queries, keys and gradients in the first 34 tokens, over which the state
+    decays, so that the start state's gradient is as small as that decay."""
+    B, Hk, H, dv = sizes
+    x = inputs(B, Hk, H, T, 128, dv, dtype, 72, rate=-6.0)
+    x[0][:, :, :34] = 0.0
+    x[1][:, :, :34] = 0.0
+    x[3][:, :, :34] = -0.5
+    gen = torch.Generator().manual_seed(4)
+    dout = torch.randn(B, H, T, dv, generator=gen).to(dtype)
+    dout[:, :, :34] = 0.0
+    S0 = torch.randn(B, H, dv, 128, generator=gen) * 0.5
+    got = kda.gdr_chunk_bwd(*(t.cuda() for t in x), dout.cuda(), scale=128 ** -0.5, initial_state=S0.cuda())
+    ref = reference(x, dout, 128 ** -0.5, S0, None)
+    for name, t in zip(NAMES, ref):
+        compare(got[name], t, dtype, name)
 
 
 @pytest.mark.parametrize("norm", [0.3, 1e-3, 300.0])
