@@ -30,6 +30,15 @@ struct LatentDecodeArgs {
     float *lse;                // [B][H]
     float *part;               // nsplit > 1: [B][nsplit][H][dc], then [B][nsplit][H] log-sum-exps (log2)
     float *part_lse;
+    // 32-key tiles of sequence b, and of each of its parts
+    __device__ __forceinline__ int tiles(int b, int &len, int &per) const {
+        const long long most = (long long)max_pages * page;
+        const int given = lengths[b];
+        len = given < 0 ? 0 : (given > most ? (int)most : given);
+        const int n = (len + 31) / 32;
+        per = (n + nsplit - 1) / nsplit;
+        return n;
+    }
 };
 
 template <int DC, int DR, bool F32, int WS, int NW>
@@ -53,9 +62,8 @@ __global__ __launch_bounds__(64 * NW, F32 ? 1 : 2) void latent_decode_kernel(con
     if (unit >= p.B * p.nsplit) return;
     const int b = unit / p.nsplit, split = unit % p.nsplit;
     const int head = (hg * HT + ht) * 16 + n, hc = head < p.H ? head : p.H - 1;
-    const long long most = (long long)p.max_pages * p.page;
-    const int given = p.lengths[b], len = given < 0 ? 0 : (given > most ? (int)most : given);
-    const int ntile = (len + 31) / 32, per = (ntile + p.nsplit - 1) / p.nsplit;
+    int len, per;
+    const int ntile = p.tiles(b, len, per);
     const int first = split * per, last = min(first + per, ntile);
     const E *cache = reinterpret_cast<const E *>(p.cache);
     const float c = p.scale * kLog2e;
@@ -161,7 +169,8 @@ __global__ __launch_bounds__(64 * NW, F32 ? 1 : 2) void latent_decode_kernel(con
         }
     }
     l = col_sum(l);
-    const float inv = l > 0.f ? 1.f / l : 0.f, lse2 = l > 0.f ? m + lg2(l) : -INFINITY;
+    // no keys: zeros, -inf; a sum that is NaN stays one
+    const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? -INFINITY : m + lg2(l);
     if (head >= p.H) return;
     if (p.nsplit == 1) {
         E *o = reinterpret_cast<E *>(p.out) + ((size_t)b * p.H + head) * DC;
@@ -176,7 +185,7 @@ __global__ __launch_bounds__(64 * NW, F32 ? 1 : 2) void latent_decode_kernel(con
     }
     const size_t row = ((size_t)b * p.nsplit + split) * p.H + head;
     if (g == 0 && ws == 0) p.part_lse[row] = lse2;
-    if (first >= last) return;  // nothing here: its -inf keeps the join from reading the part
+    if (first >= last) return;  // nothing here, and the join reads the parts that have keys
 #pragma unroll
     for (int t = 0; t < NT; t += 2) {
         float *o = p.part + row * DC + 16 * (ws * NT + t) + 8 * g;
@@ -186,26 +195,27 @@ __global__ __launch_bounds__(64 * NW, F32 ? 1 : 2) void latent_decode_kernel(con
     }
 }
 
-// Joins the parts of one (sequence, head): weights 2^(lse_i - max), 4 values a thread.
+// Joins the parts of one (sequence, head): weights 2^(lse_i - max), 4 values a thread.  Every part that
+// has keys counts, so that one whose result is not finite shows.
 template <int DC, typename E>
 __global__ __launch_bounds__(DC / 4) void latent_join_kernel(const LatentDecodeArgs p) {
     const int b = blockIdx.y, h = blockIdx.x;
     const float *e = p.part_lse + (size_t)b * p.nsplit * p.H + h;
+    int len, per;
+    const int ntile = p.tiles(b, len, per), parts = per > 0 ? (ntile + per - 1) / per : 0;
     float m = -INFINITY, sum = 0.f;
-    for (int i = 0; i < p.nsplit; ++i) m = fmaxf(m, e[(size_t)i * p.H]);
+    for (int i = 0; i < parts; ++i) m = fmaxf(m, e[(size_t)i * p.H]);
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < p.nsplit; ++i) {
-        const float x = e[(size_t)i * p.H];
-        if (x == -INFINITY) continue;
-        const float wgt = ex2(x - m);
+    for (int i = 0; i < parts; ++i) {
+        const float x = e[(size_t)i * p.H], wgt = x == -INFINITY ? 0.f : ex2(x - m);
         sum += wgt;
         o += wgt * *reinterpret_cast<const f32x4 *>(p.part + (((size_t)b * p.nsplit + i) * p.H + h) * DC + 4 * threadIdx.x);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     E *to = reinterpret_cast<E *>(p.out) + ((size_t)b * p.H + h) * DC + 4 * threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] = from_f<E>(o[i] * inv);
-    if (threadIdx.x == 0) p.lse[(size_t)b * p.H + h] = sum > 0.f ? (m + lg2(sum)) * kLn2 : -INFINITY;
+    if (threadIdx.x == 0) p.lse[(size_t)b * p.H + h] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
 }
 
 }  // namespace kda

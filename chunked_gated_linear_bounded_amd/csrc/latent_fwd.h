@@ -225,7 +225,7 @@ __global__ __launch_bounds__(256 * NG, F32 ? 1 : 2) void latent_fwd_kernel(const
         l[x] = col_sum(l[x]);
         if (r >= nq) continue;
         const size_t row = ((size_t)(b * p.H + h)) * p.seqs.T + q0 + r;
-        const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;  // a query that sees nothing: zeros, -inf
+        const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];  // a query that sees nothing: zeros, -inf; NaN stays
 #pragma unroll
         for (int t = 0; t < NT; t += 2) {
             f32x4 a = O[t][x], d = O[t + 1][x];
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(256 * NG, F32 ? 1 : 2) void latent_fwd_kernel(const
             }
             Op::store8(reinterpret_cast<E *>(p.out) + row * DN + 16 * t + 8 * g, a, d);
         }
-        if (g == 0) p.lse[row] = l[x] > 0.f ? (m[x] + lg2(l[x])) * kLn2 : -INFINITY;
+        if (g == 0) p.lse[row] = l[x] == 0.f ? -INFINITY : (m[x] + lg2(l[x])) * kLn2;
     }
 }
 

@@ -396,6 +396,8 @@ int kda_latent_attn_bwd(const void *q, const kda_strides *q_strides, const void 
  *  - lengths are clipped to 0 .. max_pages * page and pages to the cache's on the device, so no
  *    content of either leaves the arrays; a sequence of length 0 gives zeros and -inf.  Rows past a
  *    sequence's length are never used, whatever they hold.
+ *    What is not finite in q or in a row inside the length (or a score that overflows) leaves NaN in
+ *    that head's out and lse, however the keys are split.
  *  - dc in {256, 512}, dr = 64; any H up to 65535, any page size.
  * workspace: kda_latent_decode_workspace_bytes(...) bytes (may be 0). */
 size_t kda_latent_decode_workspace_bytes(int B, int H, int page, int max_pages, int dc, int dr, int io_dtype);

@@ -1,0 +1,67 @@
+"""Latent attention on the GPU outside the ordinary: values that are not finite, long histories in many
+parts, views with rows further apart than they are long, large scores.  Bounds as in test_gpu_latent.py."""
+import pytest
+import torch
+
+import chunked_gated_linear_bounded_amd as kda
+from test_gpu_latent import _check, _check_all, inputs, one, split
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    kda.lib()
+
+
+@pytest.mark.parametrize("pages", [1, 5])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_absorbed_shows_what_is_not_finite(dtype, pages):
+    """One part and several (64 rows each): a NaN or a score that overflows, in a query or in one row of
+    the cache inside the length, makes that head's or that sequence's outputs NaN; the others keep theirs."""
+    B, H, dc, page = 5, 16, 256, 64
+    gen = torch.Generator().manual_seed(pages)
+    cache = torch.randn(B * pages, page, dc + 64, generator=gen).to(dtype)
+    q = (torch.randn(B, H, dc + 64, generator=gen) * 0.5).to(dtype)
+    table = torch.arange(B * pages).reshape(B, pages).to(torch.int32)
+    n = pages * page - 3
+    at = 64 * (pages // 2) + 9
+    dirty, dq = cache.clone(), q.clone()
+    dirty[table[1, at // page].long(), at % page, 300] = NAN
+    dirty[table[2, at // page].long(), at % page, 7] = INF
+    dirty[table[3, at // page].long(), at % page] = 1e30
+    dq[3, 0], dq[3, 1:] = 1e30, 1e-30
+    dq[4, 2, 11] = NAN
+    out, lse = kda.latent_decode_step(dq.cuda(), dirty.cuda(), table.cuda(), torch.full((B,), n, dtype=torch.int32, device="cuda"), 0.07,
+                                      dc=dc, return_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.isnan(out[2]).any(-1).all() and not torch.isfinite(out[2, :, 7]).any()
+    assert torch.isnan(out[3, 0]).all() and torch.isnan(lse[3, 0])
+    assert torch.isnan(out[4, 2]).all() and torch.isnan(lse[4, 2])
+    rows = cache.reshape(B, -1, dc + 64)[:, :n]
+    for b, h in ((0, 0), (0, 15), (4, 1), (4, 3)):
+        ref = one(q[b, h][None], rows[b], rows[b][:, :dc], 0.07, dtype)
+        _check(out[b, h][None], *ref["out"], "out %d %d" % (b, h))
+        _check(lse[b, h][None], *ref["lse"], "lse %d %d" % (b, h))
+
+
+@pytest.mark.parametrize("T", [40, 300])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_expanded_shows_what_is_not_finite(dtype, T):
+    """A NaN in a query: NaN in that row's output and log-sum-exp, the other rows as they are."""
+    q, kv, r, _ = inputs((1,), 2, T, T, 64, 32, dtype, T)
+    k, v = split(kv, 64)
+    dirty = q.clone()
+    dirty[0, 1, 17, 3] = NAN
+    out, lse = kda.latent_attn_fwd(dirty.cuda(), *split(kv.cuda(), 64), r.cuda(), return_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0, 1, 17]).all() and torch.isnan(lse[0, 1, 17])
+    for h in range(2):
+        ref = one(q[0, h], torch.cat([k[0, h], r[0]], -1), v[0, h], 96 ** -0.5, dtype)
+        keep = [i for i in range(T) if (h, i) != (1, 17)]
+        _check(out[0, h, keep], *(t[keep] for t in ref["out"]), "out")
+        _check(lse[0, h, keep], *(t[keep] for t in ref["lse"]), "lse")
