@@ -43,9 +43,9 @@ __device__ __forceinline__ void ld8(const float *p, float (&x)[8]) {
     for (int i = 0; i < 4; ++i) { x[i] = a[i]; x[4 + i] = b[i]; }
 }
 
-// maximum over the work-group of x >= 0 (256 threads); red: 4 floats, free again after the next barrier
-__device__ __forceinline__ float block_max4(float x, float *red) {
-    x = wave_max(x);
+// maximum over the work-group (256 threads); red: 4 floats, free again after the next barrier
+__device__ __forceinline__ float block_most(const Most &m, float *red) {
+    const float x = m.wave();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
     __syncthreads();
     return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
     const E *qp = reinterpret_cast<const E *>(p.q) + b * p.sq.b + kh * p.sq.h + (long long)(t0 + trc) * p.sq.t + 8 * g;
     const E *kp = reinterpret_cast<const E *>(p.k) + b * p.sk.b + kh * p.sk.h + (long long)(t0 + trc) * p.sk.t + 8 * g;
     float xk[NKB][8], xq[NKB][8];
-    float mk = 0.f, mq = 0.f;
+    Most mk_, mq;
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
         ld8(kp + 32 * kb, xk[kb]);
@@ -87,13 +87,13 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            mk = fmaxf(mk, fabsf(xk[kb][j]));
-            mq = fmaxf(mq, fabsf(xq[kb][j]));
+        for (int j = 0; j < 8; j += 4) {
+            mk_.add4(f32x4{xk[kb][j], xk[kb][j + 1], xk[kb][j + 2], xk[kb][j + 3]});
+            mq.add4(f32x4{xq[kb][j], xq[kb][j + 1], xq[kb][j + 2], xq[kb][j + 3]});
         }
-    const int ek = gdr_exp(block_max4(mk, red)), eq = gdr_exp(block_max4(mq, red + 4));
+    const int ek = gdr_exp(block_most(mk_, red)), eq = gdr_exp(block_most(mq, red + 4));
     {
-        float k1 = 0.f;
+        float k1 = 0.f, mk = mk_.lane();
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
@@ -189,8 +189,9 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         hd[64 + lane] = ex2((float)(last - G));
         hd[128 + lane] = bv;
         // what the state stage bounds its operands with (GdrLayout)
-        const float ck = wave_max(fabsf(bv) * ex2((float)G) * sK1[lane]), bm = wave_max(fabsf(bv));
-        const float cl = wave_max(ex2((float)(last - G)) * sK1[lane]), k1 = wave_max(sK1[lane]);
+        auto norm = [](float x) { return wave_max(finite_mag(x)); };
+        const float ck = norm(bv * ex2((float)G) * sK1[lane]), bm = norm(bv);
+        const float cl = norm(ex2((float)(last - G)) * sK1[lane]), k1 = norm(sK1[lane]);
         float ks = in ? sKm[lane] : 0.f;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) ks += __shfl_xor(ks, d, 64);
@@ -297,7 +298,8 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         }
     __syncthreads();
     f32x4 ft[2][2], fm[2][2];
-    float mt = 0.f, mm = 0.f, rs = 0.f, rt = 0.f;
+    Most mt, mm, mrs, mrt;
+    float rs = 0.f, rt = 0.f;
     const float gi = sGf[perm_row(w, m)];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -307,8 +309,8 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
             for (int o = 0; o < 2; ++o) {
                 ft[kb][o] = *reinterpret_cast<const f32x4 *>(sT + at + 4 * o);
                 fm[kb][o] = *reinterpret_cast<const f32x4 *>(sA + at + 4 * o);
-                mt = max_abs4(ft[kb][o], mt);
-                mm = max_abs4(fm[kb][o], mm);
+                mt.add4(ft[kb][o]);
+                mm.add4(fm[kb][o]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rs += fabsf(ft[kb][o][i]);
                 const f32x4 gj = *reinterpret_cast<const f32x4 *>(sGf + 32 * kb + 8 * g + 4 * o);
@@ -318,11 +320,13 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         }
     rt += __shfl_xor(rt, 16, 64);
     rt += __shfl_xor(rt, 32, 64);
-    rt = block_max4(rt, red + 20);
+    mrt.add(rt);
+    rt = block_most(mrt, red + 20);
     rs += __shfl_xor(rs, 16, 64);
     rs += __shfl_xor(rs, 32, 64);
-    rs = block_max4(rs, red + 16);
-    const int et = gdr_exp(block_max4(mt, red + 8)), em = gdr_exp(block_max4(mm, red + 12));
+    mrs.add(rs);
+    rs = block_most(mrs, red + 16);
+    const int et = gdr_exp(block_most(mt, red + 8)), em = gdr_exp(block_most(mm, red + 12));
     if (tid == 0) {
         reinterpret_cast<int *>(vrec)[193] = et;
         reinterpret_cast<int *>(vrec)[194] = em;

@@ -130,22 +130,46 @@ __device__ __forceinline__ f32x4 mma16(const f16x8 &a, const f16x8 &b, f32x4 c) 
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// exponent that puts magnitudes up to m at 2^13 .. 2^14, kept where 2^e and 2^-e are normal floats (an
-// infinite or NaN block passes through as such).  A block of zeros has the largest, so that it does not
-// count where several blocks are brought to the smallest of their exponents.
+// The largest finite magnitude.  Exponents and bounds come from a block's finite values; an infinity or a
+// NaN stays one in its pieces and reaches the rows or columns of the products that its element takes part
+// in, and the others keep their digits.  Whole numbers order as the magnitudes whose bits they are:
+// shifted past the sign and moved up by 2^24, a zero is 2^24, and infinities and NaN have gone round the
+// end to below that.  add4 takes four values of one row or column that the products spoil as a whole: an
+// infinity among them leaves all four out, for one instruction more than a maximum of floats.
+struct Most {
+    unsigned t = 1u << 24;
+    __device__ __forceinline__ void add(float x) {
+        const unsigned y = (__builtin_bit_cast(unsigned, x) << 1) + (1u << 24);
+        t = y > t ? y : t;
+    }
+    __device__ __forceinline__ void add4(const f32x4 &x) {
+        add(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+    }
+    __device__ __forceinline__ static float value(unsigned t) { return __builtin_bit_cast(float, (t - (1u << 24)) >> 1); }
+    __device__ __forceinline__ float lane() const { return value(t); }
+    __device__ __forceinline__ float wave() const {
+        return value(__builtin_bit_cast(unsigned, wave_max(__builtin_bit_cast(float, t))));
+    }
+};
+__device__ __forceinline__ float finite_mag(float x) {
+    Most m;
+    m.add(x);
+    return m.lane();
+}
+
+// exponent that puts magnitudes up to m at 2^13 .. 2^14, kept where 2^e and 2^-e are normal floats (m may
+// be a bound that has left float's range).  A block of zeros has the largest, so that it does not count
+// where several blocks are brought to the smallest of their exponents.
 __device__ __forceinline__ int gdr_exp(float m) {
     if (!(m > 0.f)) return 120;
-    const int e = pow2_scale(m);
+    const int e = pow2_scale(fminf(m, 3.402823466e38f));
     return e > 120 ? 120 : (e < -120 ? -120 : e);
 }
 __device__ __forceinline__ float pow2f(int e) { return __builtin_bit_cast(float, (127 + e) << 23); }
 // 2^-(a+b), also where the sum leaves the range of one float's exponent
 __device__ __forceinline__ float scale_down(float x, int e) { return ldexp2(x, -e); }
 
-__device__ __forceinline__ float max_abs4(const f32x4 &x, float m) {
-    m = fmaxf(m, fmaxf(fabsf(x[0]), fabsf(x[1])));
-    return fmaxf(m, fmaxf(fabsf(x[2]), fabsf(x[3])));
-}
+__device__ __forceinline__ float max4(const f32x4 &x) { return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])); }
 
 // ---------------------------------------------------------------- fragments in LDS
 // byte offset of lane (g, m) inside a fragment

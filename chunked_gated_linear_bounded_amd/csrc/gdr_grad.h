@@ -151,7 +151,8 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
         const int tok = perm_row(rw, n), tokc = tok < nrow ? tok : nrow - 1;
         const E *dop = reinterpret_cast<const E *>(p.dout) + b * p.sdo.b + h * p.sdo.h + (long long)(t0 + tokc) * p.sdo.t + 8 * g;
         const E *vp = reinterpret_cast<const E *>(p.v) + b * p.sv.b + h * p.sv.h + (long long)(t0 + tokc) * p.sv.t + 8 * g;
-        float xo[NVB][8], xv[(NVB + 1) / 2][8], mo = 0.f;
+        float xo[NVB][8], xv[(NVB + 1) / 2][8];
+        Most mo;
 #pragma unroll
         for (int kb = 0; kb < NVB; ++kb) {
             ld8(dop + 32 * kb, xo[kb]);
@@ -162,9 +163,9 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (tok >= nrow) xo[kb][j] = 0.f;
-                mo = fmaxf(mo, fabsf(xo[kb][j]));
+                mo.add(xo[kb][j]);
             }
-        const int eo = gdr_exp(wave_max(mo));
+        const int eo = gdr_exp(mo.wave());
         f16x8 of[NI][NVB];
 #pragma unroll
         for (int kb = 0; kb < NVB; ++kb) {
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
                     }
                 }
         }
-        float m1 = 0.f, m2 = 0.f;
+        Most m1_, m2_;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             if (c < nc) {
@@ -229,11 +230,13 @@ __global__ __launch_bounds__(512) void gdr_grad_kernel(const GdrGradArgs p) {
                     dM[c][i] = row >= j ? scale_down(dM[c][i], eo + eu) * dec * p.scale : 0.f;
                     dA[c][i] = row > j ? -scale_down(dA[c][i], ex + eu) * dec : 0.f;
                 }
-                m1 = max_abs4(dM[c], m1);
-                m2 = max_abs4(dA[c], m2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // four rows
+                    m1_.add(dM[c][i]);
+                    m2_.add(dA[c][i]);
+                }
             }
-        m1 = wave_max(m1);
-        m2 = wave_max(m2);
+        const float m1 = m1_.wave(), m2 = m2_.wave();
         if (lane == 0) {
             sRed[0][w] = m1;
             sRed[1][w] = m2;

@@ -129,17 +129,14 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         auto grad_of = [&](int ct, int i) { return 64 * at + row0 + i < len ? to_f(vn[ct][i]) : 0.f; };  // none past the last row
         auto publish_max = [&]() {
             __builtin_amdgcn_sched_barrier(0);  // mixed in with what stands before, 2 % slower
-            float m = 0.f, mh = 0.f;
+            Most mo, mg;
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float d = grad_of(ct, i);
-                    m = fmaxf(m, fabsf(d));
-                    mh = fmaxf(mh, fabsf(eG[i] * d));
-                }
-            m = wave_max(m);
-            mh = wave_max(mh);
+            for (int ct = 0; ct < NCT; ++ct) {
+                const f32x4 d = {grad_of(ct, 0), grad_of(ct, 1), grad_of(ct, 2), grad_of(ct, 3)};
+                mo.add4(d);
+                mg.add4(eG * d);
+            }
+            const float m = mo.wave(), mh = mg.wave();
             if (lane == 0) {
                 sMax[12 + w] = m;
                 sMax[28 + w] = mh;
@@ -213,12 +210,12 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
                 for (int i = 0; i < 4; ++i) d0[ct][i] = scale_down(y[ct][i] + y1[ct][i], em_ + eo);
         };
         auto put_terms = [&]() {  // M^T dO, and Q^T (scale e^G dO)
-            float m0 = 0.f, mg = 0.f, mq = 0.f;
+            Most m0_, mg_, mq_;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 *reinterpret_cast<lds_f4 *>(sx + S::D0 + (w * NCT + ct) * 1024 + 16 * lane) = d0[ct];
-                m0 = max_abs4(d0[ct], m0);
-                mg = max_abs4(eG_ * d0[ct], mg);
+                m0_.add4(d0[ct]);
+                mg_.add4(eG_ * d0[ct]);
             }
 #pragma unroll
             for (int t = 0; t < NTW; ++t) {
@@ -246,12 +243,10 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) a[ct][i] = scale_down(a[ct][i] + a1[ct][i], eq_ + eh);
                     *reinterpret_cast<lds_f4 *>(sx + S::DQ + (tile * NCT + ct) * 1024 + 16 * lane) = a[ct];
-                    mq = max_abs4(a[ct], mq);
+                    mq_.add4(a[ct]);
                 }
             }
-            m0 = wave_max(m0);
-            mg = wave_max(mg);
-            mq = wave_max(mq);
+            const float m0 = m0_.wave(), mg = mg_.wave(), mq = mq_.wave();
             if (lane == 0) {
                 sMax[16 + w] = m0;
                 sMax[24 + w] = mg;
@@ -341,12 +336,12 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
             P[t][ct] = p.dfinal == nullptr ? zero
                            : *reinterpret_cast<const f32x4 *>(p.dfinal + state0 + (size_t)16 * ct * DK + perm_row(NTW * w + t, 4 * g));
     auto max_p = [&]() {
-        float m = 0.f;
+        Most m;
 #pragma unroll
         for (int t = 0; t < NTW; ++t)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) m = max_abs4(P[t][ct], m);
-        return wave_max(m);
+            for (int ct = 0; ct < NCT; ++ct) m.add4(P[t][ct]);
+        return m.wave();
     };
     auto put_p = [&](int e) {
         const float s = pow2f(e);
@@ -425,30 +420,30 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
                 Z1[ct] = mma16(kf[0][kb], pl, Z1[ct]);
                 if constexpr (NI == 2) Z1[ct] = mma16(kf[1][kb], ph, Z1[ct]);
             }
-        const int eu = gdr_exp(max_abs4(md, 0.f) + cl * pmax);
-        float um = 0.f;
+        const int eu = gdr_exp(max4(md) + cl * pmax);
+        Most mu;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 dU;
 #pragma unroll
             for (int i = 0; i < 4; ++i) dU[i] = D0[ct][i] + eL[i] * scale_down(Z[ct][i] + Z1[ct][i], ek + ep);
-            um = max_abs4(dU, um);
+            mu.add4(dU);
             f16x4 hi, lo;
             split4(dU, pow2f(eu), hi, lo);
             lds_u8 *f = sx + S::XU + ((w >> 1) * NCT + ct) * 1024;
             st_half_frag(f, w & 1, g, n, hi);
             st_half_frag(f + 2 * NCT * 1024, w & 1, g, n, lo);
         }
-        um = wave_max(um);
+        const float um = mu.wave();
         if (lane == 0) sMax[4 + w] = um;
-        const float gbound = 64.f * ubound * (max_abs4(mdg, 0.f) + last * k1 * pmax);  // of e^G dX
+        const float gbound = 64.f * ubound * (max4(mdg) + last * k1 * pmax);  // of e^G dX
         load_k(c - 1);
         barrier_lds();  // (2)
 
         // ---- 2. dX = T^T dU, F = b e^G dX
         const float xbound = 64.f * ldexp2(1.f, 14 - et) * max4(sMax + 4);
         const int ex = gdr_exp(xbound), ef = gdr_exp(bm * fminf(xbound, gbound));
-        float fm = 0.f;
+        Most mf;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 z = zero, z1 = zero;
@@ -467,7 +462,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
                 dX[i] = scale_down(z[i] + z1[i], et + eu);
                 F[i] = be[i] * eG[i] * dX[i];
             }
-            fm = max_abs4(F, fm);
+            mf.add4(F);
             f16x4 hi, lo;
             split4(F, pow2f(ef), hi, lo);
             lds_u8 *f = sx + S::XF + ((w >> 1) * NCT + ct) * 1024;
@@ -475,7 +470,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
             st_half_frag(f + 2 * NCT * 1024, w & 1, g, n, lo);
             *reinterpret_cast<lds_f4 *>(sx + S::DX + (w * NCT + ct) * 1024 + 16 * lane) = dX;
         }
-        fm = wave_max(fm);
+        const float fm = mf.wave();
         if (lane == 0) sMax[8 + w] = fm;
         if (threadIdx.x == 0) sExp[1] = ex;
         barrier_lds();  // (3)
@@ -505,7 +500,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) base[t][ct][i] = fmaf(P[t][ct][i], last, DQ[t][ct][i]);
-        const float qmax = max_abs4(mq, 0.f);
+        const float qmax = max4(mq);
         __builtin_amdgcn_sched_barrier(0);
         get(c - 1);  // behind the reads that are waited for
         __builtin_amdgcn_sched_barrier(0);

@@ -160,18 +160,15 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
             for (int i = 0; i < 3; ++i) *reinterpret_cast<lds_f16x8 *>(to + S::T + (3 * w + i) * 1024 + fo) = tf[i];
             *reinterpret_cast<__attribute__((address_space(3))) float *>(to + S::HEAD + 4 * (64 * w + lane)) = head;
             __builtin_amdgcn_sched_barrier(0);  // mixed in with what stands before, 2 % slower
-            float m = 0.f, ml = 0.f;
+            Most mv, mbl;
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
                 *reinterpret_cast<lds_e4 *>(to + S::V + ct * NI * 2048 + (w * 64 + lane) * 4 * (int)sizeof(E)) = E4{vn[ct][0], vn[ct][1], vn[ct][2], vn[ct][3]};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    m = fmaxf(m, fabsf((float)vn[ct][i]));
-                    ml = fmaxf(ml, fabsf(bl[i] * el[i] * (float)vn[ct][i]));
-                }
+                const f32x4 x = {(float)vn[ct][0], (float)vn[ct][1], (float)vn[ct][2], (float)vn[ct][3]};
+                mv.add4(x);
+                mbl.add4(bl * el * x);
             }
-            m = wave_max(m);
-            ml = wave_max(ml);
+            const float m = mv.wave(), ml = mbl.wave();
             if (lane == 0) {
                 sMax[12 + 4 * (c & 1) + w] = m;
                 sMax[20 + 4 * (c & 1) + w] = ml;
@@ -303,12 +300,12 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
             P[t][ct] = p.init_state == nullptr ? zero
                            : *reinterpret_cast<const f32x4 *>(p.init_state + state0 + (size_t)16 * ct * DK + perm_row(NTW * w + t, 4 * g));
     auto max_p = [&]() {
-        float m = 0.f;
+        Most m;
 #pragma unroll
         for (int t = 0; t < NTW; ++t)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) m = max_abs4(P[t][ct], m);
-        return wave_max(m);
+            for (int ct = 0; ct < NCT; ++ct) m.add4(P[t][ct]);
+        return m.wave();
     };
     auto put_p = [&](int e) {
         const float s = pow2f(e);
@@ -381,15 +378,15 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
                 Z1[ct] = mma16(kf[0][kb], pl, Z1[ct]);
                 if constexpr (NI == 2) Z1[ct] = mma16(kf[1][kb], ph, Z1[ct]);
             }
-        const int ex = gdr_exp(bbound * max_abs4(mv, 0.f) + kbound * pmax);
+        const int ex = gdr_exp(bbound * max4(mv) + kbound * pmax);
         f32x4 X[NCT];
-        float xm = 0.f;
+        Most mx;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 X[ct][i] = be[i] * ((float)v[ct][i] - eG[i] * scale_down(Z[ct][i] + Z1[ct][i], ek + ep));
-            xm = max_abs4(X[ct], xm);
+            mx.add4(X[ct]);
         }
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
@@ -399,15 +396,15 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
             st_half_frag(f, w & 1, g, n, hi);
             st_half_frag(f + 2 * NCT * 1024, w & 1, g, n, lo);
         }
-        xm = wave_max(xm);
+        const float xm = mx.wave();
         if (lane == 0) sMax[4 + w] = xm;
-        const float lbound = ubound * (max_abs4(ml, 0.f) + last * bbound * k1 * pmax);  // of e^{G_last - G} U
+        const float lbound = ubound * (max4(ml) + last * bbound * k1 * pmax);  // of e^{G_last - G} U
         barrier_lds();  // (2)
 
         // ---- 2. U = T X
         const float umost = tbound * max4(sMax + 4);
         const int eu = gdr_exp(umost), ee = gdr_exp(fminf(umost, lbound));
-        float um = 0.f;
+        Most mu;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 z = zero, z1 = zero;
@@ -425,7 +422,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
                 U[i] = scale_down(z[i] + z1[i], et + ex);
                 EU[i] = U[i] * eL[i];
             }
-            um = max_abs4(EU, um);
+            mu.add4(EU);
             f16x4 hi, lo;
             split4(EU, pow2f(ee), hi, lo);
             lds_u8 *f = sx + S::XE + ((w >> 1) * NCT + ct) * 1024;
@@ -437,7 +434,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
             st_half_frag(f, w & 1, g, n, hi);
             if constexpr (NI == 2) st_half_frag(f + 2 * NCT * 1024, w & 1, g, n, lo);
         }
-        um = wave_max(um);
+        const float um = mu.wave();
         if (lane == 0) sMax[8 + w] = um;
         if (threadIdx.x == 0) sExp[1] = eu;
         barrier_lds();  // (3)

@@ -309,6 +309,8 @@ int kda_decode_step(const void *q, const void *k, const void *v, const void *a, 
  *  - out : [B][H][T][dv] contiguous.  initial_state (nullable) and final_state (nullable):
  *    [N][H][dv][dk] float32, they may be the same array.
  *  - dk, dv in {64, 128}; H a multiple of Hk; H and (without cu_seqlens) N at most 65535.
+ *  - An infinity or a NaN in q reaches its token's outputs only; in v its channel, of k, g or beta its
+ *    head, of the outputs from its chunk of 64 tokens on and of the state.
  * Operands of the matrix products that feed the state keep 22 bits, so the float32 final state is
  * accurate to about 1e-6 of its norm also with bf16 inputs (and to 2^-37 of the largest value that the
  * last chunk of 64 tokens wrote, where decays inside the chunk leave the state smaller than that). */

@@ -129,3 +129,43 @@ def test_zero_channels(dtype, sizes):
         t *= 2.0 ** -20
         t[..., -32:] = 0.0
     _fwd_and_grads(x, dout, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_bad_value_stays_in_its_channel(dtype, sizes, bad):
+    """An infinity or NaN in one channel of v reaches that channel of the outputs and of the state, from
+    its chunk on, and no other; one in dout that channel of dv and of the start state's gradient."""
+    B, Hk, H, dv = sizes
+    x = list(inputs(B, Hk, H, 150, 128, dv, dtype, 101))
+    x[2] *= 8.0
+    dout = (8.0 * torch.randn(B, H, 150, dv, generator=torch.Generator().manual_seed(6))).to(dtype)
+    rest = [c for c in range(dv) if c != 5]
+    d = [t.cuda() for t in x]
+    d[2] = d[2].clone()
+    d[2][:, :, 70, 5] = bad
+    out, fs = kda.gdr_chunk_fwd(*d, return_final_state=True)
+    _check_fwd(x, out, fs, 1.0, rest)
+    assert torch.isfinite(out[:, :, :64]).all() and not torch.isfinite(out[:, :, 70:, 5]).any()
+    assert not torch.isfinite(fs[:, :, 5]).all(-1).any()
+    ref = reference(x, dout, 1.0, torch.zeros(B, H, dv, 128), None)
+    dirty = dout.cuda()
+    dirty[:, :, 70, 5] = bad
+    got = kda.gdr_chunk_bwd(*(t.cuda() for t in x), dirty)
+    compare(got["dv"][..., rest], ref[2][..., rest], dtype, "dv")
+    compare(got["dinitial_state"][:, :, rest], ref[5][:, :, rest], dtype, "dinitial_state")
+    assert not torch.isfinite(got["dv"][:, :, 70, 5]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_bad_query_stays_in_its_row(dtype):
+    x = list(inputs(1, 1, 2, 150, 128, 64, dtype, 111))
+    x[0] *= 64.0
+    d = [t.cuda() for t in x]
+    d[0] = d[0].clone()
+    d[0][:, :, 70, 3] = float("inf")
+    out, fs = kda.gdr_chunk_fwd(*d, return_final_state=True)
+    assert not torch.isfinite(out[:, :, 70]).any()
+    out[:, :, 70] = recurrent(*x, 1.0)[0][:, :, 70].to(out)
+    _check_fwd(x, out, fs, 1.0)
