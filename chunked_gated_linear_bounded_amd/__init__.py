@@ -36,6 +36,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -459,6 +460,7 @@ class KdaChunkFunction(torch.autograd.Function):
         return out, fs
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout, dfinal):
         q, k, v, a, beta = ctx.saved_tensors
         dout = torch.zeros_like(q[..., :1].expand(*q.shape[:-1], v.shape[-1])) if dout is None else dout

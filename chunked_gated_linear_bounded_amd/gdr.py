@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import KDA_OK, KdaError, _DTYPES, _empty, _on_device, _stream_of, lib
 
@@ -183,6 +184,7 @@ class GdrChunkFunction(torch.autograd.Function):
         return out, fs
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout, dfinal):
         q, k, v, g, beta, s0, cu = ctx.saved_tensors
         d = _bwd(q, k, v, g, beta, dout.contiguous(), cu, ctx.scale, s0, dfinal.contiguous(), None, None,

@@ -7,6 +7,7 @@ and v = kv[..., dn:].transpose(1, 2) are taken as they are."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import KDA_OK, KdaError, _DTYPES, _empty, _on_device, _stream_of, lib
 from .gdr import _S3, _plain, _view, _workspace
@@ -139,6 +140,7 @@ class LatentAttnFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         *x, out, lse, cu_q, cu_k = ctx.saved_tensors
         g = _bwd(*x, out, lse, dout.contiguous(), cu_q, cu_k, ctx.scale, None, None)

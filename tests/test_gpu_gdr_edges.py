@@ -169,3 +169,13 @@ def test_bad_query_stays_in_its_row(dtype):
     assert not torch.isfinite(out[:, :, 70]).any()
     out[:, :, 70] = recurrent(*x, 1.0)[0][:, :, 70].to(out)
     _check_fwd(x, out, fs, 1.0)
+
+
+def test_second_derivatives_are_refused():
+    """The gradients carry no graph of their own: a penalty on one is an error, not a term left out."""
+    x = [t.cuda().requires_grad_() for t in inputs(1, 1, 1, 64, 64, 64, F32, 121)]
+    a = [t.cuda().requires_grad_() for t in inputs(1, 1, 1, 64, 64, 64, F32, 122)]
+    for leaf, out in ((x, kda.GdrChunkFunction.apply(*x)[0]), (a, kda.KdaChunkFunction.apply(*a[:3], a[0] * 1.0, a[4])[0])):
+        first = torch.autograd.grad(out.square().sum(), leaf[2], create_graph=True)[0]
+        with pytest.raises(RuntimeError):
+            (first.square().sum() + leaf[0].sum()).backward()

@@ -65,3 +65,11 @@ def test_expanded_shows_what_is_not_finite(dtype, T):
         keep = [i for i in range(T) if (h, i) != (1, 17)]
         _check(out[0, h, keep], *(t[keep] for t in ref["out"]), "out")
         _check(lse[0, h, keep], *(t[keep] for t in ref["lse"]), "lse")
+
+
+def test_second_derivatives_are_refused():
+    q, kv, r, _ = inputs((1,), 1, 40, 40, 64, 32, F32, 3)
+    leaf = [t.cuda().requires_grad_() for t in (q, *(t.contiguous() for t in split(kv, 64)), r)]
+    first = torch.autograd.grad(kda.LatentAttnFunction.apply(*leaf).square().sum(), leaf[2], create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        (first.square().sum() + leaf[0].sum()).backward()
