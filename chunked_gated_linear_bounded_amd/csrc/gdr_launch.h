@@ -48,4 +48,13 @@ inline bool gdr_two_tiles(const GdrLaunch &p) {
     return (long long)p.N * p.H * (p.dv / 16) > places;
 }
 
+// Whether the launches of a call stay below 2^32 work-items in x, which is as far as a launch goes.
+inline bool gdr_grids_fit(const GdrLaunch &p, bool backward) {
+    const long long most = 4294967295LL, packed = p.cu != nullptr, units = ((long long)p.N * p.H + 7) / 8 * 8;
+    const long long slots = packed ? (long long)p.T / 64 + p.N : ((long long)p.T + 63) / 64;
+    const int columns = !gdr_two_tiles(p) || (backward && p.fp32 && p.dk == 128) ? 16 : 32;
+    return slots * (backward ? 512 : 256) <= most && units * (p.dv / columns) * 512 <= most;
+}
+inline bool gdr_decode_grid_fits(const GdrLaunch &p) { return (long long)p.B * p.H * (p.dv / 16) * 256 <= 4294967295LL; }
+
 }  // namespace kda

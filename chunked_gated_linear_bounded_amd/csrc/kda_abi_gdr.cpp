@@ -10,15 +10,24 @@ namespace {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-int check_shape(bool packed, int N, int Hk, int H, int T, int dk, int dv, int io) {
+kda::GdrLaunch shape(bool packed, int N, int Hk, int H, int T, int dk, int dv, int io) {
+    kda::GdrLaunch p{};
+    static const int somewhere = 0;  // sizes go by packed or not; launches put the caller's pointer here
+    p.cu = packed ? &somewhere : nullptr;
+    p.N = N; p.B = packed ? 1 : N; p.Hk = Hk; p.H = H; p.T = T; p.dk = dk; p.dv = dv;
+    p.fp32 = io == KDA_FP32;
+    return p;
+}
+
+int check_shape(bool backward, bool packed, int N, int Hk, int H, int T, int dk, int dv, int io) {
     if (io != KDA_BF16 && io != KDA_FP32) return KDA_ERR_DTYPE;
     if (N < 1 || Hk < 1 || H < 1 || T < 0 || H % Hk != 0 || H > 65535) return KDA_ERR_SHAPE;
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return KDA_ERR_SHAPE;
     if (!packed && N > 65535) return KDA_ERR_SHAPE;                          // grid z of the chunk stage
-    if ((long long)N * H * (dv / 16) + 64 > 2147483647LL) return KDA_ERR_SHAPE;  // grid of the state stage
+    if ((long long)N * H * (dv / 16) + 64 > 2147483647LL) return KDA_ERR_SHAPE;  // units in 32 bits
     if ((long long)T / 64 + N + 1 > 2147483647LL || T > 2147483647 - 128) return KDA_ERR_SHAPE;
     if ((packed ? 1.0 : (double)N) * H * (double)T * (dk > dv ? dk : dv) >= 1099511627776.0) return KDA_ERR_SHAPE;  // 2^40
-    return KDA_OK;
+    return kda::gdr_grids_fit(shape(packed, N, Hk, H, T, dk, dv, io), backward) ? KDA_OK : KDA_ERR_SHAPE;
 }
 
 // strides of a tensor whose last dimension has `inner` elements; unit: elements that a row's start
@@ -34,15 +43,6 @@ bool set_strides(long long (&s)[3], const kda_strides *given, long long H, long 
     s[1] = given->h;
     s[2] = given->t;
     return s[0] % unit == 0 && s[1] % unit == 0 && s[2] % unit == 0;
-}
-
-kda::GdrLaunch shape(bool packed, int N, int Hk, int H, int T, int dk, int dv, int io) {
-    kda::GdrLaunch p{};
-    static const int somewhere = 0;  // sizes go by packed or not; launches put the caller's pointer here
-    p.cu = packed ? &somewhere : nullptr;
-    p.N = N; p.B = packed ? 1 : N; p.Hk = Hk; p.H = H; p.T = T; p.dk = dk; p.dv = dv;
-    p.fp32 = io == KDA_FP32;
-    return p;
 }
 
 int inputs(kda::GdrLaunch &p, const void *q, const kda_strides *qs, const void *k, const kda_strides *ks, const void *v,
@@ -73,7 +73,7 @@ int inputs(kda::GdrLaunch &p, const void *q, const kda_strides *qs, const void *
 extern "C" {
 
 size_t kda_gdr_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype) {
-    if (check_shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype) != KDA_OK) return 0;
+    if (check_shape(backward != 0, packed != 0, N, Hk, H, T, dk, dv, io_dtype) != KDA_OK) return 0;
     const kda::GdrLaunch p = shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype);
     return backward ? kda::gdr_bwd_bytes(p) : kda::gdr_fwd_bytes(p);
 }
@@ -83,7 +83,7 @@ int kda_gdr_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k
                       const void *beta, const kda_strides *beta_strides, const int *cu_seqlens, int N, int Hk,
                       int H, int T, int dk, int dv, int io_dtype, float scale, const float *initial_state,
                       void *out, float *final_state, void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    int st = check_shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
+    int st = check_shape(false, cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
     if (st != KDA_OK) return st;
     kda::GdrLaunch p = shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
     if (T > 0 && !out) return KDA_ERR_NULL;
@@ -104,7 +104,7 @@ int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k
                       int dv, int io_dtype, float scale, const float *initial_state, const float *dfinal_state,
                       void *dq, void *dk_out, void *dv_out, void *dg, void *dbeta, float *dinitial_state,
                       void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    int st = check_shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
+    int st = check_shape(true, cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
     if (st != KDA_OK) return st;
     kda::GdrLaunch p = shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
     if (T > 0 && (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta)) return KDA_ERR_NULL;
@@ -126,17 +126,18 @@ int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k
 int kda_gdr_decode_step(const void *q, const void *k, const void *v, const void *g, const void *beta, int B, int Hk,
                         int H, int dk, int dv, int io_dtype, float scale, float *state, void *out,
                         hipStream_t stream) {
-    const int st = check_shape(true, B, Hk, H, 1, dk, dv, io_dtype);
-    if (st != KDA_OK) return st;
+    if (io_dtype != KDA_BF16 && io_dtype != KDA_FP32) return KDA_ERR_DTYPE;
+    if (B < 1 || Hk < 1 || H < 1 || H % Hk != 0 || H > 65535 || (dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return KDA_ERR_SHAPE;
+    kda::GdrLaunch p{};
+    p.B = B; p.Hk = Hk; p.H = H; p.T = 1; p.dk = dk; p.dv = dv;
+    if (!kda::gdr_decode_grid_fits(p)) return KDA_ERR_SHAPE;
     if (!isfinite(scale)) return KDA_ERR_SCALE;
     if (!q || !k || !v || !g || !beta || !state || !out) return KDA_ERR_NULL;
     const int esz = io_dtype == KDA_FP32 ? 4 : 2;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, esz) || !aligned(beta, esz) ||
         !aligned(state, 16) || !aligned(out, 16))
         return KDA_ERR_ALIGN;
-    kda::GdrLaunch p{};
     p.q = q; p.k = k; p.v = v; p.g = g; p.beta = beta;
-    p.B = B; p.Hk = Hk; p.H = H; p.T = 1; p.dk = dk; p.dv = dv;
     p.fp32 = io_dtype == KDA_FP32;
     p.scale = scale;
     p.state = state;

@@ -11,16 +11,21 @@ namespace {
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 bool bad_scale(float s) { return !isfinite(s) || !(s > 0.f); }
 
-int check_shape(bool packed, int N, int H, int T, int S, int dn, int dr, int io) {
+kda::LatentLaunch shape(bool packed, int N, int H, int T, int S, int dn, int dr, int io) {
+    kda::LatentLaunch p{};
+    p.N = N; p.B = packed ? 1 : N; p.H = H; p.T = T; p.S = S; p.dn = dn; p.dr = dr;
+    p.fp32 = io == KDA_FP32;
+    p.packed = packed;
+    return p;
+}
+
+int check_shape(bool backward, bool packed, int N, int H, int T, int S, int dn, int dr, int io) {
     if (io != KDA_BF16 && io != KDA_FP32) return KDA_ERR_DTYPE;
     if (N < 1 || H < 1 || T < 0 || S < 0 || H > 65535) return KDA_ERR_SHAPE;
     if ((dn != 64 && dn != 128) || (dr != 32 && dr != 64)) return KDA_ERR_SHAPE;
     if (!packed && N > 65535) return KDA_ERR_SHAPE;
     if (T > 2147483647 - 256 || S > 2147483647 - 256) return KDA_ERR_SHAPE;
-    // grids: one work-group per 64 or 128 rows of either side and head
-    const double tiles = (double)(T > S ? T : S) / 64 + N + 1, units = (packed ? 1.0 : (double)N) * H + 8;
-    if (tiles * units > 2147483647.0) return KDA_ERR_SHAPE;
-    return KDA_OK;
+    return kda::latent_grids_fit(shape(packed, N, H, T, S, dn, dr, io), backward) ? KDA_OK : KDA_ERR_SHAPE;
 }
 
 // b, h, t strides of a tensor of H heads (0: none) and T rows of `inner` elements
@@ -42,13 +47,6 @@ bool far_rows(const long long (&s)[3], long long rows, bool fp32) {
     return rows > 1 && (s[2] < 0 || s[2] > 2147483647LL / 64 / (fp32 ? 4 : 2));
 }
 
-kda::LatentLaunch shape(bool packed, int N, int H, int T, int S, int dn, int dr, int io) {
-    kda::LatentLaunch p{};
-    p.N = N; p.B = packed ? 1 : N; p.H = H; p.T = T; p.S = S; p.dn = dn; p.dr = dr;
-    p.fp32 = io == KDA_FP32;
-    return p;
-}
-
 int inputs(kda::LatentLaunch &p, const void *q, const kda_strides *qs, const void *k, const kda_strides *ks, const void *v,
            const kda_strides *vs, const void *kr, const kda_strides *krs, const int *cu_q, const int *cu_k, float scale) {
     const int unit = p.fp32 ? 4 : 8;
@@ -68,18 +66,19 @@ int inputs(kda::LatentLaunch &p, const void *q, const kda_strides *qs, const voi
     return KDA_OK;
 }
 
-int check_decode(int B, int H, int page, int max_pages, int dc, int dr, int io) {
-    if (io != KDA_BF16 && io != KDA_FP32) return KDA_ERR_DTYPE;
-    if (B < 1 || B > 65535 || H < 1 || H > 65535 || page < 1 || max_pages < 1) return KDA_ERR_SHAPE;
-    if ((dc != 256 && dc != 512) || dr != 64) return KDA_ERR_SHAPE;
-    if ((long long)max_pages * page > 2147483647LL - 128) return KDA_ERR_SHAPE;
-    return KDA_OK;
-}
 kda::LatentLaunch decode_shape(int B, int H, int page, int max_pages, int dc, int io) {
     kda::LatentLaunch p{};
     p.B = B; p.H = H; p.page = page; p.max_pages = max_pages; p.dc = dc;
     p.fp32 = io == KDA_FP32;
     return p;
+}
+
+int check_decode(int B, int H, int page, int max_pages, int dc, int dr, int io) {
+    if (io != KDA_BF16 && io != KDA_FP32) return KDA_ERR_DTYPE;
+    if (B < 1 || B > 65535 || H < 1 || H > 65535 || page < 1 || max_pages < 1) return KDA_ERR_SHAPE;
+    if ((dc != 256 && dc != 512) || dr != 64) return KDA_ERR_SHAPE;
+    if ((long long)max_pages * page > 2147483647LL - 128) return KDA_ERR_SHAPE;
+    return kda::latent_decode_grid_fits(decode_shape(B, H, page, max_pages, dc, io)) ? KDA_OK : KDA_ERR_SHAPE;
 }
 
 }  // namespace
@@ -92,7 +91,7 @@ int kda_latent_attn_fwd(const void *q, const kda_strides *q_strides, const void 
                         int H, int T, int S, int dn, int dr, int io_dtype, float scale, void *out, float *lse,
                         hipStream_t stream) {
     const bool packed = cu_seqlens_q != nullptr;
-    int st = check_shape(packed, N, H, T, S, dn, dr, io_dtype);
+    int st = check_shape(false, packed, N, H, T, S, dn, dr, io_dtype);
     if (st != KDA_OK) return st;
     kda::LatentLaunch p = shape(packed, N, H, T, S, dn, dr, io_dtype);
     if (T > 0 && (!out || !lse)) return KDA_ERR_NULL;
@@ -106,7 +105,7 @@ int kda_latent_attn_fwd(const void *q, const kda_strides *q_strides, const void 
 }
 
 size_t kda_latent_attn_bwd_workspace_bytes(int packed, int N, int H, int T, int S, int dn, int dr, int io_dtype) {
-    if (check_shape(packed != 0, N, H, T, S, dn, dr, io_dtype) != KDA_OK) return 0;
+    if (check_shape(true, packed != 0, N, H, T, S, dn, dr, io_dtype) != KDA_OK) return 0;
     return kda::latent_bwd_bytes(shape(packed != 0, N, H, T, S, dn, dr, io_dtype));
 }
 
@@ -117,7 +116,7 @@ int kda_latent_attn_bwd(const void *q, const kda_strides *q_strides, const void 
                         int H, int T, int S, int dn, int dr, int io_dtype, float scale, void *dq, void *dk_out,
                         void *dv_out, void *dk_rope, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     const bool packed = cu_seqlens_q != nullptr;
-    int st = check_shape(packed, N, H, T, S, dn, dr, io_dtype);
+    int st = check_shape(true, packed, N, H, T, S, dn, dr, io_dtype);
     if (st != KDA_OK) return st;
     kda::LatentLaunch p = shape(packed, N, H, T, S, dn, dr, io_dtype);
     if ((T > 0 && (!out || !lse || !dout || !dq)) || (S > 0 && (!dk_out || !dv_out || !dk_rope))) return KDA_ERR_NULL;

@@ -21,6 +21,12 @@ size_t latent_decode_bytes(const LatentLaunch &p) {
     return n == 1 ? 0 : (size_t)p.B * n * p.H * (p.dc + 1) * 4;
 }
 
+// a group of 64 heads is eight waves
+bool latent_decode_grid_fits(const LatentLaunch &p) {
+    const long long groups = ((long long)p.B * splits(p) + 7) / 8 * 8 * head_groups(p);
+    return groups <= 4294967295LL / (heads_per_group(p) == 64 ? 512 : 256);
+}
+
 template <int DC, bool F32, int WS, int NW>
 static hipError_t run(const LatentLaunch &p) {
     LatentDecodeArgs a{p.q, p.cache, p.table, p.lengths, p.B, p.H, p.pages, p.page, p.max_pages, splits(p), head_groups(p),

@@ -308,7 +308,9 @@ int kda_decode_step(const void *q, const void *k, const void *v, const void *a, 
  *    document covers are not written.
  *  - out : [B][H][T][dv] contiguous.  initial_state (nullable) and final_state (nullable):
  *    [N][H][dv][dk] float32, they may be the same array.
- *  - dk, dv in {64, 128}; H a multiple of Hk; H and (without cu_seqlens) N at most 65535.
+ *  - dk, dv in {64, 128}; H a multiple of Hk; H and (without cu_seqlens) N at most 65535, and launches
+ *    below 2^32 work-items (KDA_ERR_SHAPE): 2^23 / (dv / 32) sequences and heads (backward of float32 at
+ *    dk = 128: 2^23 / (dv / 16)) and 2^30 tokens (backward: 2^29) of one batch entry or stream.
  *  - An infinity or a NaN in q reaches its token's outputs only; in v its channel, of k, g or beta its
  *    head, of the outputs from its chunk of 64 tokens on and of the state.
  * Operands of the matrix products that feed the state keep 22 bits, so the float32 final state is
@@ -369,7 +371,9 @@ int kda_gdr_decode_step(const void *q, const void *k, const void *v, const void 
  *  - out : [B][H][T][dn] in io_dtype, lse : [B][H][T] float32 (natural log), contiguous.
  *  - dn in {64, 128} (v has dn channels too), dr in {32, 64}; scale > 0; finite inputs at every
  *    token of a sequence (what lies outside the sequences is never used).
- *  - H and (without boundaries) N at most 65535. */
+ *  - H and (without boundaries) N at most 65535, and launches below 2^32 work-items (KDA_ERR_SHAPE):
+ *    256 in the forward, 512 in the backward, per head and 128 queries (backward: or keys; float32: 64)
+ *    begun by a sequence. */
 int kda_latent_attn_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
                         const void *v, const kda_strides *v_strides, const void *k_rope,
                         const kda_strides *k_rope_strides, const int *cu_seqlens_q, const int *cu_seqlens_k, int N,
@@ -400,7 +404,7 @@ int kda_latent_attn_bwd(const void *q, const kda_strides *q_strides, const void 
  *    sequence's length are never used, whatever they hold.
  *    What is not finite in q or in a row inside the length (or a score that overflows) leaves NaN in
  *    that head's out and lse, however the keys are split.
- *  - dc in {256, 512}, dr = 64; any H up to 65535, any page size.
+ *  - dc in {256, 512}, dr = 64; any B and H up to 65535 (a launch below 2^32 work-items), any page size.
  * workspace: kda_latent_decode_workspace_bytes(...) bytes (may be 0). */
 size_t kda_latent_decode_workspace_bytes(int B, int H, int page, int max_pages, int dc, int dr, int io_dtype);
 int kda_latent_decode_step(const void *q, const void *cache, const int *block_table, const int *lengths, int B, int H,
