@@ -30,18 +30,18 @@ int check_shape(bool backward, bool packed, int N, int Hk, int H, int T, int dk,
     return kda::gdr_grids_fit(shape(packed, N, Hk, H, T, dk, dv, io), backward) ? KDA_OK : KDA_ERR_SHAPE;
 }
 
-// strides of a tensor whose last dimension has `inner` elements; unit: elements that a row's start
-// must be a multiple of (1: any)
-bool set_strides(long long (&s)[3], const kda_strides *given, long long H, long long T, long long inner, int unit) {
+// strides of a tensor of B x H x T rows of `inner` elements; unit: elements that a row's start must be a
+// multiple of (1: any).  A dimension of one has none.
+bool set_strides(long long (&s)[3], const kda_strides *given, int B, long long H, long long T, long long inner, int unit) {
     if (given == nullptr) {
         s[2] = inner;
         s[1] = T * inner;
         s[0] = H * T * inner;
         return true;
     }
-    s[0] = given->b;
-    s[1] = given->h;
-    s[2] = given->t;
+    s[0] = B > 1 ? given->b : 0;
+    s[1] = H > 1 ? given->h : 0;
+    s[2] = T > 1 ? given->t : 0;
     return s[0] % unit == 0 && s[1] % unit == 0 && s[2] % unit == 0;
 }
 
@@ -54,9 +54,9 @@ int inputs(kda::GdrLaunch &p, const void *q, const kda_strides *qs, const void *
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(g, esz) || !aligned(beta, esz) ||
         !aligned(cu, 4) || !aligned(init, 16))
         return KDA_ERR_ALIGN;
-    if (!set_strides(p.sq, qs, p.Hk, p.T, p.dk, unit) || !set_strides(p.sk, ks, p.Hk, p.T, p.dk, unit) ||
-        !set_strides(p.sv, vs, p.H, p.T, p.dv, unit) || !set_strides(p.sg, gs, p.H, p.T, 1, 1) ||
-        !set_strides(p.sb, bs, p.H, p.T, 1, 1))
+    if (!set_strides(p.sq, qs, p.B, p.Hk, p.T, p.dk, unit) || !set_strides(p.sk, ks, p.B, p.Hk, p.T, p.dk, unit) ||
+        !set_strides(p.sv, vs, p.B, p.H, p.T, p.dv, unit) || !set_strides(p.sg, gs, p.B, p.H, p.T, 1, 1) ||
+        !set_strides(p.sb, bs, p.B, p.H, p.T, 1, 1))
         return KDA_ERR_ALIGN;
     if (need > 0 && (!workspace || given < need)) return KDA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return KDA_ERR_ALIGN;
@@ -110,7 +110,7 @@ int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k
     if (T > 0 && (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta)) return KDA_ERR_NULL;
     if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk_out, 16) || !aligned(dv_out, 16) || !aligned(dg, 4) ||
         !aligned(dbeta, 4) || !aligned(dfinal_state, 16) || !aligned(dinitial_state, 16) ||
-        !set_strides(p.sdo, dout_strides, H, T, dv, p.fp32 ? 4 : 8))
+        !set_strides(p.sdo, dout_strides, p.B, H, T, dv, p.fp32 ? 4 : 8))
         return KDA_ERR_ALIGN;
     st = inputs(p, q, q_strides, k, k_strides, v, v_strides, g, g_strides, beta, beta_strides, cu_seqlens, scale,
                 initial_state, workspace, workspace_bytes, kda::gdr_bwd_bytes(p));

@@ -28,17 +28,18 @@ int check_shape(bool backward, bool packed, int N, int H, int T, int S, int dn, 
     return kda::latent_grids_fit(shape(packed, N, H, T, S, dn, dr, io), backward) ? KDA_OK : KDA_ERR_SHAPE;
 }
 
-// b, h, t strides of a tensor of H heads (0: none) and T rows of `inner` elements
-bool set_strides(long long (&s)[3], const kda_strides *given, long long H, long long T, long long inner, int unit) {
+// b, h, t strides of a tensor of B entries, H heads (0: none) and T rows of `inner` elements; a dimension
+// of one has none
+bool set_strides(long long (&s)[3], const kda_strides *given, int B, long long H, long long T, long long inner, int unit) {
     if (given == nullptr) {
         s[2] = inner;
         s[1] = H > 0 ? T * inner : 0;
         s[0] = (H > 0 ? H : 1) * T * inner;
         return true;
     }
-    s[0] = given->b;
-    s[1] = H > 0 ? given->h : 0;
-    s[2] = given->t;
+    s[0] = B > 1 ? given->b : 0;
+    s[1] = H > 1 ? given->h : 0;
+    s[2] = T > 1 ? given->t : 0;
     return s[0] % unit == 0 && s[1] % unit == 0 && s[2] % unit == 0;
 }
 
@@ -55,8 +56,8 @@ int inputs(kda::LatentLaunch &p, const void *q, const kda_strides *qs, const voi
     if ((p.T > 0 && !q) || (p.S > 0 && (!k || !v || !kr))) return KDA_ERR_NULL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(kr, 16) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
         return KDA_ERR_ALIGN;
-    if (!set_strides(p.sq, qs, p.H, p.T, p.dn + p.dr, unit) || !set_strides(p.sk, ks, p.H, p.S, p.dn, unit) ||
-        !set_strides(p.sv, vs, p.H, p.S, p.dn, unit) || !set_strides(p.skr, krs, 0, p.S, p.dr, unit))
+    if (!set_strides(p.sq, qs, p.B, p.H, p.T, p.dn + p.dr, unit) || !set_strides(p.sk, ks, p.B, p.H, p.S, p.dn, unit) ||
+        !set_strides(p.sv, vs, p.B, p.H, p.S, p.dn, unit) || !set_strides(p.skr, krs, p.B, 0, p.S, p.dr, unit))
         return KDA_ERR_ALIGN;
     if (far_rows(p.sq, p.T, p.fp32) || far_rows(p.sk, p.S, p.fp32) || far_rows(p.sv, p.S, p.fp32) || far_rows(p.skr, p.S, p.fp32))
         return KDA_ERR_SHAPE;
@@ -121,7 +122,7 @@ int kda_latent_attn_bwd(const void *q, const kda_strides *q_strides, const void 
     kda::LatentLaunch p = shape(packed, N, H, T, S, dn, dr, io_dtype);
     if ((T > 0 && (!out || !lse || !dout || !dq)) || (S > 0 && (!dk_out || !dv_out || !dk_rope))) return KDA_ERR_NULL;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk_out, 16) ||
-        !aligned(dv_out, 16) || !aligned(dk_rope, 16) || !set_strides(p.sdo, dout_strides, H, T, dn, p.fp32 ? 4 : 8))
+        !aligned(dv_out, 16) || !aligned(dk_rope, 16) || !set_strides(p.sdo, dout_strides, p.B, H, T, dn, p.fp32 ? 4 : 8))
         return KDA_ERR_ALIGN;
     st = inputs(p, q, q_strides, k, k_strides, v, v_strides, k_rope, k_rope_strides, cu_seqlens_q, cu_seqlens_k, scale);
     if (st != KDA_OK) return st;

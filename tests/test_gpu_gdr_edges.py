@@ -179,3 +179,22 @@ def test_second_derivatives_are_refused():
         first = torch.autograd.grad(out.square().sum(), leaf[2], create_graph=True)[0]
         with pytest.raises(RuntimeError):
             (first.square().sum() + leaf[0].sum()).backward()
+
+
+def _loose(t, dims):
+    """t with a stride of 13 in dimensions of one, which no row's start depends on."""
+    t = t.cuda().contiguous()
+    assert all(t.shape[i] == 1 for i in dims)
+    return t.as_strided(t.shape, [13 if i in dims else s for i, s in enumerate(t.stride())])
+
+
+@pytest.mark.parametrize("T,dims", [(70, (0, 1)), (1, (0, 2))])
+def test_strides_of_dimensions_of_one(T, dims):
+    H = 1 if 1 in dims else 3
+    x = inputs(1, H, H, T, 64, 64, BF, 131)
+    dout = torch.randn(1, H, T, 64, generator=torch.Generator().manual_seed(7)).to(BF)
+    a, b = [t.cuda() for t in x], [_loose(t, dims) for t in x]
+    want, got = kda.gdr_chunk_fwd(*a, return_final_state=True), kda.gdr_chunk_fwd(*b, return_final_state=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want, got = kda.gdr_chunk_bwd(*a, dout.cuda()), kda.gdr_chunk_bwd(*b, _loose(dout, dims))
+    assert all(torch.equal(got[n], want[n]) for n in NAMES)

@@ -73,3 +73,19 @@ def test_second_derivatives_are_refused():
     first = torch.autograd.grad(kda.LatentAttnFunction.apply(*leaf).square().sum(), leaf[2], create_graph=True)[0]
     with pytest.raises(RuntimeError):
         (first.square().sum() + leaf[0].sum()).backward()
+
+
+@pytest.mark.parametrize("T,dims", [(70, (0, 1)), (1, (0, 2))])
+def test_strides_of_dimensions_of_one(T, dims):
+    """A stride of 13 in dimensions of one: no row's start depends on it."""
+    H = 1 if 1 in dims else 3
+    q, kv, r, do = inputs((1,), H, T, T, 64, 32, BF, 5)
+    a = [t.cuda().contiguous() for t in (q, *split(kv, 64), r, do)]
+    loose = lambda t, d: t.as_strided(t.shape, [13 if i in d else s for i, s in enumerate(t.stride())])
+    b = [loose(t, dims if t.dim() == 4 else (0,)) for t in a]
+    got = []
+    for x in (a, b):
+        out, lse = kda.latent_attn_fwd(*x[:4], return_lse=True)
+        got.append([out, lse, *kda.latent_attn_bwd(*x[:4], out, lse, x[4]).values()])
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(*got))
