@@ -198,3 +198,15 @@ def test_strides_of_dimensions_of_one(T, dims):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     want, got = kda.gdr_chunk_bwd(*a, dout.cuda()), kda.gdr_chunk_bwd(*b, _loose(dout, dims))
     assert all(torch.equal(got[n], want[n]) for n in NAMES)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_strided_gradient(dtype):
+    """dout as a model has it, [B,T,H,d] seen as [B,H,T,d] and a slice of wider rows."""
+    x = inputs(2, 2, 4, 70, 128, 64, dtype, 141)
+    wide = torch.randn(2, 70, 4, 96, generator=torch.Generator().manual_seed(8)).to(dtype).cuda()
+    dout = wide[..., 16:80].transpose(1, 2)
+    assert not dout.is_contiguous()
+    d = [t.cuda() for t in x]
+    want, got = kda.gdr_chunk_bwd(*d, dout.contiguous()), kda.gdr_chunk_bwd(*d, dout)
+    assert all(torch.equal(got[n], want[n]) for n in NAMES)

@@ -89,3 +89,60 @@ def test_strides_of_dimensions_of_one(T, dims):
         got.append([out, lse, *kda.latent_attn_bwd(*x[:4], out, lse, x[4]).values()])
     torch.cuda.synchronize()
     assert all(torch.equal(s, t) for s, t in zip(*got))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,S", [(70, 70), (40, 200)])
+def test_wide_rows(T, S, dtype):
+    """k_rope as a slice of the down-projection's output [B,S,dc+dr], q as one of wider rows, dout
+    transposed from [B,T,H,d]."""
+    dn, dr, dc, B, H = 128, 64, 96, 2, 3
+    q, kv, r, do = inputs((B,), H, T, S, dn, dr, dtype, 31)
+    gen = torch.Generator().manual_seed(1)
+    down = torch.randn(B, S, dc + dr, generator=gen).to(dtype)
+    down[..., dc:] = r
+    qw = torch.randn(B, T, H, dn + dr + 32, generator=gen).to(dtype)
+    qw[..., :dn + dr] = q.transpose(1, 2)
+    k, v = split(kv, dn)
+    dev = (qw.cuda()[..., :dn + dr].transpose(1, 2), *split(kv.cuda(), dn), down.cuda()[..., dc:])
+    dd = do.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    assert not any(t.is_contiguous() for t in (*dev, dd))
+    out, lse = kda.latent_attn_fwd(*dev, return_lse=True)
+    g = kda.latent_attn_bwd(*dev, out, lse, dd)
+    torch.cuda.synchronize()
+    for b in range(B):
+        _check_all(q[b], k[b], v[b], r[b], do[b], (dn + dr) ** -0.5, dtype, out[b], lse[b], {n: t[b] for n, t in g.items()}, "%d " % b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H,n", [(1, 16, 9000), (2, 5, 4500)])
+def test_absorbed_long_history(B, H, n, dtype):
+    """One or two users with more rows than the largest number of parts has 64-row shares of."""
+    dc, page = 512, 64
+    gen = torch.Generator().manual_seed(n)
+    M = -(-n // page)
+    cache = torch.randn(B * M, page, dc + 64, generator=gen).to(dtype)
+    table = torch.randperm(B * M, generator=gen).reshape(B, M)
+    q = (torch.randn(B, H, dc + 64, generator=gen) * 0.5).to(dtype)
+    lens = [n - 777 * b for b in range(B)]
+    out, lse = kda.latent_decode_step(q.cuda(), cache.cuda(), table.to(torch.int32).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 0.07,
+                                      dc=dc, return_lse=True)
+    torch.cuda.synchronize()
+    for b in range(B):
+        rows = cache[table[b]].reshape(-1, dc + 64)[:lens[b]]
+        for h in (0, H - 1):
+            ref = one(q[b, h][None], rows, rows[:, :dc], 0.07, dtype)
+            _check(out[b, h][None], *ref["out"], "out %d %d" % (b, h))
+            _check(lse[b, h][None], *ref["lse"], "lse %d %d" % (b, h))
+
+
+def test_large_scores():
+    """Scores of a few hundred with bf16 inputs: one or two keys have all of a row's weight."""
+    q, kv, r, do = inputs((1,), 2, 200, 200, 128, 64, BF, 5)
+    q = q * 32
+    k, v = split(kv, 128)
+    dev = (q.cuda(), *split(kv.cuda(), 128), r.cuda())
+    out, lse = kda.latent_attn_fwd(*dev, return_lse=True)
+    g = kda.latent_attn_bwd(*dev, out, lse, do.cuda())
+    torch.cuda.synchronize()
+    _check_all(q[0], k[0], v[0], r[0], do[0], 192 ** -0.5, BF, out[0], lse[0], {n: t[0] for n, t in g.items()})
