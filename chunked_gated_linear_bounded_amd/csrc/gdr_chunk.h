@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256, 4) void gdr_chunk_kernel(const GdrChunkArgs p)
         hd[128 + lane] = bv;
         // what the state stage bounds its operands with (GdrLayout)
         auto norm = [](float x) { return wave_max(finite_mag(x)); };
-        const float ck = norm(bv * ex2((float)G) * sK1[lane]), bm = norm(bv);
+        const float ck = norm(bv * sK1[lane] * ex2((float)G)), bm = norm(bv);
         const float cl = norm(ex2((float)(last - G)) * sK1[lane]), k1 = norm(sK1[lane]);
         float ks = in ? sKm[lane] : 0.f;
 #pragma unroll

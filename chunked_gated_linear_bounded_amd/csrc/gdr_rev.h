@@ -436,7 +436,7 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
         }
         const float um = mu.wave();
         if (lane == 0) sMax[4 + w] = um;
-        const float gbound = 64.f * ubound * (max4(mdg) + last * k1 * pmax);  // of e^G dX
+        const float gbound = 64.f * ubound * (max4(mdg) + last * pmax * k1);  // of e^G dX
         load_k(c - 1);
         barrier_lds();  // (2)
 

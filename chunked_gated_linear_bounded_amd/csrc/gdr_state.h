@@ -398,7 +398,7 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
         }
         const float xm = mx.wave();
         if (lane == 0) sMax[4 + w] = xm;
-        const float lbound = ubound * (max4(ml) + last * bbound * k1 * pmax);  // of e^{G_last - G} U
+        const float lbound = ubound * (max4(ml) + last * pmax * (bbound * k1));  // of e^{G_last - G} U
         barrier_lds();  // (2)
 
         // ---- 2. U = T X

@@ -210,3 +210,26 @@ def test_strided_gradient(dtype):
     d = [t.cuda() for t in x]
     want, got = kda.gdr_chunk_bwd(*d, dout.contiguous()), kda.gdr_chunk_bwd(*d, dout)
     assert all(torch.equal(got[n], want[n]) for n in NAMES)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_factors_of_a_bound_far_apart(dtype):
+    """A state of 1e30 that decays by e^-80 at a chunk's first token, keys of 1e6 with betas of 1e-12, no
+    values: every term is of ordinary size, though products of some of a bound's factors leave float's
+    range.  (Spread over the chunk, that decay would leave the state below 2^-37 of what its first tokens
+    wrote.)"""
+    x = list(inputs(1, 1, 2, 130, 64, 64, dtype, 151))
+    x[1] = (x[1].double() * 1e6).to(dtype)
+    x[2] = torch.zeros_like(x[2])
+    x[3] = torch.full_like(x[3], -0.01)
+    x[3][:, :, 0] = -80.0
+    x[4] = (x[4].double() * 0.9e-12).to(dtype)
+    S0 = torch.randn(1, 2, 64, 64, generator=torch.Generator().manual_seed(9)) * 1e30
+    dfin = torch.randn(1, 2, 64, 64, generator=torch.Generator().manual_seed(10))
+    d = [t.cuda() for t in x]
+    _, fs = kda.gdr_chunk_fwd(*d, return_final_state=True, initial_state=S0.cuda())
+    _, S = recurrent(*x, 1.0, S0)
+    check(fs[0], S[0], state_bound(chunk_terms(*(t[0] for t in x), 1.0, S0[0])[2]), "state")
+    got = kda.gdr_chunk_bwd(*d, torch.zeros_like(d[2]), initial_state=S0.cuda(), dfinal_state=dfin.cuda())
+    ref = reference(x, torch.zeros_like(x[2]), 1.0, S0, dfin)
+    compare(got["dinitial_state"], ref[5], dtype, "dinitial_state")
