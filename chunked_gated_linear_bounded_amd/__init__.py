@@ -450,7 +450,7 @@ class KdaChunkFunction(torch.autograd.Function):
     """out, final_state = KdaChunkFunction.apply(q, k, v, a, beta, g_min, chunk, gate): the chunked
     forward with its backward, for training.  Forward through kda_chunk_fwd_ex, backward through
     kda_chunk_bwd (T % 16 == 0); the float32 gradients are returned in the inputs' dtype.  No
-    initial state (S_0 = 0)."""
+    initial state (S_0 = 0).  Once differentiable."""
 
     @staticmethod
     def forward(ctx, q, k, v, a, beta, g_min=-5.0, chunk=64, gate="bounded"):

@@ -15,7 +15,7 @@
 // columns is brought to the smallest of them on its way into LDS.  diag(b) X2 takes b times the power of
 // two that brings max |b| below 1: X2 itself sits at 2^13 .. 2^14, and a beta of 4 would reach fp16's end.
 // The stage reads about 200 KiB a chunk and value head at d = 128 (bf16) and writes 32 KiB a key head;
-// its 656 MFMAs a head are a tenth of that traffic's time (4096 tokens x 32 heads: 166 us, most of it
+// its 656 MFMAs a head are a tenth of that traffic's time (4096 tokens x 32 heads: 168 us, most of it
 // the four phases' barriers with one work-group of eight waves a CU), so the four phases share one 64
 // KiB buffer (P, then dP', then K and Q; dX, then X1 and X2).
 #pragma once

@@ -42,7 +42,8 @@ hipError_t launch_gdr_decode(const GdrLaunch &p);
 // state stage and the reverse pass, 16 columns / 32: 5 sequences of 1024 x 12 heads (480 work-groups of
 // 16), dk = 128: 51 and 80 / 42 and 60, dk = 64: 36 and 53 / 36 and 50; 11 documents of 5000 tokens x 4
 // heads (352), dk = 128: 37 and 60 / 59 and 82, dk = 64: 23 and 36 / 33 and 47; 32 documents of 12,000
-// tokens x 8 heads (2048), dk = 128: 99 and 161 / 79 and 119.
+// tokens x 8 heads (2048), dk = 128: 99 and 161 / 79 and 119.  Lengths are on the device, so documents of
+// one length get the ragged ones' choice: at 257 to 512 work-groups and dk = 128 the first line's loss.
 inline bool gdr_two_tiles(const GdrLaunch &p) {
     const long long places = p.cu != nullptr || (p.dk == 64 && !p.fp32) ? 512 : 256;
     return (long long)p.N * p.H * (p.dv / 16) > places;

@@ -13,11 +13,11 @@
 // exponents of the pieces come from bounds as in gdr_state.h, |dU| <= max|M^T dO| + max(e^{G_last - G}
 // |k|_1) max|dP'|, |dX| <= 64 max|T| max|dU|, |dP| <= e^{G_last} max|dP'| + max|Q^T H| + sum(max|k|)
 // max|F|.  H and F have their own, of the decayed values, F_j = b_j sum_i (T_ij e^{G_j - G_i}) e^{G_i} dU_i
-// with |e^G dU| <= max|e^G M^T dO| + e^{G_last} max|k|_1 max|dP'|: where the chunk's first tokens have no gradient, both are as small as the decay over them.  A state
-// gradient that a caller asks for (dinitial_state, float32) is exact to the same 22 bits as the final
-// state.
+// with |e^G dU| <= max|e^G M^T dO| + e^{G_last} max|k|_1 max|dP'|: where the chunk's first tokens have no
+// gradient, both are as small as the decay over them.  A state gradient that a caller asks for
+// (dinitial_state, float32) is exact to the same 22 bits as the final state.
 //
-// 4096 tokens x 32 heads: 2.4 us a chunk, 157 us; with everything on the chain's four waves, and a
+// 4096 tokens x 32 heads: 2.5 us a chunk, 159 us; with everything on the chain's four waves, and a
 // fourth barrier for dP's maximum, 3.2 us, 204 us.
 #pragma once
 #include "gdr_state.h"
@@ -59,7 +59,8 @@ __global__ __launch_bounds__(512) void gdr_rev_kernel(const GdrRevArgs p) {
     typedef __attribute__((address_space(3))) f32x4 lds_f4;
     typedef __attribute__((address_space(3))) float lds_f1;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
-    __shared__ __attribute__((aligned(16))) float sMax[32];  // per wave: max |dP'|, |dU|, |F|, |dO|, |M^T dO|, |Q^T H|, |e^G M^T dO|, |e^G dO|
+    // per wave: max |dP'|, |dU|, |F|, |dO|, |M^T dO|, |Q^T H|, |e^G M^T dO|, |e^G dO|
+    __shared__ __attribute__((aligned(16))) float sMax[32];
     __shared__ int sExp[2];     // exponents of dP's and of dX's pieces
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wid & 3;

@@ -16,9 +16,9 @@
 // U|: the maximum is that of the decayed U, so the sum is not decayed again (keys that end before the
 // chunk does would leave it far below P').  The decayed U has a bound of its own, e^{G_last - G_i} U_i =
 // sum_j (T_ij e^{G_j - G_i}) e^{G_last - G_j} X_j with |e^{G_last - G} X| <= max(b e^{G_last - G} |V|) +
-// e^{G_last} max b max|k|_1 max|P|: where the chunk's last tokens write nothing, all of it
-// is as small as the decay over them, and U's exponent would leave its pieces no bits.  A bound that is
-// 2^10 too large still leaves two pieces their 22 bits.
+// e^{G_last} max b max|k|_1 max|P|: where the chunk's last tokens write nothing, all of it is as small as
+// the decay over them, and U's exponent would leave its pieces no bits.  A bound that is 2^10 too large
+// still leaves two pieces their 22 bits.
 //
 // The chain of chunks is what bounds the stage, three exchanges through LDS one behind the other.
 // 65,536 tokens x 32 heads (16 columns a work-group, one work-group a CU): 1.48 us a chunk; the chain's
@@ -96,7 +96,8 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     constexpr GdrLayout L{NI, DK, MP};
     constexpr GdrSave SV{NI, DK};
     __shared__ __attribute__((aligned(1024))) unsigned char smem[S::BYTES];
-    __shared__ __attribute__((aligned(16))) float sMax[28];  // per wave: max |P|, |X|, |e^{G_last-G} U|; |V| of two chunks; b e^{G_last-G} |V| of two
+    // per wave: max |P|, |X|, |e^{G_last-G} U|; |V| of two chunks, b e^{G_last-G} |V| of two
+    __shared__ __attribute__((aligned(16))) float sMax[28];
     __shared__ int sExp[2];     // exponents of P and of U's pieces
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wid & 3;
@@ -360,7 +361,8 @@ __global__ __launch_bounds__(512) void gdr_state_kernel(const GdrStateArgs p) {
     }
     for (int c = 0; c < nchunk; ++c) {
         barrier_lds();  // (1)
-        const float pmax = max4(sMax), last = h0[0], kbound = h1[1], bbound = h1[2], tbound = h1[3], ksum = h2[0], ubound = h2[2], k1 = h2[3];
+        const float pmax = max4(sMax), last = h0[0], kbound = h1[1], bbound = h1[2], tbound = h1[3];
+        const float ksum = h2[0], ubound = h2[2], k1 = h2[3];
         const float et_ = h0[1], ek_ = h0[3];
         const int et = __builtin_bit_cast(int, et_), ek = __builtin_bit_cast(int, ek_);
 

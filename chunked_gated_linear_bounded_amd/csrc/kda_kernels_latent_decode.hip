@@ -9,8 +9,9 @@ namespace kda {
 // Four waves on 16 heads or on 32, eight on 64 (float32, whose registers do not allow eight: 32).
 static int heads_per_group(const LatentLaunch &p) { return p.H <= 16 ? 16 : p.H <= 32 || p.fp32 ? 32 : 64; }
 static int head_groups(const LatentLaunch &p) { return (p.H + heads_per_group(p) - 1) / heads_per_group(p); }
-// Parts the keys are cut into: about two work-groups a CU, each with at least 64 keys of the longest
-// sequence that the table can hold (the lengths are on the device).
+// Parts the keys are cut into: up to 512 work-groups, each with at least 64 keys of the longest sequence
+// that the table can hold (the lengths are on the device), and 64 of one sequence, whom the join takes
+// one after the other (latent_decode.h has the times): one user's 20,000 rows keep 64 CUs busy, no more.
 static int splits(const LatentLaunch &p) {
     const long long want = 512 / ((long long)p.B * head_groups(p)), most = ((long long)p.max_pages * p.page + 63) / 64;
     const long long n = want < most ? want : most;

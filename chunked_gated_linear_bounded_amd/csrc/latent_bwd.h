@@ -496,7 +496,7 @@ __global__ __launch_bounds__(512) void latent_dkv_kernel(const LatentBwdArgs p) 
 }
 
 // Sum of the heads' partials of the rotary key part: part [B][H][S][DR] -> out [B][S][DR], keys that
-// no sequence covers as zeros; and those keys' rows of dk, dv, those queries' rows of dq as zeros.
+// no sequence covers as zeros.
 template <typename E>
 __global__ __launch_bounds__(256) void latent_dkr_kernel(const float *part, AttnSeqs seqs, int H, int DR, E *out) {
     const int b = blockIdx.y;

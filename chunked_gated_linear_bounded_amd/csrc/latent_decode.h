@@ -11,9 +11,12 @@
 // Up to 16 heads the 2 * 16 * (576 + 512) flops a 1,152-byte row costs are far below what HBM lets
 // pass; at 128 heads (two work-groups on the same keys, side by side on one XCD) the 272 KiB of LDS
 // reads per tile and work-group take about the time HBM needs for the tile.  The keys are split
-// over work-groups until there are two a CU; the parts are joined by their log-sum-exps in a second
-// kernel.  48 sequences of 6,000 to 12,000 rows, 128 heads: 313 us and 14 for the join (three
-// work-groups a CU: 345 and 24).
+// over work-groups until there are 512, two a CU (on 64 heads at dc = 512 one behind the other: 221
+// registers leave a CU one work-group of eight waves), but a sequence into at most 64 parts; the parts
+// are joined by their log-sum-exps in a second kernel, which walks them one behind the other.  48
+// sequences of 6,000 to 12,000 rows, 128 heads: 309 us and 14 for the join (768 work-groups: 345 and
+// 24).  One sequence of 20,000 rows, 16 heads, whole calls: 47 us with 64 parts, 105 with 256, 151
+// with 313.
 #pragma once
 #include "latent_common.h"
 

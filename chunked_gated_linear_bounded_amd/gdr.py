@@ -174,7 +174,8 @@ def gdr_chunk_bwd_varlen(q, k, v, g, beta, dout, cu_seqlens, scale=1.0, initial_
 
 class GdrChunkFunction(torch.autograd.Function):
     """out, final_state = GdrChunkFunction.apply(q, k, v, g, beta, scale, initial_state, cu_seqlens): the
-    chunked forward with its backward, for a batch or (cu_seqlens given) for packed documents."""
+    chunked forward with its backward, for a batch or (cu_seqlens given) for packed documents.  Once
+    differentiable: a gradient of the gradients is an error."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, scale=1.0, initial_state=None, cu_seqlens=None):

@@ -130,7 +130,8 @@ def latent_attn_bwd_varlen(q, k, v, k_rope, out, lse, dout, cu_seqlens_q, cu_seq
 
 class LatentAttnFunction(torch.autograd.Function):
     """out = LatentAttnFunction.apply(q, k, v, k_rope, scale, cu_seqlens_q, cu_seqlens_k): the expanded form
-    with its backward, for a batch or (boundaries given) for packed sequences."""
+    with its backward, for a batch or (boundaries given) for packed sequences.  Once differentiable: a
+    gradient of the gradients is an error."""
 
     @staticmethod
     def forward(ctx, q, k, v, k_rope, scale=None, cu_seqlens_q=None, cu_seqlens_k=None):

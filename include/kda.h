@@ -58,6 +58,9 @@
 extern "C" {
 #endif
 
+/* Version 8 also stands for the entry points kda_gdr_* and kda_latent_*, kda_strides and KDA_ERR_SCALE,
+ * which came later and changed nothing that was there: a caller that may meet a library without them
+ * looks their symbols up. */
 #define KDA_ABI_VERSION 8
 /* The most negative g_min accepted: the constant the method fixes.  Inside a
  * 16-token tile the key operands of the diagonal sub-tile grow by up to
