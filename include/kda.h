@@ -337,7 +337,9 @@ int kda_gdr_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k
  * dfinal_state : [N][H][dv][dk] float32 or NULL.  dq, dk_out : [B][Hk][T][dk] (summed over the value
  * heads of a key head), dv_out : [B][H][T][dv], dg, dbeta : [B][H][T], contiguous, in io_dtype;
  * dinitial_state : [N][H][dv][dk] float32 or NULL.  The gradients of tokens that no document covers
- * are written as zeros.  Everything is recomputed from the inputs; no float atomics. */
+ * are written as zeros.  Everything is recomputed from the inputs; no float atomics.  dinitial_state is as
+ * accurate as the final state.  dg is what is left of larger terms that cancel: where decays are strong
+ * its floor is float32's rounding of those terms, not of dg. */
 int kda_gdr_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
                       const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
                       const void *beta, const kda_strides *beta_strides, const void *dout,
