@@ -15,6 +15,13 @@ built, every entry point raises; there is no fallback.
     out, S = kda.KdaChunkFunction.apply(q, k, v, a, beta)              # the same, under autograd
     G = kda.gate_cumsum(a, g_min=-5.0, chunk=64)
 
+Linear attention with one decay per token and value head (lin.py):
+
+    out, S = kda.lin_chunk_fwd(q, k, v, g, return_final_state=True)
+    o_t = kda.lin_decode_step(q_t, k_t, v_t, g_t, S)
+    grads = kda.lin_chunk_bwd(q, k, v, g, dout)                      # dq, dk, dv, dg, dinitial_state
+    out, S = kda.LinChunkFunction.apply(q, k, v, g)                  # the same, under autograd
+
 The gated delta rule, one decay per token and value head (gdr.py):
 
     out, S = kda.gdr_chunk_fwd(q, k, v, g, beta, return_final_state=True)
@@ -110,6 +117,14 @@ def lib():
         L.kda_latent_decode_workspace_bytes.restype = sz
         L.kda_latent_decode_step.argtypes = [vp] * 4 + [i] * 8 + [f, vp, vp, vp, sz, vp]
         L.kda_latent_decode_step.restype = i
+        L.kda_lin_workspace_bytes.argtypes = [i] * 9
+        L.kda_lin_workspace_bytes.restype = sz
+        L.kda_lin_chunk_fwd.argtypes = [vp, vp] * 4 + [vp] + [i] * 8 + [f] + [vp] * 4 + [sz, vp]
+        L.kda_lin_chunk_fwd.restype = i
+        L.kda_lin_chunk_bwd.argtypes = [vp, vp] * 5 + [vp] + [i] * 8 + [f] + [vp] * 8 + [sz, vp]
+        L.kda_lin_chunk_bwd.restype = i
+        L.kda_lin_decode_step.argtypes = [vp] * 4 + [i] * 7 + [f, vp, vp, vp]
+        L.kda_lin_decode_step.restype = i
         _lib = L
     return _lib
 
@@ -501,3 +516,5 @@ from .gdr import (GdrChunkFunction, gdr_chunk_bwd, gdr_chunk_bwd_varlen, gdr_chu
 from .latent import (LatentAttnFunction, latent_attn_bwd, latent_attn_bwd_varlen, latent_attn_fwd,  # noqa: E402
                      latent_attn_fwd_varlen, latent_bwd_workspace_bytes, latent_decode_step,
                      latent_decode_workspace_bytes)
+from .lin import (LinChunkFunction, lin_chunk_bwd, lin_chunk_bwd_varlen, lin_chunk_fwd,  # noqa: E402
+                  lin_chunk_fwd_varlen, lin_decode_step, lin_workspace_bytes)

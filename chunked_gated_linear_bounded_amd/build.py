@@ -43,9 +43,12 @@ UNITS = [
     ("kda_kernels_latent.hip", "kda_kernels_latent.o", []),
     ("kda_kernels_latent_bwd.hip", "kda_kernels_latent_bwd.o", []),
     ("kda_kernels_latent_decode.hip", "kda_kernels_latent_decode.o", []),
+    ("kda_kernels_lin.hip", "kda_kernels_lin.o", []),
+    ("kda_kernels_lin_bwd.hip", "kda_kernels_lin_bwd.o", []),
     ("kda_abi.cpp", "kda_abi.o", []),
     ("kda_abi_gdr.cpp", "kda_abi_gdr.o", []),
     ("kda_abi_latent.cpp", "kda_abi_latent.o", []),
+    ("kda_abi_lin.cpp", "kda_abi_lin.o", []),
 ]
 
 

@@ -1,0 +1,136 @@
+// Instantiations and launchers of decayed linear attention's backward.
+#include <hip/hip_runtime.h>
+
+#include "lin_run.h"
+
+namespace kda {
+
+// Workspace: start states of the segments, forwards and backwards, and their decays; the sequences' end
+// states; the two dot products a token that the decays' gradient is made of; and, where key heads are
+// shared, the value heads' float32 partials of dq and dk.
+struct LinBwdPlan {
+    size_t units, state, tokens, part;
+    size_t seg[2], decay[2], last, dots[2], parts[2], bytes;
+    explicit LinBwdPlan(const LinLaunch &p) {
+        units = (size_t)p.B * p.H * lin_slots(p);
+        state = (size_t)p.dk * p.dv;
+        tokens = (size_t)p.B * p.H * p.T;
+        part = p.H == p.Hk ? 0 : tokens * p.dk;
+        size_t at = 0;
+        auto take = [&](size_t floats) {
+            const size_t here = at;
+            at += (floats * 4 + 255) / 256 * 256;
+            return here;
+        };
+        for (int i = 0; i < 2; ++i) {
+            seg[i] = take(units * state);
+            decay[i] = take(units);
+            dots[i] = take(tokens);
+            parts[i] = take(part);
+        }
+        last = take((size_t)p.N * p.H * state);
+        bytes = at;
+    }
+};
+size_t lin_bwd_bytes(const LinLaunch &p) { return LinBwdPlan(p).bytes; }
+
+#define KDA_LAUNCH(...)                             \
+    do {                                            \
+        hipLaunchKernelGGL(__VA_ARGS__);            \
+        const hipError_t e_ = hipGetLastError();    \
+        if (e_ != hipSuccess) return e_;            \
+    } while (0)
+
+template <int DK, int DV, bool F32, bool DOT, bool SUM>
+static hipError_t bwd_t(const LinLaunch &p) {
+    using E = typename std::conditional<F32, float, __bf16>::type;
+    const LinBwdPlan m(p);
+    auto f = [&](size_t at) { return reinterpret_cast<float *>(p.workspace + at); };
+    const int r = p.H / p.Hk;
+    const Strides3 sq = lin_st3(p.sq), sk = lin_st3(p.sk), sv = lin_st3(p.sv), sdo = lin_st3(p.sdo);
+    const unsigned grid = lin_walk_grid(p);
+    const bool want_last = DOT && p.dfinal != nullptr, many = p.T > lin_segment(p);
+    LinWalkArgs a = lin_walk_args(p);
+    const dim3 block(256);
+    // each segment's own part of the state, and of the gradient by it
+    LinWalkArgs s0 = a, s1 = a;
+    s0.b = p.k; s0.sb = sk; s0.rb = r; s0.c = p.v; s0.sc = sv;
+    s0.seg = f(m.seg[0]);
+    s0.seg_decay = f(m.decay[0]);
+    s0.all = want_last;
+    s1.b = p.q; s1.sb = sq; s1.rb = r; s1.c = p.dout; s1.sc = sdo;
+    s1.into = p.scale;
+    s1.seg = f(m.seg[1]);
+    s1.seg_decay = f(m.decay[1]);
+    if (many || want_last) KDA_LAUNCH((lin_walk_kernel<DK, DV, F32, false, false, false, false, false>), dim3(grid), block, 0, p.stream, s0);
+    if (many) KDA_LAUNCH((lin_walk_kernel<DK, DV, F32, true, false, false, false, false>), dim3(grid), block, 0, p.stream, s1);
+    if (many || want_last) {
+        LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {}};
+        s.side[0] = {p.init_state, f(m.seg[0]), want_last ? f(m.last) : nullptr, f(m.decay[0]), want_last};
+        s.side[1] = {p.dfinal, many ? f(m.seg[1]) : nullptr, p.dinit, f(m.decay[1]), false};
+        KDA_LAUNCH(lin_scan_kernel, dim3((unsigned)p.N * p.H * (DK * DV / 1024), 2), block, 0, p.stream, s);
+    }
+    // dq: forwards, with the transposed state
+    LinWalkArgs w = a;
+    w.a = p.dout; w.sa = sdo;
+    w.b = p.v; w.sb = sv;
+    w.c = p.k; w.sc = sk; w.rc = r;
+    w.y = p.q; w.sy = sq; w.ry = r;
+    w.inter = p.scale;
+    w.init = p.init_state;
+    w.seg = f(m.seg[0]);
+    w.dots = f(m.dots[0]);
+    w.out = SUM ? f(m.parts[0]) : p.dq;
+    KDA_LAUNCH((lin_walk_kernel<DV, DK, F32, false, true, true, DOT, SUM>), dim3(grid), block, 0, p.stream, w);
+    // dk and dv: backwards in time
+    w = a;
+    w.a = p.v; w.sa = sv;
+    w.b = p.dout; w.sb = sdo;
+    w.c = p.q; w.sc = sq; w.rc = r;
+    w.y = p.k; w.sy = sk; w.ry = r;
+    w.into = p.scale;
+    w.init = p.dfinal;
+    w.seg = f(m.seg[1]);
+    w.dots = f(m.dots[1]);
+    w.out = SUM ? f(m.parts[1]) : p.dk_;
+    KDA_LAUNCH((lin_walk_kernel<DV, DK, F32, true, true, true, DOT, SUM>), dim3(grid), block, 0, p.stream, w);
+    w = a;
+    w.a = p.k; w.sa = sk; w.ra = r;
+    w.b = p.q; w.sb = sq; w.rb = r;
+    w.c = p.dout; w.sc = sdo;
+    w.into = p.scale;
+    w.init = p.dfinal;
+    w.final_state = p.dinit;
+    w.seg = f(m.seg[1]);
+    w.out = p.dv_;
+    KDA_LAUNCH((lin_walk_kernel<DK, DV, F32, true, false, true, false, false>), dim3(grid), block, 0, p.stream, w);
+    if (p.T == 0) return hipSuccess;
+    if (DOT) {
+        LinDecayGradArgs d{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,
+                           f(m.dots[0]), f(m.dots[1]), p.dg};
+        KDA_LAUNCH(lin_decay_grad_kernel, dim3((unsigned)m.units), block, 0, p.stream, d);
+    }
+    if (SUM) {
+        const long long n4 = (long long)p.T * DK / 4, all = n4 * p.B * p.Hk;
+        KDA_LAUNCH((lin_head_sum_kernel<E>), dim3((unsigned)((all + 255) / 256), 2), block, 0, p.stream,
+                   f(m.parts[0]), f(m.parts[1]), static_cast<E *>(p.dq), static_cast<E *>(p.dk_), r, n4, all);
+    }
+    if (p.packed) {
+        const LinUncovered<E> u{static_cast<E *>(p.dq), static_cast<E *>(p.dk_), static_cast<E *>(p.dv_), p.dg, a.seqs, p.Hk, p.H, DK, DV, p.g32};
+        KDA_LAUNCH((lin_uncovered_kernel<E>), dim3((unsigned)((p.T + 63) / 64), p.H), block, 0, p.stream, u);
+    }
+    return hipSuccess;
+}
+template <int DK, int DV, bool F32>
+static hipError_t bwd_d(const LinLaunch &p) {
+    if (p.dg) return p.H == p.Hk ? bwd_t<DK, DV, F32, true, false>(p) : bwd_t<DK, DV, F32, true, true>(p);
+    return p.H == p.Hk ? bwd_t<DK, DV, F32, false, false>(p) : bwd_t<DK, DV, F32, false, true>(p);
+}
+template <bool F32>
+static hipError_t bwd_io(const LinLaunch &p) {
+    if (p.dk == 64) return p.dv == 64 ? bwd_d<64, 64, F32>(p) : bwd_d<64, 128, F32>(p);
+    return p.dv == 64 ? bwd_d<128, 64, F32>(p) : bwd_d<128, 128, F32>(p);
+}
+hipError_t launch_lin_bwd(const LinLaunch &p) { return p.fp32 ? bwd_io<true>(p) : bwd_io<false>(p); }
+
+}  // namespace kda

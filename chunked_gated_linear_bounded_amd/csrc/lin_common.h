@@ -1,0 +1,129 @@
+// Building blocks of linear attention with one log-decay per token and value head:
+//   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   g_t <= 0,   S dv x dk.
+// In chunks of 64 tokens, with P = S^T at a chunk's start, G the inclusive prefix sum of g inside the
+// chunk and D_ij = e^{G_i - G_j} (i >= j):
+//   O = scale ((Q K^T o D) V + e^G Q P),   P' = e^{G_last} P + K^T diag(e^{G_last - G}) V.
+// The gradients are three operators of the same form.  With R the gradient by the state behind a token,
+// transposed as P is,
+//   dQ = scale ((dO V^T o D) K + e^G dO P^T)                   forwards, the state P^T;
+//   dK = scale (dO V^T o D)^T Q + e^{G_last - G} V R^T         backwards in time;
+//   dV = scale (Q K^T o D)^T dO + e^{G_last - G} K R           backwards in time;
+//   R at the chunk's start = e^{G_last} R + scale Q^T diag(e^G) dO.
+// So one walk over chunks does all four: out = a-rows against b-rows, times c-rows, plus a-rows against
+// a state that gathers b c^T (lin_walk.h), forwards or backwards.
+//
+// The state has no delta rule in it: what a piece of a sequence adds to it does not depend on what came
+// before.  So a sequence is cut into segments, walked side by side: first each segment's own
+// contribution (b and c are read), then a scan over the segments (lin_scan.h), then the outputs.
+//
+// log-decays are summed in float64 and kept as two floats, so that a difference of two prefix sums is
+// as exact where strong decays came before as where none did.
+#pragma once
+#include "latent_common.h"
+
+namespace kda {
+
+struct LinSeqs {
+    const int *cu;    // NULL: fixed-length
+    int N, T, seg;    // sequences; tokens of one sequence (fixed) or of the stream; tokens of a segment
+    __device__ __forceinline__ int clip(int x) const { return x < 0 ? 0 : (x > T ? T : x); }
+    __device__ __forceinline__ int start(int n) const { return cu ? clip(cu[n]) : 0; }
+    __device__ __forceinline__ int length(int n) const {
+        if (!cu) return T;
+        const int s = clip(cu[n]), e = clip(cu[n + 1]);
+        return e > s ? e - s : 0;
+    }
+    // first segment slot of sequence n inside its batch entry; as in GdrSeqs, floor(start / seg) + n
+    // leaves every sequence room for its segments (and at least one slot)
+    __device__ __forceinline__ int slot0(int n) const { return cu ? clip(cu[n]) / seg + n : 0; }
+    __device__ __forceinline__ int segments(int n) const { return (length(n) + seg - 1) / seg; }
+    // the segment at slot j of batch entry b: its sequence n, its number in it; false: none there
+    __device__ __forceinline__ bool find(int b, int j, int &n, int &c) const {
+        n = b;
+        c = j;
+        if (cu) {
+            int lo = 0, hi = N - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (slot0(mid) <= j) lo = mid;
+                else hi = mid - 1;
+            }
+            n = lo;
+            c = j - slot0(n);
+        }
+        const int have = segments(n);
+        return c >= 0 && (c < have || c == 0);
+    }
+};
+
+// ---------------------------------------------------------------- log-decays
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ double dpp_add64(double x) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    const unsigned lo = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWMASK, 0xF, false);
+    const unsigned hi = (unsigned)__builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWMASK, 0xF, false);
+    return x + __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+// inclusive prefix sum over the 64 lanes
+__device__ __forceinline__ double wave_scan64(double x) {
+    x = dpp_add64<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8
+    x = dpp_add64<0x112, 0xF>(x);
+    x = dpp_add64<0x114, 0xF>(x);
+    x = dpp_add64<0x118, 0xF>(x);
+    x = dpp_add64<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+    x = dpp_add64<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+    return x;
+}
+__device__ __forceinline__ double lane64(double x, int lane) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)u, lane);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(u >> 32), lane);
+    return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+// a log-decay in log2 units; below -1000 (-inf too) it is a decay to zero, and sums stay finite
+__device__ __forceinline__ double decay_log2(float g) { return (double)(g < -1000.f ? -1000.f : g) * 1.4426950408889634; }
+
+__device__ __forceinline__ float load_g(const void *g, long long at, bool g32) {
+    return g32 ? reinterpret_cast<const float *>(g)[at] : (float)reinterpret_cast<const __bf16 *>(g)[at];
+}
+
+// ---------------------------------------------------------------- operands
+// What is computed in float32 and enters a product again is carried in pieces where operands are bf16:
+// x = hi + lo keeps 16 bits (M and P, whose products are rounded to bf16 outputs), a third piece all 24
+// (what the float32 state gathers).  bf16 has float's exponents, so pieces need no scaling.  float32
+// inputs use float32 MFMAs and one piece.
+template <bool F32> struct LinOp : AttnOp<F32> {
+    using V8 = typename AttnOp<F32>::V8;
+    static constexpr int MP = F32 ? 1 : 2, SP = F32 ? 1 : 3;
+    // pieces of the pair (x, y)
+    template <int NP>
+    __device__ __forceinline__ static void pieces(f32x4 x, f32x4 y, V8 (&r)[NP]) {
+        if constexpr (F32) {
+            r[0] = V8{x, y};
+        } else {
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                r[p] = AttnOp<F32>::pair(x, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] -= (float)r[p][i];
+                    y[i] -= (float)r[p][4 + i];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ static void split(const V8 &v, f32x4 &x, f32x4 &y) {
+        if constexpr (F32) {
+            x = v.a;
+            y = v.b;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = (float)v[i];
+                y[i] = (float)v[4 + i];
+            }
+        }
+    }
+};
+
+}  // namespace kda

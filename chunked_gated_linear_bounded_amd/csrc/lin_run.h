@@ -1,0 +1,27 @@
+// What the launchers of decayed linear attention's forward and backward share.
+#pragma once
+#include "lin_launch.h"
+#include "lin_scan.h"
+#include "lin_walk.h"
+
+namespace kda {
+
+inline Strides3 lin_st3(const long long (&s)[3]) { return Strides3{s[0], s[1], s[2]}; }
+
+inline LinWalkArgs lin_walk_args(const LinLaunch &p) {
+    LinWalkArgs a{};
+    a.g = p.g;
+    a.sg = lin_st3(p.sg);
+    a.g32 = p.g32;
+    a.ra = a.rb = a.rc = a.ry = 1;
+    a.seqs = LinSeqs{p.cu, p.N, p.T, lin_segment(p)};
+    a.B = p.B;
+    a.H = p.H;
+    a.nslot = (int)lin_slots(p);
+    a.scale = p.scale;
+    a.inter = a.into = 1.f;
+    return a;
+}
+inline unsigned lin_walk_grid(const LinLaunch &p) { return (unsigned)(((long long)p.B * p.H * lin_slots(p) + 7) / 8 * 8); }
+
+}  // namespace kda

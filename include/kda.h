@@ -58,7 +58,7 @@
 extern "C" {
 #endif
 
-/* Version 8 also stands for the entry points kda_gdr_* and kda_latent_*, kda_strides and KDA_ERR_SCALE,
+/* Version 8 also stands for the entry points kda_gdr_*, kda_latent_* and kda_lin_*, kda_strides and KDA_ERR_SCALE,
  * which came later and changed nothing that was there: a caller that may meet a library without them
  * looks their symbols up. */
 #define KDA_ABI_VERSION 8
@@ -415,6 +415,49 @@ size_t kda_latent_decode_workspace_bytes(int B, int H, int page, int max_pages, 
 int kda_latent_decode_step(const void *q, const void *cache, const int *block_table, const int *lengths, int B, int H,
                            int pages, int page, int max_pages, int dc, int dr, int io_dtype, float scale, void *out,
                            float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Linear attention with one log-decay per token and value head, key heads shared by groups of value
+ * heads, the plain member of the family above:
+ *
+ *   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+ *
+ * Layouts, strides, packed documents, states and limits as for the gated delta rule, except:
+ *  - g : [B][H][T] in g_dtype, which is KDA_FP32 or io_dtype; any strides, 0 too (a constant per head);
+ *    g <= 0, and anything below -1000, -inf too, is a decay to zero.
+ *  - the t strides of q, k, v and dout are not negative, and 64 of them take less than 2^31 bytes
+ *    (KDA_ERR_SHAPE otherwise).
+ *  - launches below 2^32 work-items (KDA_ERR_SHAPE): 2^24 segments of 256 to 2048 tokens over all heads,
+ *    2^24 / (dk dv / 1024) sequences and heads, 2^24 pieces of 16 tokens of a head.
+ *  - What is not finite in q reaches its token's outputs; in v its channel of the outputs from its chunk
+ *    of 64 tokens on and of the state; in k or g its head's.
+ * What feeds the state keeps all 24 bits, also with bf16 inputs. */
+size_t kda_lin_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
+
+int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                      const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
+                      const int *cu_seqlens, int N, int Hk, int H, int T, int dk, int dv, int io_dtype, int g_dtype,
+                      float scale, const float *initial_state, void *out, float *final_state, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dout * out) + sum(dfinal_state * final_state), from the inputs alone.  dq, dk_out :
+ * [B][Hk][T][dk] (summed over the value heads of a key head), dv_out : [B][H][T][dv] in io_dtype, dg :
+ * [B][H][T] in g_dtype or NULL (not wanted), dinitial_state : [N][H][dv][dk] float32 or NULL; all
+ * contiguous.  The gradients of tokens that no document covers are written as zeros.  No float atomics.
+ * dg is what is left of a segment's sums of larger terms: where decays are strong its floor is these sums'
+ * rounding. */
+int kda_lin_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
+                      const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
+                      const void *dout, const kda_strides *dout_strides, const int *cu_seqlens, int N, int Hk, int H,
+                      int T, int dk, int dv, int io_dtype, int g_dtype, float scale, const float *initial_state,
+                      const float *dfinal_state, void *dq, void *dk_out, void *dv_out, void *dg, float *dinitial_state,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token per (batch, value head), the state updated in place.  Contiguous q, k : [B][Hk][dk],
+ * v, out : [B][H][dv], g : [B][H] in g_dtype, state : [B][H][dv][dk] float32.  q, k, v, state and out
+ * 16-byte aligned. */
+int kda_lin_decode_step(const void *q, const void *k, const void *v, const void *g, int B, int Hk, int H, int dk, int dv,
+                        int io_dtype, int g_dtype, float scale, float *state, void *out, hipStream_t stream);
 
 #ifdef __cplusplus
 }
