@@ -34,7 +34,9 @@ Latent attention, keys and values from one latent vector a token (latent.py):
     out, lse = kda.latent_attn_fwd(q, k, v, k_rope, return_lse=True)
     grads = kda.latent_attn_bwd(q, k, v, k_rope, out, lse, dout)     # dq, dk, dv, dk_rope
     out = kda.LatentAttnFunction.apply(q, k, v, k_rope)              # the same, under autograd
+    kda.latent_append(latent, k_rope, cache, block_table, lengths, freqs, q_rope=q_rope, q=q)   # new tokens' rows
     o_t = kda.latent_decode_step(q_t, cache, block_table, lengths, scale)
+    o = kda.latent_tree_step(q, cache, block_table, lengths, tree_mask, scale)   # drafted tokens
 """
 from __future__ import annotations
 
@@ -117,6 +119,12 @@ def lib():
         L.kda_latent_decode_workspace_bytes.restype = sz
         L.kda_latent_decode_step.argtypes = [vp] * 4 + [i] * 8 + [f, vp, vp, vp, sz, vp]
         L.kda_latent_decode_step.restype = i
+        L.kda_latent_append.argtypes = [vp] * 9 + [f] + [vp] * 6 + [i] * 10 + [vp]
+        L.kda_latent_append.restype = i
+        L.kda_latent_tree_workspace_bytes.argtypes = [i] * 8
+        L.kda_latent_tree_workspace_bytes.restype = sz
+        L.kda_latent_tree_step.argtypes = [vp] * 6 + [i] * 9 + [f, vp, vp, vp, sz, vp]
+        L.kda_latent_tree_step.restype = i
         L.kda_lin_workspace_bytes.argtypes = [i] * 9
         L.kda_lin_workspace_bytes.restype = sz
         L.kda_lin_chunk_fwd.argtypes = [vp, vp] * 4 + [vp] + [i] * 8 + [f] + [vp] * 4 + [sz, vp]
@@ -513,8 +521,8 @@ def decode_step(q, k, v, a, beta, state, g_min=-5.0, gate="bounded", out=None, s
 
 from .gdr import (GdrChunkFunction, gdr_chunk_bwd, gdr_chunk_bwd_varlen, gdr_chunk_fwd,  # noqa: E402
                   gdr_chunk_fwd_varlen, gdr_decode_step, gdr_workspace_bytes)
-from .latent import (LatentAttnFunction, latent_attn_bwd, latent_attn_bwd_varlen, latent_attn_fwd,  # noqa: E402
-                     latent_attn_fwd_varlen, latent_bwd_workspace_bytes, latent_decode_step,
-                     latent_decode_workspace_bytes)
+from .latent import (LatentAttnFunction, latent_append, latent_append_varlen, latent_attn_bwd,  # noqa: E402
+                     latent_attn_bwd_varlen, latent_attn_fwd, latent_attn_fwd_varlen, latent_bwd_workspace_bytes,
+                     latent_decode_step, latent_decode_workspace_bytes, latent_tree_step, latent_tree_workspace_bytes)
 from .lin import (LinChunkFunction, lin_chunk_bwd, lin_chunk_bwd_varlen, lin_chunk_fwd,  # noqa: E402
                   lin_chunk_fwd_varlen, lin_decode_step, lin_workspace_bytes)

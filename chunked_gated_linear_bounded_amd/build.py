@@ -43,6 +43,8 @@ UNITS = [
     ("kda_kernels_latent.hip", "kda_kernels_latent.o", []),
     ("kda_kernels_latent_bwd.hip", "kda_kernels_latent_bwd.o", []),
     ("kda_kernels_latent_decode.hip", "kda_kernels_latent_decode.o", []),
+    ("kda_kernels_latent_append.hip", "kda_kernels_latent_append.o", []),
+    ("kda_kernels_latent_tree.hip", "kda_kernels_latent_tree.o", []),
     ("kda_kernels_lin.hip", "kda_kernels_lin.o", []),
     ("kda_kernels_lin_bwd.hip", "kda_kernels_lin_bwd.o", []),
     ("kda_abi.cpp", "kda_abi.o", []),

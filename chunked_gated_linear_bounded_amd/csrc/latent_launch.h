@@ -45,4 +45,36 @@ bool latent_decode_grid_fits(const LatentLaunch &p);
 size_t latent_decode_bytes(const LatentLaunch &p);
 hipError_t launch_latent_decode(const LatentLaunch &p);
 
+// new tokens into the paged cache, and their queries' rotary part
+struct LatentAppendLaunch {
+    const void *latent, *kr, *qr, *weight;
+    long long sl[2], sk[2], sq[3];  // element strides b, t (qr: and head)
+    void *cache, *q;
+    const int *table, *lengths, *positions, *counts, *cu;
+    const float *freqs;
+    int N, B, T, H, pages, page, max_pages, dc;  // H 0: no queries
+    bool fp32, interleaved;
+    float eps;
+    hipStream_t stream;
+};
+bool latent_append_grid_fits(const LatentAppendLaunch &p);
+hipError_t launch_latent_append(const LatentAppendLaunch &p);
+
+// drafted tokens against the paged cache: q, out [B][T][H][..], lse [B][T][H]
+struct LatentTreeLaunch {
+    const void *q, *cache;
+    const int *table, *lengths, *counts;
+    const unsigned long long *mask;  // [B][T]
+    int B, T, H, pages, page, max_pages, dc;
+    bool fp32;
+    float scale;
+    void *out;
+    float *lse;
+    unsigned char *workspace;
+    hipStream_t stream;
+};
+bool latent_tree_grid_fits(const LatentTreeLaunch &p);
+size_t latent_tree_bytes(const LatentTreeLaunch &p);
+hipError_t launch_latent_tree(const LatentTreeLaunch &p);
+
 }  // namespace kda

@@ -186,3 +186,111 @@ def latent_decode_step(q, cache, block_table, lengths, scale, dc=512, out=None, 
     if st != KDA_OK:
         raise KdaError("kda_latent_decode_step", st)
     return (out, lse) if return_lse else out
+
+
+def _append(latent, k_rope, cache, block_table, lengths, freqs, cu_seqlens, norm_weight, eps, positions, counts, interleaved, q_rope, q,
+            stream):
+    if not all(isinstance(t, torch.Tensor) for t in (latent, k_rope, cache, block_table)):
+        raise TypeError("latent, k_rope, cache and block_table must be torch.Tensors")
+    dtype, dev = cache.dtype, cache.device
+    if dtype not in _DTYPES:
+        raise ValueError("unsupported dtype %s" % dtype)
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q go together")
+    dims = 3 if cu_seqlens is None else 2
+    if latent.dim() != dims or k_rope.dim() != dims or cache.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("latent, k_rope, cache and block_table must have %d, %d, 3 and 2 dimensions" % (dims, dims))
+    lead, dc, dr, (pages, page), (N, max_pages) = tuple(latent.shape[:-1]), latent.shape[-1], k_rope.shape[-1], cache.shape[:2], block_table.shape
+    if tuple(k_rope.shape[:-1]) != lead or cache.shape[2] != dc + dr or (cu_seqlens is None and lead[0] != N):
+        raise ValueError("shape mismatch")
+    T, H = lead[-1], 0
+    if q_rope is not None:
+        if not isinstance(q_rope, torch.Tensor) or not isinstance(q, torch.Tensor):
+            raise TypeError("q_rope and q must be torch.Tensors")
+        if q_rope.dim() != dims + 1 or tuple(q_rope.shape[:-2]) != lead or q_rope.shape[-1] != dr:
+            raise ValueError("q_rope must have shape %s, has %s" % (lead + ("H", dr), tuple(q_rope.shape)))
+        H = q_rope.shape[-2]
+    pl, sl = _view(latent, "latent", dtype, dev)
+    pk, sk = _view(k_rope, "k_rope", dtype, dev)
+    pr, sr = _view(q_rope, "q_rope", dtype, dev) if q_rope is not None else (None, None)
+    # (.., b, t) and (b, t, h) as the library's (b, h, t)
+    sl, sk = _S3(sl[1], 0, sl[2]), _S3(sk[1], 0, sk[2])
+    sr = None if sr is None else _S3(sr[0], sr[2], sr[1])
+    args = [_plain(cache, "cache", dtype, dev, (pages, page, dc + dr)),
+            _plain(block_table, "block_table", torch.int32, dev, (N, max_pages)), _plain(lengths, "lengths", torch.int32, dev, (N,)),
+            _plain(freqs, "freqs", torch.float32, dev, (dr // 2,)), _plain(norm_weight, "norm_weight", dtype, dev, (dc,)), float(eps),
+            _plain(positions, "positions", torch.int32, dev, lead), _plain(counts, "counts", torch.int32, dev, (N,)),
+            pr, sr, _plain(q, "q", dtype, dev, lead + (H, dc + dr)),
+            None if cu_seqlens is None else _plain(cu_seqlens, "cu_seqlens", torch.int32, dev, (N + 1,))]
+    with _on_device(dev):
+        st = lib().kda_latent_append(pl, sl, pk, sk, *args, N, T, H, pages, page, max_pages, dc, dr, _DTYPES[dtype], int(bool(interleaved)),
+                                     _stream_of(stream, dev))
+    if st != KDA_OK:
+        raise KdaError("kda_latent_append", st)
+    return cache
+
+
+def latent_append(latent, k_rope, cache, block_table, lengths, freqs, norm_weight=None, eps=1e-6, positions=None, counts=None,
+                  interleaved=True, q_rope=None, q=None, stream=None):
+    """Writes T new tokens a sequence into the paged cache that latent_decode_step and latent_tree_step read:
+    latent [B,T,dc], normalised by its root mean square and norm_weight [dc] where that is given, and
+    k_rope [B,T,dr], rotated; both may be strided views (the two parts of one projection).  lengths int32
+    [B] are those with the new tokens; counts int32 [B] how many of T are tokens (all by default): token i
+    becomes row lengths[b] - counts[b] + i.  A pair turns by position * freqs[i] (float32 [dr / 2]);
+    positions int32 [B,T], by default the rows'; pairs are neighbours (interleaved) or dr / 2 apart.  With
+    q_rope [B,T,H,dr], the queries' rotary part, its rotation goes into the last dr channels of q
+    [B,T,H,dc+dr].  Returns cache."""
+    return _append(latent, k_rope, cache, block_table, lengths, freqs, None, norm_weight, eps, positions, counts, interleaved, q_rope, q,
+                   stream)
+
+
+def latent_append_varlen(latent, k_rope, cache, block_table, lengths, freqs, cu_seqlens, norm_weight=None, eps=1e-6, positions=None,
+                         interleaved=True, q_rope=None, q=None, stream=None):
+    """latent_append of packed sequences: latent [T,dc], k_rope [T,dr], positions [T], q_rope [T,H,dr], q
+    [T,H,dc+dr]; boundaries int32 [N+1] on the GPU.  Tokens that no sequence covers are not written."""
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be a torch.Tensor")
+    return _append(latent, k_rope, cache, block_table, lengths, freqs, cu_seqlens, norm_weight, eps, positions, None, interleaved, q_rope, q,
+                   stream)
+
+
+def latent_tree_workspace_bytes(B, T, H, page, max_pages, dc, dr, dtype) -> int:
+    io = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(lib().kda_latent_tree_workspace_bytes(B, T, H, page, max_pages, dc, dr, io))
+
+
+def latent_tree_step(q, cache, block_table, lengths, tree_mask, scale, dc=512, counts=None, out=None, lse=None, return_lse=False,
+                     workspace=None, stream=None):
+    """Absorbed form, up to 64 drafted tokens per sequence, whose rows are the last of the cache
+    (latent_append): q [B,T,H,dc+dr]; cache, block_table, lengths and scale as for latent_decode_step, lengths
+    with the drafted tokens.  Every drafted token sees the rows before them, and of theirs those whose bits
+    are set in its tree_mask (int64 [B,T]; bit j: the token j of the sequence, its own among them: a chain
+    has 2 << i - 1).  counts int32 [B]: how many of T are tokens (all by default); the others give zeros.
+    Returns out [B,T,H,dc] (and the float32 log-sum-exps [B,T,H])."""
+    if not all(isinstance(t, torch.Tensor) for t in (q, cache, block_table, tree_mask)):
+        raise TypeError("q, cache, block_table and tree_mask must be torch.Tensors")
+    dtype, dev = q.dtype, q.device
+    if dtype not in _DTYPES:
+        raise ValueError("unsupported dtype %s" % dtype)
+    if dev.type != "cuda":
+        raise ValueError("q must be a GPU tensor")
+    if q.dim() != 4 or cache.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q, cache and block_table must have 4, 3 and 2 dimensions")
+    (B, T, H, D), (pages, page), max_pages = q.shape, cache.shape[:2], block_table.shape[1]
+    ptrs = [_plain(q, "q", dtype, dev, (B, T, H, D)), _plain(cache, "cache", dtype, dev, (pages, page, D)),
+            _plain(block_table, "block_table", torch.int32, dev, (B, max_pages)),
+            _plain(lengths, "lengths", torch.int32, dev, (B,)), _plain(counts, "counts", torch.int32, dev, (B,)),
+            _plain(tree_mask, "tree_mask", torch.int64, dev, (B, T))]
+    with _on_device(dev):
+        if out is None:
+            out = _empty((B, T, H, dc), dtype, dev, stream)
+        if lse is None:
+            lse = _empty((B, T, H), torch.float32, dev, stream)
+        need = latent_tree_workspace_bytes(B, T, H, page, max_pages, dc, D - dc, dtype)
+        workspace = _workspace(workspace, need, dev, stream)
+        st = lib().kda_latent_tree_step(*ptrs, B, T, H, pages, page, max_pages, dc, D - dc, _DTYPES[dtype], float(scale),
+                                        _plain(out, "out", dtype, dev, (B, T, H, dc)), _plain(lse, "lse", torch.float32, dev, (B, T, H)),
+                                        workspace.data_ptr(), workspace.numel(), _stream_of(stream, dev))
+    if st != KDA_OK:
+        raise KdaError("kda_latent_tree_step", st)
+    return (out, lse) if return_lse else out

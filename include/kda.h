@@ -85,7 +85,8 @@ typedef enum {
     KDA_ERR_MODE = -9,      /* gate_mode unknown                                */
     KDA_ERR_SCRATCH = -10,  /* kda_chunk_fwd_noalloc: the problem needs more than
                                KDA_NOALLOC_SCRATCH_BYTES of device scratch      */
-    KDA_ERR_SCALE = -11     /* scale not finite, or (latent attention) not positive */
+    KDA_ERR_SCALE = -11     /* scale not finite, or (latent attention) not positive; eps not finite
+                               or negative                                      */
 } kda_status;
 
 /* Bytes of device scratch that kda_chunk_fwd_noalloc works in: a static device array of the
@@ -415,6 +416,51 @@ size_t kda_latent_decode_workspace_bytes(int B, int H, int page, int max_pages, 
 int kda_latent_decode_step(const void *q, const void *cache, const int *block_table, const int *lengths, int B, int H,
                            int pages, int page, int max_pages, int dc, int dr, int io_dtype, float scale, void *out,
                            float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* New tokens into the paged cache that kda_latent_decode_step and kda_latent_tree_step read, and the
+ * rotary part of their queries:
+ *   row = [latent / sqrt(mean latent^2 + eps) norm_weight, R(position) k_rope],   q[.. dc, dc + dr) = R(position) q_rope;
+ * R turns pair i of a rotary part by position * freqs[i]: the elements 2 i and 2 i + 1 (interleaved) or i
+ * and i + dr / 2.
+ *  - latent : [B][T][dc], k_rope : [B][T][dr], q_rope : [B][T][H][dr] in io_dtype, each with element strides
+ *    b, t and (q_rope) h (NULL: contiguous), any sign; the last dimension is contiguous and every row
+ *    starts at a multiple of 16 bytes.  q : [B][T][H][dc + dr] contiguous; only its last dr channels are
+ *    written.  H = 0: no queries (q_rope and q NULL).  norm_weight : [dc] in io_dtype, or NULL: the latent
+ *    as it is.  freqs : [dr / 2] float32.  positions : [B][T] int32, or NULL: the rows' numbers.
+ *  - cache : [pages][page][dc + dr], block_table : [B][max_pages], lengths : [B] as for
+ *    kda_latent_decode_step; lengths are those with the new tokens.  counts : [B] int32, clipped to 0 .. T:
+ *    how many of a sequence's T are tokens (NULL: all).  Token i of sequence b becomes row
+ *    lengths[b] - counts[b] + i.
+ *  - cu_seqlens not NULL: packed streams of T tokens ([T][dc], [T][dr], [T][H][..], strides b unused) and N
+ *    sequences, boundaries clipped to the stream; counts is NULL then (KDA_ERR_NULL otherwise).
+ *  - A token whose row is negative, behind the table, or on a page outside the cache is not written into
+ *    the cache; what is no token (behind its sequence's count, outside the boundaries) is not written at
+ *    all.  Two tokens on one row (a page twice in the table) leave one of the two.
+ *  - dc in {256, 512}, dr = 64; eps >= 0 (KDA_ERR_SCALE otherwise); a launch below 2^32 work-items
+ *    (KDA_ERR_SHAPE): 2^26 tokens and 32 heads. */
+int kda_latent_append(const void *latent, const kda_strides *latent_strides, const void *k_rope,
+                      const kda_strides *k_rope_strides, void *cache, const int *block_table, const int *lengths,
+                      const float *freqs, const void *norm_weight, float eps, const int *positions, const int *counts,
+                      const void *q_rope, const kda_strides *q_rope_strides, void *q, const int *cu_seqlens, int N, int T,
+                      int H, int pages, int page, int max_pages, int dc, int dr, int io_dtype, int interleaved,
+                      hipStream_t stream);
+
+/* Absorbed form, T drafted tokens per sequence (1 <= T <= 64), whose rows are the sequence's last: with
+ * n = counts[b] (clipped to 0 .. T; counts NULL: T) token i sees the rows before lengths[b] - n, and row
+ * lengths[b] - n + j where bit j of tree_mask[b][i] is set, j < n.  Bit i is its own row: a chain has
+ * (2 << i) - 1.  A token that sees no row, and one behind the count, gives zeros and -inf.
+ *  - q : [B][T][H][dc + dr], out : [B][T][H][dc] in io_dtype, lse : [B][T][H] float32, tree_mask : [B][T]
+ *    64 bits (8-byte aligned); cache, block_table, lengths and what is out of range as for
+ *    kda_latent_decode_step; all contiguous, on the device.
+ *  - What is not finite in a drafted row leaves NaN in the out and lse of the tokens that see it and of no
+ *    others; in q in its head's; in another row, or a score that overflows, in every token's out.
+ *  - dc in {256, 512}, dr = 64; B and H up to 65535, launches below 2^32 work-items.
+ * workspace: kda_latent_tree_workspace_bytes(...) bytes (may be 0). */
+size_t kda_latent_tree_workspace_bytes(int B, int T, int H, int page, int max_pages, int dc, int dr, int io_dtype);
+int kda_latent_tree_step(const void *q, const void *cache, const int *block_table, const int *lengths, const int *counts,
+                         const unsigned long long *tree_mask, int B, int T, int H, int pages, int page, int max_pages, int dc,
+                         int dr, int io_dtype, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                         hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * Linear attention with one log-decay per token and value head, key heads shared by groups of value
