@@ -22,7 +22,7 @@ size_t latent_tree_bytes(const LatentTreeLaunch &p) {
     return n == 1 ? 0 : (size_t)p.B * n * rows(p) * (p.dc + 1) * 4;
 }
 bool latent_tree_grid_fits(const LatentTreeLaunch &p) {
-    return ((long long)p.B * splits(p) + 7) / 8 * 8 * groups(p) <= 4294967295LL / 256 && p.B * rows(p) <= 4294967295LL / 128;
+    return ((long long)p.B * splits(p) * groups(p) + 7) / 8 * 8 <= 4294967295LL / 256 && p.B * rows(p) <= 4294967295LL / 128;
 }
 
 template <int DC, bool F32, int NQ>
@@ -30,7 +30,7 @@ static hipError_t run(const LatentTreeLaunch &p) {
     LatentTreeArgs a{p.q, p.cache, p.table, p.lengths, p.counts, p.mask, p.B, p.T, p.H, p.pages, p.page, p.max_pages, splits(p), groups(p),
                      p.scale, p.out, p.lse, reinterpret_cast<float *>(p.workspace), nullptr};
     a.part_lse = a.part + (size_t)p.B * a.nsplit * rows(p) * DC;
-    const unsigned grid = (unsigned)((p.B * (long long)a.nsplit + 7) / 8 * 8) * (unsigned)a.rgroups;
+    const unsigned grid = (unsigned)((p.B * (long long)a.nsplit * a.rgroups + 7) / 8 * 8);
     hipLaunchKernelGGL((latent_tree_kernel<DC, 64, F32, NQ>), dim3(grid), dim3(256), 0, p.stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.nsplit == 1) return e;

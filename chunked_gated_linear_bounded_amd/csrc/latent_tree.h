@@ -128,7 +128,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int D = DC + DR, NKB = D / 32, NT = DC / 64, FB = Op::FB, NBUF = F32 ? 1 : 2, TILE = 4 * NKB * FB, NL = Op::NL;
-    constexpr int ES = (int)sizeof(E);
+    constexpr int ES = (int)sizeof(E), AHEAD = F32 ? 1 : 3;
     typedef __attribute__((address_space(3))) float lds_f;
     typedef __attribute__((address_space(3))) int lds_i;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * TILE];
@@ -140,8 +140,10 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
     lds_i *sgrown = (lds_i *)lds_base(sgrown_);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int unit = blockIdx.x / (8 * p.rgroups) * 8 + (blockIdx.x & 7), rg = (blockIdx.x >> 3) % p.rgroups;
-    if (unit >= p.B * p.nsplit) return;
+    // work-groups in eight runs, one an XCD: those on the same keys are neighbours there
+    const unsigned all = (unsigned)p.B * p.nsplit * p.rgroups, run = (all + 7) / 8, at_ = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= run || at_ >= all) return;
+    const int unit = at_ / p.rgroups, rg = at_ % p.rgroups;
     const int b = unit / p.nsplit, split = unit % p.nsplit, R = p.T * p.H, row0 = rg * 16 * NQ;
     int len, per;
     const int ntile = p.tiles(b, len, per), count = p.counts ? AttnSeqs::clip(p.counts[b], p.T) : p.T;
@@ -169,7 +171,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
         for (int x = 0; x < NQ; ++x)
 #pragma unroll
             for (int kb = 0; kb < NKB; ++kb)
-                if ((x * NKB + kb) * 4 < 240) asm volatile("" : "+a"(qf[x][kb]));
+                if ((x * NKB + kb) * 4 < 256) asm volatile("" : "+a"(qf[x][kb]));
     }
     // rows of a tile: a lane's key(s), past the last the last; pages outside the cache are clipped
     const int *table = p.table + (size_t)b * p.max_pages;
@@ -179,14 +181,21 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
 #pragma unroll
         for (int i = 0; i < NL; ++i) pg[i] = table[key_of(tile, i) / p.page];
     };
-    auto load = [&](int tile, lds_u8 *to) {
+    const E *from[NL];
+    auto find = [&](int tile) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const int at = pg[i] < 0 ? 0 : (pg[i] >= p.pages ? p.pages - 1 : pg[i]);
-            const E *row = cache + ((long long)at * p.page + key_of(tile, i) % p.page) * D + Op::load_col(lane, i);
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) direct_load<32 * ES>(row, (to + (w * NKB + kb) * FB + 1024 * i), kb);
+            from[i] = cache + ((long long)at * p.page + key_of(tile, i) % p.page) * D + Op::load_col(lane, i);
         }
+    };
+    auto load = [&](lds_u8 *to, int kb) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) direct_load<32 * ES>(from[i], to + (w * NKB + kb) * FB + 1024 * i, kb);
+    };
+    auto load_all = [&](lds_u8 *to) {
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) load(to, kb);
     };
     f32x4 O[NT][NQ];
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -202,7 +211,8 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
     }
     if (first < last) {
         fetch(first);
-        load(first, sk);
+        find(first);
+        load_all(sk);
         fetch(first + 1);
     }
     for (int tile = first; tile < last; ++tile) {
@@ -210,12 +220,8 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
         lds_u8 *here = sk + (NBUF == 2 ? par * TILE : 0);
         wait_vmcnt<0>();
         barrier_lds();  // the tile is there, and the other buffer has been read
-        if constexpr (NBUF == 2) {
-            if (tile + 1 < last) {
-                load(tile + 1, sk + (par ^ 1) * TILE);
-                fetch(tile + 2);
-            }
-        }
+        find(tile + 1);  // behind the last tile its last row again
+        fetch(tile + 2);
         f32x4 s[NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x) s[x] = zero;
@@ -237,11 +243,18 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
             const unsigned long long k = __builtin_amdgcn_ballot_w64(bad);
             badrows = (unsigned)(k | k >> 16 | k >> 32 | k >> 48) & 0xffff;
         }
+        // fragments AHEAD steps before their MFMAs, in this order: left alone, the scheduler reads each one
+        // right before its use, and the wave waits; a piece of the next tile is asked for in each step
+        V8 ring[AHEAD + 1];
+#pragma unroll
+        for (int kb = 0; kb < AHEAD; ++kb) ring[kb] = Op::get(mine + kb * FB, lane);
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb) {
-            const V8 kf = Op::get(mine + kb * FB, lane);
+            if (kb + AHEAD < NKB) ring[(kb + AHEAD) % (AHEAD + 1)] = Op::get(mine + (kb + AHEAD) * FB, lane);
+            if constexpr (NBUF == 2) load(sk + (par ^ 1) * TILE, kb);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) s[x] = Op::mma(kf, qf[x][kb], s[x]);
+            for (int x = 0; x < NQ; ++x) s[x] = Op::mma(ring[kb % (AHEAD + 1)], qf[x][kb], s[x]);
         }
         if (edge) {
 #pragma unroll
@@ -297,29 +310,32 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
         }
 #pragma unroll
         for (int x = 0; x < NQ; ++x) l[x] += (P[x][0] + P[x][1]) + (P[x][2] + P[x][3]);
+        auto value = [&](int k) {  // step k: keys 32 (k / NT) .., channel tile k % NT
+            const int tt = w * NT + k % NT;
+            const lds_u8 *f = here + (k / NT * 2 * NKB + (tt >> 1)) * FB;
+            return Op::get_t(f, f + NKB * FB, tt & 1, lane);
+        };
+        V8 pf[NQ];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            V8 pf[NQ];
+        for (int k = 0; k < AHEAD; ++k) ring[k] = value(k);
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) pf[x] = Op::get_lane(sp + (kb * NQ + x) * FB, lane);
+        for (int k = 0; k < 2 * NT; ++k) {
+            if (k % NT == 0) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int tt = w * NT + t;
-                const lds_u8 *f = here + (2 * kb * NKB + (tt >> 1)) * FB;
-                const V8 vf = Op::get_t(f, f + NKB * FB, tt & 1, lane);
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) O[t][x] = Op::mma(vf, pf[x], O[t][x]);
+                for (int x = 0; x < NQ; ++x) pf[x] = Op::get_lane(sp + (k / NT * NQ + x) * FB, lane);
             }
+            if (k + AHEAD < 2 * NT) ring[(k + AHEAD) % (AHEAD + 1)] = value(k + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) O[k % NT][x] = Op::mma(ring[k % (AHEAD + 1)], pf[x], O[k % NT][x]);
         }
         if constexpr (NBUF == 1) {
-            if (tile + 1 < last) {
-                barrier_lds();  // the tile has been read
-                load(tile + 1, sk);
-                fetch(tile + 2);
-            }
+            barrier_lds();  // the tile has been read
+            if (tile + 1 < last) load_all(sk);
         }
     }
-    // the sum over the waves' keys
+    // the sum over the waves' keys; the loads behind the last tile end before the wave does
+    wait_vmcnt<0>();
     barrier_lds();
 #pragma unroll
     for (int x = 0; x < NQ; ++x) {
