@@ -17,12 +17,13 @@
 // scaled a few times a row and not every tile: a wave makes P with the maximum it has, says whether a row
 // has outgrown it, and only where one has all four waves agree on new maxima and make P again.
 //
-// Fragments are 64 slots of 16 bytes, lane (g, m) at slot 16 g + (m ^ 4 g) as in gdr_common.h: a direct
-// load fills one KiB in lane order, so slots cannot be cut in planes as latent_common.h does.  The
-// transposed read of 16 channels takes their 8-byte halves of a slot; with the same half of every slot,
-// every second pair of banks would idle.  So channel tile o of a column block takes half o of the first
-// two column groups and half 1 - o of the other two, and a lane's pair of channel tiles changes places where
-// g >= 2.
+// A fragment (16 rows x 32 channels) is rows of 64 bytes, because a direct load fills LDS in lane order and
+// is fast where four neighbouring lanes read one row: with a row a lane it made 64 accesses to the cache in
+// place of 16 and took most of the time.  Row m's four 16-byte pieces are exchanged by m / 4, which puts the
+// 16 lanes of a plain read on all banks.  The transposed read of 16 channels takes 8-byte halves; with the
+// same half of every piece it would meet its neighbour's banks.  So channel tile o of a column block takes
+// half o of the even pieces and half 1 - o of the odd ones, and a lane's pair of channel tiles changes
+// places where g is odd.
 #pragma once
 #include "latent_common.h"
 
@@ -55,17 +56,18 @@ template <bool F32> struct TreeOp;
 template <> struct TreeOp<false> : AttnOp<false> {
     static constexpr int NL = 1;  // direct loads a fragment
     // row of the fragment that lane `lane` of load i fills, and the element of the row it starts at
-    __device__ __forceinline__ static int load_row(int lane, int) { return (lane & 15) ^ (4 * (lane >> 4)); }
-    __device__ __forceinline__ static int load_col(int lane, int) { return 8 * (lane >> 4); }
+    __device__ __forceinline__ static int load_row(int lane, int) { return lane >> 2; }
+    __device__ __forceinline__ static int load_col(int lane, int) { return 8 * ((lane & 3) ^ (lane >> 4)); }
+    __device__ __forceinline__ static int slot(int piece, int m) { return 64 * m + 16 * (piece ^ (m >> 2)); }
     __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
-        return *reinterpret_cast<const lds_b8 *>(f + frag_slot(lane >> 4, lane & 15));
+        return *reinterpret_cast<const lds_b8 *>(f + slot(lane >> 4, lane & 15));
     }
     __device__ __forceinline__ static void put(lds_u8 *f, int lane, const V8 &x) {
-        *reinterpret_cast<lds_b8 *>(f + frag_slot(lane >> 4, lane & 15)) = x;
+        *reinterpret_cast<lds_b8 *>(f + slot(lane >> 4, lane & 15)) = x;
     }
     __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int o, int lane) {
         const int g = lane >> 4, s = lane & 15, cg = s & 3;
-        const int off = frag_slot(cg, 4 * g + (s >> 2)) + 8 * (o ^ (cg >> 1));
+        const int off = slot(cg, 4 * g + (s >> 2)) + 8 * (o ^ (cg & 1));
         const bf16x4 a = ld_tr16<bf16x4>(f0 + off), b = ld_tr16<bf16x4>(f1 + off);
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
@@ -91,10 +93,29 @@ template <> struct TreeOp<false> : AttnOp<false> {
 };
 template <> struct TreeOp<true> : AttnOp<true> {
     static constexpr int NL = 2;
-    __device__ __forceinline__ static int load_row(int lane, int i) { return ((lane >> 1) & 15) ^ (4 * (2 * i + (lane >> 5))); }
-    __device__ __forceinline__ static int load_col(int lane, int i) { return 8 * (2 * i + (lane >> 5)) + 4 * (lane & 1); }
-    __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) { return AttnOp<true>::get(f, 0, lane); }
-    __device__ __forceinline__ static void put(lds_u8 *f, int lane, const V8 &x) { AttnOp<true>::put(f, 0, lane >> 4, lane & 15, x); }
+    __device__ __forceinline__ static int load_row(int lane, int i) { return 8 * i + (lane >> 3); }
+    __device__ __forceinline__ static int load_col(int lane, int i) { return 4 * ((lane & 7) ^ (load_row(lane, i) >> 1)); }
+    __device__ __forceinline__ static int slot(int piece, int m) { return 128 * m + 16 * (piece ^ (m >> 1)); }
+    __device__ __forceinline__ static V8 get(const lds_u8 *f, int lane) {
+        const int g = lane >> 4, m = lane & 15;
+        return V8{*reinterpret_cast<const lds_f4 *>(f + slot(2 * g, m)), *reinterpret_cast<const lds_f4 *>(f + slot(2 * g + 1, m))};
+    }
+    __device__ __forceinline__ static void put(lds_u8 *f, int lane, const V8 &x) {
+        const int g = lane >> 4, m = lane & 15;
+        *reinterpret_cast<lds_f4 *>(f + slot(2 * g, m)) = x.a;
+        *reinterpret_cast<lds_f4 *>(f + slot(2 * g + 1, m)) = x.b;
+    }
+    __device__ __forceinline__ static V8 get_t(const lds_u8 *f0, const lds_u8 *f1, int o, int lane) {
+        const int g = lane >> 4, m = lane & 15;
+        V8 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int off = slot(2 * (m >> 2) + o, 4 * g + j) + 4 * (m & 3);
+            r.a[j] = *reinterpret_cast<const __attribute__((address_space(3))) float *>(f0 + off);
+            r.b[j] = *reinterpret_cast<const __attribute__((address_space(3))) float *>(f1 + off);
+        }
+        return r;
+    }
     static constexpr bool kSwap = false;
     __device__ __forceinline__ static void put_half(lds_u8 *f, int lane, int h, const f32x4 &x) {
         *reinterpret_cast<lds_f4 *>(f + 16 * lane + 1024 * h) = x;
@@ -357,7 +378,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
             E *o = reinterpret_cast<E *>(p.out) + ((size_t)b * R + row) * DC + w * (DC / 4) + 8 * g;
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
-                const bool swap = Op::kSwap && g >= 2;
+                const bool swap = Op::kSwap && (g & 1);
                 f32x4 u = swap ? O[t + 1][x] : O[t][x], v = swap ? O[t][x] : O[t + 1][x];
                 u = none ? zero : u * inv;
                 v = none ? zero : v * inv;
@@ -371,7 +392,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
             float *o = p.part + at * DC + w * (DC / 4) + 8 * g;
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
-                const bool swap = Op::kSwap && g >= 2;
+                const bool swap = Op::kSwap && (g & 1);
                 f32x4 u = swap ? O[t + 1][x] : O[t][x], v = swap ? O[t][x] : O[t + 1][x];
                 u = none ? zero : u * inv;
                 v = none ? zero : v * inv;
