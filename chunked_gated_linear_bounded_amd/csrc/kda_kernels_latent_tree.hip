@@ -8,34 +8,42 @@ namespace kda {
 
 static long long rows(const LatentTreeLaunch &p) { return (long long)p.T * p.H; }
 // column tiles of 16 rows a work-group takes (float32: the queries of 32 rows fill the registers)
-static int tiles(const LatentTreeLaunch &p) { return rows(p) <= 16 ? 1 : rows(p) <= 32 || p.fp32 ? 2 : 4; }
-static int groups(const LatentTreeLaunch &p) { return (int)((rows(p) + 16 * tiles(p) - 1) / (16 * tiles(p))); }
-// parts the keys are cut into: up to 512 work-groups, each with at least 64 keys of the longest sequence
-// that the table can hold (the lengths are on the device)
-static int splits(const LatentTreeLaunch &p) {
-    const long long want = 512 / ((long long)p.B * groups(p)), most = ((long long)p.max_pages * p.page + 63) / 64;
-    const long long n = want < most ? want : most;
-    return n < 1 ? 1 : (n > 64 ? 64 : (int)n);
+static int tiles(const LatentTreeLaunch &p) {
+    const int most = rows(p) <= 16 ? 1 : rows(p) <= 32 || p.fp32 ? 2 : 4;
+    const long long keys = ((long long)p.max_pages * p.page + 63) / 64;
+    for (int n = most; n > 1; n /= 2)
+        if (p.B * ((rows(p) + 16 * n - 1) / (16 * n)) * keys >= 512) return n;
+    return 1;
 }
+static int groups(const LatentTreeLaunch &p) { return (int)((rows(p) + 16 * tiles(p) - 1) / (16 * tiles(p))); }
+// Work-groups that share all tiles evenly (latent_tree.h), one a CU, as long as the units alone do not fill
+// the card four times over, and no more than there can be tiles; 0: one a unit.
+static int shared(const LatentTreeLaunch &p) {
+    const long long units = (long long)p.B * groups(p), most = units * (((long long)p.max_pages * p.page + 63) / 64);
+    return units >= 1024 ? 0 : most < 256 ? (int)most : 256;
+}
+static size_t part_rows(const LatentTreeLaunch &p) { return 2 * (size_t)shared(p) * 16 * tiles(p); }
 size_t latent_tree_bytes(const LatentTreeLaunch &p) {
-    const int n = splits(p);
-    return n == 1 ? 0 : (size_t)p.B * n * rows(p) * (p.dc + 1) * 4;
+    return shared(p) <= 1 ? 0 : part_rows(p) * (p.dc + 1) * 4 + ((size_t)p.B + 2) * 4;
 }
 bool latent_tree_grid_fits(const LatentTreeLaunch &p) {
-    return ((long long)p.B * splits(p) * groups(p) + 7) / 8 * 8 <= 4294967295LL / 256 && p.B * rows(p) <= 4294967295LL / 128;
+    const long long units = (long long)p.B * groups(p), tiles = ((long long)p.max_pages * p.page + 63) / 64;
+    return (units + 7) / 8 * 8 <= 4294967295LL / 256 && (units >= 1024 || units * tiles <= 2147483647LL);
 }
 
 template <int DC, bool F32, int NQ>
 static hipError_t run(const LatentTreeLaunch &p) {
-    LatentTreeArgs a{p.q, p.cache, p.table, p.lengths, p.counts, p.mask, p.B, p.T, p.H, p.pages, p.page, p.max_pages, splits(p), groups(p),
-                     p.scale, p.out, p.lse, reinterpret_cast<float *>(p.workspace), nullptr};
-    a.part_lse = a.part + (size_t)p.B * a.nsplit * rows(p) * DC;
-    const unsigned grid = (unsigned)((p.B * (long long)a.nsplit * a.rgroups + 7) / 8 * 8);
-    hipLaunchKernelGGL((latent_tree_kernel<DC, 64, F32, NQ>), dim3(grid), dim3(256), 0, p.stream, a);
+    LatentTreeArgs a{p.q, p.cache, p.table, p.lengths, p.counts, p.mask, p.B, p.T, p.H, p.pages, p.page, p.max_pages, groups(p),
+                     p.scale, p.out, p.lse, shared(p), reinterpret_cast<float *>(p.workspace), nullptr, nullptr};
+    if (a.groups == 1) a.groups = 0;  // one unit of one tile
+    a.part_lse = a.part + part_rows(p) * DC;
+    a.from = reinterpret_cast<int *>(a.part_lse + part_rows(p));
+    const long long all = a.groups > 0 ? a.groups : (long long)p.B * a.rgroups;
+    hipLaunchKernelGGL((latent_tree_kernel<DC, 64, F32, NQ>), dim3((unsigned)((all + 7) / 8 * 8)), dim3(256), 0, p.stream, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.nsplit == 1) return e;
-    const long long joins = (p.B * rows(p) + 1024 / DC - 1) / (1024 / DC);
-    hipLaunchKernelGGL((latent_tree_join_kernel<DC, typename AttnOp<F32>::E>), dim3((unsigned)joins), dim3(256), 0, p.stream, a);
+    if (e != hipSuccess || a.groups == 0) return e;
+    hipLaunchKernelGGL((latent_tree_join_kernel<DC, NQ, typename AttnOp<F32>::E>), dim3(a.groups, 16 * NQ * DC / 1024),
+                       dim3(256), 0, p.stream, a);
     return hipGetLastError();
 }
 template <int DC, bool F32>

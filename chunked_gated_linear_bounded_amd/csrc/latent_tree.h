@@ -36,20 +36,23 @@ struct LatentTreeArgs {
     const int *lengths;        // [B]
     const int *counts;         // [B] (NULL: T)
     const unsigned long long *mask;  // [B][T]
-    int B, T, H, pages, page, max_pages, nsplit, rgroups;
+    int B, T, H, pages, page, max_pages, rgroups;
     float scale;
     void *out;                 // [B][T][H][dc]
     float *lse;                // [B][T][H]
-    float *part, *part_lse;    // nsplit > 1: [B][nsplit][T H][dc]; [B][nsplit][T H] log-sum-exps (log2)
-    // 64-key tiles of sequence b, and of each of its parts
-    __device__ __forceinline__ int tiles(int b, int &len, int &per) const {
+    // groups > 0: that many work-groups share the tiles of all units evenly, and what each has of its first
+    // and last unit goes to part, [2 groups][rows of a unit][dc], and part_lse (log2); from: [B + 1], the
+    // first tile of sequence b's units, and [B + 1 ..] the tiles of a work-group.  0: a work-group a unit.
+    int groups;
+    float *part, *part_lse;
+    int *from;
+    __device__ __forceinline__ int length(int b) const {
         const long long most = (long long)max_pages * page;
         const int given = lengths[b];
-        len = given < 0 ? 0 : (given > most ? (int)most : given);
-        const int n = (len + 63) / 64;
-        per = (n + nsplit - 1) / nsplit;
-        return n;
+        return given < 0 ? 0 : (given > most ? (int)most : given);
     }
+    // 64-key tiles of one of sequence b's units; one at least, so that somebody writes its rows
+    __device__ __forceinline__ int tiles(int b) const { return max(1, (length(b) + 63) / 64); }
 };
 
 template <bool F32> struct TreeOp;
@@ -133,14 +136,27 @@ template <> struct TreeOp<true> : AttnOp<true> {
     }
 };
 
-// Lane l's 16 bytes at `src` + STEP kb to dst + 16 l, past the registers.  In assembly, because behind the
-// builtin every LDS read waits for all direct loads, those of the other buffer too; the caller waits with
-// wait_vmcnt.  The instruction adds its offset to both addresses.
-template <int STEP>
-__device__ __forceinline__ void direct_load(const void *src, lds_u8 *dst, int kb) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%2" ::"v"(src),
-                 "s"(__builtin_amdgcn_readfirstlane((int)(unsigned)(size_t)dst - STEP * kb)), "n"(STEP * kb)
-                 : "memory", "m0");
+// Lane l's 16 bytes at `src` + STEP kb to the LDS address `to` (the same in all lanes) + FB kb + off + 16 l,
+// past the registers.  In assembly, because behind the builtin every LDS read waits for all direct loads,
+// those of the other buffer too; the caller waits with wait_vmcnt.  The instruction adds its offset to both
+// addresses.
+template <int STEP, int FB>
+__device__ __forceinline__ void direct_load(const void *src, int to, int kb, int off) {
+    asm volatile("s_add_u32 m0, %1, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%2" ::"v"(src), "s"(to), "n"(STEP * kb),
+                 "n"(FB * kb + off - STEP * kb)
+                 : "memory", "m0", "scc");
+}
+// A lane's number that what comes after it is computed from on the spot: what the edges and the ends need
+// would otherwise be kept in registers across the tiles, which have none left.
+__device__ __forceinline__ int lane_here(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+// A barrier and nothing else: LDS reads in flight stay in flight.
+__device__ __forceinline__ void barrier_only() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
 template <int DC, int DR, bool F32, int NQ>
@@ -149,282 +165,402 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
     using E = typename Op::E;
     using V8 = typename Op::V8;
     constexpr int D = DC + DR, NKB = D / 32, NT = DC / 64, FB = Op::FB, NBUF = F32 ? 1 : 2, TILE = 4 * NKB * FB, NL = Op::NL;
-    constexpr int ES = (int)sizeof(E), AHEAD = F32 ? 1 : 3;
+    constexpr int ES = (int)sizeof(E), AHEAD = F32 ? 1 : 3, RING = AHEAD + 1, NV = 2 * NT;  // NV: steps of the value products
+    static_assert(NBUF == 1 || NV % RING == 0, "the ring's places carry on from the values into the next scores");
     typedef __attribute__((address_space(3))) float lds_f;
     typedef __attribute__((address_space(3))) int lds_i;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF * TILE];
     __shared__ __attribute__((aligned(1024))) unsigned char sp_[2 * NQ * FB];
-    __shared__ float smax_[2 * 4 * 16 * NQ];  // by tile parity: waves' maxima of their keys
-    __shared__ int sgrown_[2 * 4];
+    __shared__ float smax_[4 * 16 * NQ];
+    __shared__ int sgrown_[2 * 4];  // by tile parity
     lds_u8 *sk = lds_base(smem), *sp = lds_base(sp_);
     lds_f *smax = (lds_f *)lds_base(smax_);
     lds_i *sgrown = (lds_i *)lds_base(sgrown_);
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // work-groups in eight runs, one an XCD: those on the same keys are neighbours there
-    const unsigned all = (unsigned)p.B * p.nsplit * p.rgroups, run = (all + 7) / 8, at_ = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= run || at_ >= all) return;
-    const int unit = at_ / p.rgroups, rg = at_ % p.rgroups;
-    const int b = unit / p.nsplit, split = unit % p.nsplit, R = p.T * p.H, row0 = rg * 16 * NQ;
-    int len, per;
-    const int ntile = p.tiles(b, len, per), count = p.counts ? AttnSeqs::clip(p.counts[b], p.T) : p.T;
-    const int base = len - count;  // the first drafted row; below 0 where fewer rows than drafted tokens are there
-    // rows of tokens past the count see nothing
-    const int first = split * per, last = row0 / p.H >= count ? first : min(first + per, ntile);
+    const int R = p.T * p.H;
     const E *cache = reinterpret_cast<const E *>(p.cache);
     const float c = p.scale * kLog2e;
 
-    V8 qf[NQ][NKB];
-    unsigned long long bits[NQ];  // the drafted rows that a lane's row sees
-    bool dead[NQ];
+    // what this work-group does: `left` tiles from tile t0 of unit (b, rg) on.  Work-groups in eight runs, one
+    // an XCD: those on the same keys are neighbours there.
+    const unsigned all = p.groups > 0 ? p.groups : (unsigned)p.B * p.rgroups, run = (all + 7) / 8;
+    const unsigned me = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= run || me >= all) return;
+    int b, rg, t0 = 0, left;
+    if (p.groups > 0) {
+        // tiles in front of each sequence: 256 sequences a step
+        lds_i *si = (lds_i *)lds_base(smem);
+        int total = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 256) {
+            int x = b0 + tid < p.B ? p.tiles(b0 + tid) * p.rgroups : 0;
+            const int mine = x;
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        const int row = min(row0 + 16 * x + n, R - 1), node = row / p.H;
-        bits[x] = p.mask[(size_t)b * p.T + node];
-        dead[x] = node >= count;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-            qf[x][kb] = Op::load(reinterpret_cast<const E *>(p.q) + ((size_t)b * R + row) * D + 32 * kb + 8 * g);
-    }
-    // as many as fit stay in accumulation registers, where MFMAs take operands from as well
-    if constexpr (!F32 && NQ * NKB * 4 > 128) {
-#pragma unroll
-        for (int x = 0; x < NQ; ++x)
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb)
-                if ((x * NKB + kb) * 4 < 256) asm volatile("" : "+a"(qf[x][kb]));
-    }
-    // rows of a tile: a lane's key(s), past the last the last; pages outside the cache are clipped
-    const int *table = p.table + (size_t)b * p.max_pages;
-    auto key_of = [&](int tile, int i) { return min(64 * min(tile, last - 1) + perm_row(w, Op::load_row(lane, i)), len - 1); };
-    int pg[NL];
-    auto fetch = [&](int tile) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) pg[i] = table[key_of(tile, i) / p.page];
-    };
-    const E *from[NL];
-    auto find = [&](int tile) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int at = pg[i] < 0 ? 0 : (pg[i] >= p.pages ? p.pages - 1 : pg[i]);
-            from[i] = cache + ((long long)at * p.page + key_of(tile, i) % p.page) * D + Op::load_col(lane, i);
-        }
-    };
-    auto load = [&](lds_u8 *to, int kb) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) direct_load<32 * ES>(from[i], to + (w * NKB + kb) * FB + 1024 * i, kb);
-    };
-    auto load_all = [&](lds_u8 *to) {
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) load(to, kb);
-    };
-    f32x4 O[NT][NQ];
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int x = 0; x < NQ; ++x) O[t][x] = zero;
-    float m[NQ], l[NQ];  // the rows' maximum (log2 units); the wave's keys' part of their sum
-#pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        m[x] = -INFINITY;
-        l[x] = 0.f;
-    }
-    if (first < last) {
-        fetch(first);
-        find(first);
-        load_all(sk);
-        fetch(first + 1);
-    }
-    for (int tile = first; tile < last; ++tile) {
-        const int par = (tile - first) & 1;
-        lds_u8 *here = sk + (NBUF == 2 ? par * TILE : 0);
-        wait_vmcnt<0>();
-        barrier_lds();  // the tile is there, and the other buffer has been read
-        find(tile + 1);  // behind the last tile its last row again
-        fetch(tile + 2);
-        f32x4 s[NQ];
-#pragma unroll
-        for (int x = 0; x < NQ; ++x) s[x] = zero;
-        lds_u8 *mine = here + w * NKB * FB;
-        const bool edge = 64 * tile + 64 > base;  // drafted rows, or rows past the last
-        unsigned badrows = 0;
-        if (edge) {
-            // a drafted row that is not finite reaches the tokens that see it, as NaN, and no others: the
-            // products take it as zeros
-            bool bad = false;
-#pragma unroll 1
-            for (int kb = 0; kb < NKB; ++kb) {
-                V8 x = Op::get(mine + kb * FB, lane);
-                if (Op::mend(x)) {
-                    Op::put(mine + kb * FB, lane, x);
-                    bad = true;
-                }
+            for (int k = 1; k < 64; k <<= 1) {
+                const int y = __shfl_up(x, k);
+                x += lane >= k ? y : 0;
             }
-            const unsigned long long k = __builtin_amdgcn_ballot_w64(bad);
-            badrows = (unsigned)(k | k >> 16 | k >> 32 | k >> 48) & 0xffff;
+            if (lane == 63) si[2048 + w] = x;
+            __syncthreads();
+            int before = total;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k < w) before += si[2048 + k];
+                total += si[2048 + k];
+            }
+            if (b0 + tid < p.B) si[b0 + tid] = before + x - mine;
+            __syncthreads();
         }
-        // fragments AHEAD steps before their MFMAs, in this order: left alone, the scheduler reads each one
-        // right before its use, and the wave waits; a piece of the next tile is asked for in each step
-        V8 ring[AHEAD + 1];
-#pragma unroll
-        for (int kb = 0; kb < AHEAD; ++kb) ring[kb] = Op::get(mine + kb * FB, lane);
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            if (kb + AHEAD < NKB) ring[(kb + AHEAD) % (AHEAD + 1)] = Op::get(mine + (kb + AHEAD) * FB, lane);
-            if constexpr (NBUF == 2) load(sk + (par ^ 1) * TILE, kb);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) s[x] = Op::mma(ring[kb % (AHEAD + 1)], qf[x][kb], s[x]);
-        }
-        if (edge) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = 64 * tile + perm_row(w, 4 * g + i), j = key - base;
-                const bool bad = badrows >> (4 * g + i) & 1;
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) {
-                    const bool see = key < len && (j < 0 || (bits[x] >> (j & 63) & 1) != 0);
-                    s[x][i] = !see ? -INFINITY : bad ? NAN : s[x][i];
-                }
+        const int each = (total + p.groups - 1) / p.groups;
+        const long long at = (long long)me * each;
+        if (me == 0) {
+            for (int i = tid; i < p.B; i += 256) p.from[i] = si[i];
+            if (tid == 0) {
+                p.from[p.B] = total;
+                p.from[p.B + 1] = each;
             }
         }
-        float mx[NQ];
-        bool grown = false;
+        if (at >= total) return;
+        left = min(each, total - (int)at);
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (si[mid] <= (int)at) lo = mid;
+            else hi = mid - 1;
+        }
+        b = lo;
+        const int nt = p.tiles(b), in = (int)at - si[b];
+        rg = in / nt;
+        t0 = in % nt;
+    } else {
+        b = me / p.rgroups;
+        rg = me % p.rgroups;
+        left = p.tiles(b);
+    }
+
+    while (left > 0) {
+        const int nt = p.tiles(b), t1 = min(nt, t0 + left), row0 = rg * 16 * NQ;
+        const int len = p.length(b), count = p.counts ? AttnSeqs::clip(p.counts[b], p.T) : p.T;
+        const int base = len - count;  // the first drafted row; below 0 where fewer rows than drafted tokens are there
+        // rows of tokens past the count see nothing
+        const int last = len == 0 || row0 / p.H >= count ? t0 : t1;
+        // rows of a tile: a lane's key(s), past the last the last; pages outside the cache are clipped
+        const int *table = p.table + (size_t)b * p.max_pages;
+        int pg[NL], in[NL];  // page and row in it of the tile after next
+        auto fetch = [&](int tile) {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int key = min(64 * min(tile, last - 1) + perm_row(w, Op::load_row(lane, i)), len - 1);
+                pg[i] = table[key / p.page];
+                in[i] = key % p.page;
+            }
+        };
+        const E *from[NL];
+        auto find = [&]() {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int at = pg[i] < 0 ? 0 : (pg[i] >= p.pages ? p.pages - 1 : pg[i]);
+                from[i] = cache + ((long long)at * p.page + in[i]) * D + Op::load_col(lane, i);
+            }
+        };
+        auto load = [&](int to, int kb) {  // to: the wave's fragments in LDS
+#pragma unroll
+            for (int i = 0; i < NL; ++i) direct_load<32 * ES, FB>(from[i], to, kb, 1024 * i);
+        };
+        const int mine0 = __builtin_amdgcn_readfirstlane((int)(unsigned)(size_t)(sk + w * NKB * FB));
+        f32x4 O[NT][NQ];
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) O[t][x] = zero;
+        // of a row: minus the maximum that its exponentials are taken against (log2 units; 0 while there is
+        // none), the score that outgrows it, and the wave's keys' part of the sum
+        float nm[NQ], most[NQ], l[NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
-            mx[x] = col_max(max4(s[x])) * c;
-            grown |= mx[x] > m[x] + 8.f;  // any finite score at first: m is -inf
+            nm[x] = 0.f;
+            most[x] = -INFINITY;
+            l[x] = 0.f;
         }
-        f32x4 P[NQ];
-        auto make = [&]() {
+        V8 ring[RING];
+        barrier_lds();  // what was in LDS has been read
+        if (t0 < last) {
+            fetch(t0);
+            find();
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) load(mine0, kb);
+            fetch(t0 + 1);
+        }
+        V8 qf[NQ][NKB];
+        {
+            const int ln = lane_here(lane);
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
-                const float mm = m[x] == -INFINITY ? 0.f : m[x];
+                const int row = min(row0 + 16 * x + (ln & 15), R - 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) P[x][i] = ex2(fmaf(s[x][i], c, -mm));
-                Op::put_half(sp + ((w >> 1) * NQ + x) * FB, lane, w & 1, P[x]);
+                for (int kb = 0; kb < NKB; ++kb)
+                    qf[x][kb] = Op::load(reinterpret_cast<const E *>(p.q) + ((size_t)b * R + row) * D + 32 * kb + 8 * (ln >> 4));
             }
-        };
-        make();
-        const bool any = __builtin_amdgcn_ballot_w64(grown) != 0;
-        if (lane == 0) sgrown[4 * par + w] = any;
-        if (g == 0) {
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) smax[((4 * par + w) * NQ + x) * 16 + n] = mx[x];
         }
-        barrier_lds();  // P is there
-        if (sgrown[4 * par] | sgrown[4 * par + 1] | sgrown[4 * par + 2] | sgrown[4 * par + 3]) {
+        // as many as fit stay in accumulation registers, where MFMAs take operands from as well; and all are
+        // there before the loop, in which a wait for them would be one for the direct loads
+        if constexpr (!F32) {
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) {
-                float now = m[x];
+            for (int x = 0; x < NQ; ++x)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) now = fmaxf(now, smax[((4 * par + k) * NQ + x) * 16 + n]);
-                const float alpha = now == -INFINITY ? 1.f : ex2(m[x] - now);
-                m[x] = now;
-                l[x] *= alpha;
+                for (int kb = 0; kb < NKB; ++kb) {
+                    if (NQ * NKB * 4 > 128 && (x * NKB + kb) * 4 < 256) asm volatile("" : "+a"(qf[x][kb]));
+                    else asm volatile("" : "+v"(qf[x][kb]));
+                }
+        }
+        if (NBUF == 2 && t0 < last) {
+            wait_vmcnt<0>();
 #pragma unroll
-                for (int t = 0; t < NT; ++t) O[t][x] *= alpha;
+            for (int kb = 0; kb < AHEAD; ++kb) ring[kb] = Op::get(sk + (w * NKB + kb) * FB, lane);
+        }
+        for (int tile = t0; tile < last; ++tile) {
+            const int par = (tile - t0) & 1;
+            lds_u8 *here = sk + (NBUF == 2 ? par * TILE : 0), *mine = here + w * NKB * FB;
+            // a wave's row tile is its own load; the others' are there behind the barrier in front of the values
+            if constexpr (NBUF == 1) wait_vmcnt<0>();
+            find();  // behind the last tile its last row again
+            fetch(tile + 2);
+            f32x4 s[NQ];
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) s[x] = zero;
+            const bool edge = 64 * tile + 64 > base;  // drafted rows, or rows past the last
+            unsigned badrows = 0;
+            if (edge) {
+                // a drafted row that is not finite reaches the tokens that see it, as NaN, and no others: the
+                // products take it as zeros
+                bool bad = false;
+                const int ln = lane_here(lane);
+#pragma unroll 1
+                for (int kb = 0; kb < NKB; ++kb) {
+                    V8 x = Op::get(mine + kb * FB, ln);
+                    if (Op::mend(x)) {
+                        Op::put(mine + kb * FB, ln, x);
+                        bad = true;
+                    }
+                }
+                const unsigned long long k = __builtin_amdgcn_ballot_w64(bad);
+                badrows = (unsigned)(k | k >> 16 | k >> 32 | k >> 48) & 0xffff;
             }
-            make();
-            barrier_lds();
-        }
+            if (NBUF == 1 || edge) {
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) l[x] += (P[x][0] + P[x][1]) + (P[x][2] + P[x][3]);
-        auto value = [&](int k) {  // step k: keys 32 (k / NT) .., channel tile k % NT
-            const int tt = w * NT + k % NT;
-            const lds_u8 *f = here + (k / NT * 2 * NKB + (tt >> 1)) * FB;
-            return Op::get_t(f, f + NKB * FB, tt & 1, lane);
-        };
-        V8 pf[NQ];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) ring[k] = value(k);
-#pragma unroll
-        for (int k = 0; k < 2 * NT; ++k) {
-            if (k % NT == 0) {
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) pf[x] = Op::get_lane(sp + (k / NT * NQ + x) * FB, lane);
+                for (int kb = 0; kb < AHEAD; ++kb) ring[kb] = Op::get(mine + kb * FB, lane);
             }
-            if (k + AHEAD < 2 * NT) ring[(k + AHEAD) % (AHEAD + 1)] = value(k + AHEAD);
-            __builtin_amdgcn_sched_barrier(0);
+            // fragments AHEAD steps before their MFMAs, in this order: left alone, the scheduler reads each one
+            // right before its use, and the wave waits; a piece of the next tile is asked for in each step, once
+            // all waves have read the buffer it goes to
 #pragma unroll
-            for (int x = 0; x < NQ; ++x) O[k % NT][x] = Op::mma(ring[k % (AHEAD + 1)], pf[x], O[k % NT][x]);
+            for (int kb = 0; kb < NKB; ++kb) {
+                if (kb + AHEAD < NKB) ring[(kb + AHEAD) % RING] = Op::get(mine + (kb + AHEAD) * FB, lane);
+                if constexpr (NBUF == 2) {
+                    if (kb == 1) barrier_only();
+                    if (kb > 0) load(mine0 + (par ^ 1) * TILE, kb - 1);
+                    if (kb == NKB - 1) load(mine0 + (par ^ 1) * TILE, kb);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) s[x] = Op::mma(ring[kb % RING], qf[x][kb], s[x]);
+            }
+            if (edge) {
+                const int ln = lane_here(lane);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const int node = min(row0 + 16 * x + (ln & 15), R - 1) / p.H;
+                    const unsigned long long bits = p.mask[(size_t)b * p.T + node];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 4 * (ln >> 4) + i, key = 64 * tile + perm_row(w, r), j = key - base;
+                        const bool see = key < len && (j < 0 || (bits >> (j & 63) & 1) != 0), bad = badrows >> r & 1;
+                        s[x][i] = !see ? -INFINITY : bad ? NAN : s[x][i];
+                    }
+                }
+            }
+            // P against the maxima there are, and whether a row has outgrown its own by 2^8 (at first: has any)
+            auto value = [&](int k) {  // step k: keys 32 (k / NT) .., channel tile k % NT
+                const int tt = w * NT + k % NT;
+                const lds_u8 *f = here + (k / NT * 2 * NKB + (tt >> 1)) * FB;
+                return Op::get_t(f, f + NKB * FB, tt & 1, lane);
+            };
+            auto make = [&](float (&sum)[NQ]) {
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    f32x4 P;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) P[i] = ex2(fmaf(s[x][i], c, nm[x]));
+                    Op::put_half(sp + ((w >> 1) * NQ + x) * FB, lane, w & 1, P);
+                    sum[x] += (P[0] + P[1]) + (P[2] + P[3]);
+                }
+            };
+            bool grown = false;
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) grown |= max4(s[x]) > most[x];
+            float sum[NQ];
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) sum[x] = l[x];
+            make(sum);
+            const bool any = __builtin_amdgcn_ballot_w64(grown) != 0;
+            if (lane == 0) sgrown[4 * par + w] = any;
+            barrier_lds();  // P and the whole tile are there
+            if (__builtin_amdgcn_readfirstlane(sgrown[4 * par] | sgrown[4 * par + 1] | sgrown[4 * par + 2] | sgrown[4 * par + 3])) {
+                // new maxima, of all four waves' keys, and P again
+                const int ln = lane_here(lane);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const float a = col_max(max4(s[x])) * c;
+                    if (ln < 16) smax[(w * NQ + x) * 16 + ln] = a;
+                }
+                barrier_lds();
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    const float was = most[x] == -INFINITY ? -INFINITY : -nm[x];
+                    float now = was;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) now = fmaxf(now, smax[(k * NQ + x) * 16 + (ln & 15)]);
+                    const float alpha = now == -INFINITY ? 1.f : ex2(was - now);
+                    nm[x] = now == -INFINITY ? 0.f : -now;
+                    most[x] = now == -INFINITY ? now : (now + 8.f) / c;
+                    sum[x] = l[x] * alpha;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) O[t][x] *= alpha;
+                }
+                make(sum);
+                barrier_lds();
+            }
+            V8 pf[NQ];
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) pf[x] = Op::get_lane(sp + x * FB, lane);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) ring[k] = value(k);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) l[x] = sum[x];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (k == NT) {
+#pragma unroll
+                    for (int x = 0; x < NQ; ++x) pf[x] = Op::get_lane(sp + (NQ + x) * FB, lane);
+                }
+                if (k + AHEAD < NV) {
+                    ring[(k + AHEAD) % RING] = value(k + AHEAD);
+                } else if constexpr (NBUF == 2) {  // into the next tile's scores
+                    if (k + AHEAD == NV) wait_vmcnt<0>();
+                    ring[(k + AHEAD) % RING] = Op::get(sk + (par ^ 1) * TILE + (w * NKB + k + AHEAD - NV) * FB, lane);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) O[k % NT][x] = Op::mma(ring[k % RING], pf[x], O[k % NT][x]);
+            }
+            if constexpr (NBUF == 1) {
+                barrier_lds();  // the tile has been read
+                if (tile + 1 < last) {
+#pragma unroll
+                    for (int kb = 0; kb < NKB; ++kb) load(mine0, kb);
+                }
+            }
         }
-        if constexpr (NBUF == 1) {
-            barrier_lds();  // the tile has been read
-            if (tile + 1 < last) load_all(sk);
+        // the sum over the waves' keys; the loads behind the last tile end before the wave does
+        wait_vmcnt<0>();
+        barrier_lds();
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const float sum = col_sum(l[x]);
+            if (lane < 16) smax[(w * NQ + x) * 16 + lane] = sum;
         }
-    }
-    // the sum over the waves' keys; the loads behind the last tile end before the wave does
-    wait_vmcnt<0>();
-    barrier_lds();
+        barrier_lds();
+        const bool whole = t0 == 0 && t1 == nt;
+        const int ln = lane_here(lane), n2 = ln & 15, g2 = ln >> 4;
+        const size_t slot = 2 * (size_t)me + (t0 == 0 ? 1 : 0);
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        const float sum = col_sum(l[x]);
-        if (g == 0) smax[(w * NQ + x) * 16 + n] = sum;
-    }
-    barrier_lds();
+        for (int x = 0; x < NQ; ++x) {
+            float sum = 0.f;
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) {
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum += smax[(k * NQ + x) * 16 + n];
-        const int row = row0 + 16 * x + n;
-        if (row >= R) continue;
-        // nothing seen: zeros, -inf; a sum that is NaN stays one
-        const bool none = dead[x] || sum == 0.f;
-        const float inv = 1.f / sum, lse2 = none ? -INFINITY : m[x] + lg2(sum);
-        if (p.nsplit == 1) {
-            E *o = reinterpret_cast<E *>(p.out) + ((size_t)b * R + row) * DC + w * (DC / 4) + 8 * g;
+            for (int k = 0; k < 4; ++k) sum += smax[(k * NQ + x) * 16 + n2];
+            const int row = row0 + 16 * x + n2;
+            if (row >= R) continue;
+            // nothing seen: zeros, -inf; a sum that is NaN stays one
+            const bool none = row / p.H >= count || sum == 0.f;
+            const float inv = 1.f / sum, lse2 = none ? -INFINITY : lg2(sum) - nm[x];
+            const size_t at = (size_t)b * R + row, in_part = slot * (16 * NQ) + 16 * x + n2;
+            if (g2 == 0 && w == 0) {
+                if (whole) p.lse[at] = lse2 * kLn2;
+                else p.part_lse[in_part] = lse2;
+            }
+            const int d = w * (DC / 4) + 8 * g2;
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
-                const bool swap = Op::kSwap && (g & 1);
+                const bool swap = Op::kSwap && (g2 & 1);
                 f32x4 u = swap ? O[t + 1][x] : O[t][x], v = swap ? O[t][x] : O[t + 1][x];
                 u = none ? zero : u * inv;
                 v = none ? zero : v * inv;
-                Op::store8(o + 16 * t, u, v);
+                if (whole) {
+                    Op::store8(reinterpret_cast<E *>(p.out) + at * DC + d + 16 * t, u, v);
+                } else {
+                    float *o = p.part + in_part * DC + d + 16 * t;
+                    *reinterpret_cast<f32x4 *>(o) = u;
+                    *reinterpret_cast<f32x4 *>(o + 4) = v;
+                }
             }
-            if (g == 0 && w == 0) p.lse[(size_t)b * R + row] = lse2 * kLn2;
-        } else {
-            const size_t at = ((size_t)b * p.nsplit + split) * R + row;
-            if (g == 0 && w == 0) p.part_lse[at] = lse2;
-            if (first >= last && !dead[x]) continue;  // nothing here, and the join reads the parts that have keys
-            float *o = p.part + at * DC + w * (DC / 4) + 8 * g;
-#pragma unroll
-            for (int t = 0; t < NT; t += 2) {
-                const bool swap = Op::kSwap && (g & 1);
-                f32x4 u = swap ? O[t + 1][x] : O[t][x], v = swap ? O[t][x] : O[t + 1][x];
-                u = none ? zero : u * inv;
-                v = none ? zero : v * inv;
-                *reinterpret_cast<f32x4 *>(o + 16 * t) = u;
-                *reinterpret_cast<f32x4 *>(o + 16 * t + 4) = v;
-            }
+        }
+        left -= t1 - t0;
+        t0 = 0;
+        if (++rg == p.rgroups) {
+            rg = 0;
+            ++b;
         }
     }
 }
 
-// Joins the parts of a row: weights 2^(lse_i - max), 4 values a thread.  Every part that has keys counts, so
-// that one whose result is not finite shows.
-template <int DC, typename E>
+// Joins the pieces of the units that more than one work-group had: weights 2^(lse_i - max).  Work-group x of
+// the first grid dimension takes the unit that work-group x of the kernel above began and did not end; a
+// wave takes 256 channels of one row, lane i the weight of piece i, and four pieces' values are on their way
+// at a time.
+template <int DC, int NQ, typename E>
 __global__ __launch_bounds__(256) void latent_tree_join_kernel(const LatentTreeArgs p) {
-    constexpr int TPR = DC / 4;  // threads a row
-    const int R = p.T * p.H;
-    const long long at = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-    if (at >= (long long)p.B * R) return;
-    const int b = (int)(at / R), row = (int)(at % R), d = 4 * (threadIdx.x % TPR);
-    const float *e = p.part_lse + (size_t)b * p.nsplit * R + row;
-    const float *o_ = p.part + ((size_t)b * p.nsplit * R + row) * DC + d;
-    int len, per;
-    const int ntile = p.tiles(b, len, per), parts = per > 0 ? (ntile + per - 1) / per : 0;
-    float m = -INFINITY, sum = 0.f;
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, e[(size_t)i * R]);
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < parts; ++i) {
-        const float x = e[(size_t)i * R], wgt = x == -INFINITY ? 0.f : ex2(x - m);
-        sum += wgt;
-        o += wgt * *reinterpret_cast<const f32x4 *>(o_ + (size_t)i * R * DC);
+    constexpr int WPR = DC / 256, ROWS = 4 / WPR;  // waves a row; rows a work-group
+    const int total = p.from[p.B], each = p.from[p.B + 1], me = blockIdx.x, R = p.T * p.H;
+    const long long end = (long long)(me + 1) * each;
+    if (end >= total) return;
+    int lo = 0, hi = p.B - 1;  // the sequence that has tile end - 1
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.from[mid] < end) lo = mid;
+        else hi = mid - 1;
     }
+    const int b = lo, nt = p.tiles(b), rg = ((int)end - 1 - p.from[b]) / nt, begin = p.from[b] + rg * nt;
+    // it ended there, or this work-group did not begin it
+    if (begin + nt == end || begin < (long long)me * each) return;
+    const int parts = (begin + nt - 1) / each - me + 1;
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * me + 1 : 2 * (me + i)) * (16 * NQ); };
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = ROWS * blockIdx.y + w / WPR, row = rg * 16 * NQ + r, d = 256 * (w % WPR) + 4 * lane;
+    if (row >= R) return;
+    float m = -INFINITY, sum = 0.f;
+    for (int i = lane; i < parts; i += 64) m = fmaxf(m, p.part_lse[slot(i) + r]);
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < parts; i0 += 64) {
+        const float x = i0 + lane < parts ? p.part_lse[slot(i0 + lane) + r] : -INFINITY;
+        const float mine = x == -INFINITY ? 0.f : ex2(x - m);  // one that is NaN stays one
+        const int here = min(64, parts - i0);
+        sum += mine;
+        for (int i = 0; i < here; i += 4) {
+            f32x4 y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = *reinterpret_cast<const f32x4 *>(p.part + (slot(i0 + min(i + k, here - 1)) + r) * DC + d);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < here) o += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), i + k)) * y[k];
+        }
+    }
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t at = (size_t)b * R + row;
     st_tile(reinterpret_cast<E *>(p.out) + at * DC + d, 0, o * inv);
     if (d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
 }
