@@ -131,6 +131,13 @@ template <> struct AttnOp<true> {
     }
 };
 
+// A lane's number that what comes after it is computed from on the spot: what the edges and the ends need
+// would otherwise be kept in registers across the tiles, which have none left.
+__device__ __forceinline__ int lane_here(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // row tile and row of index r inside a 64-row block (the inverse of perm_row)
 __device__ __forceinline__ int perm_tile(int r) { return 2 * (r >> 5) + ((r >> 2) & 1); }
 __device__ __forceinline__ int perm_m(int r) { return 4 * ((r >> 3) & 3) + (r & 3); }

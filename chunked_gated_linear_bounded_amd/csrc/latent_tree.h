@@ -146,12 +146,6 @@ __device__ __forceinline__ void direct_load(const void *src, int to, int kb, int
                  "n"(FB * kb + off - STEP * kb)
                  : "memory", "m0", "scc");
 }
-// A lane's number that what comes after it is computed from on the spot: what the edges and the ends need
-// would otherwise be kept in registers across the tiles, which have none left.
-__device__ __forceinline__ int lane_here(int lane) {
-    asm volatile("" : "+v"(lane));
-    return lane;
-}
 // A barrier and nothing else: LDS reads in flight stay in flight.
 __device__ __forceinline__ void barrier_only() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);

@@ -95,22 +95,22 @@ __device__ __forceinline__ float load_g(const void *g, long long at, bool g32) {
 template <bool F32> struct LinOp : AttnOp<F32> {
     using V8 = typename AttnOp<F32>::V8;
     static constexpr int MP = F32 ? 1 : 2, SP = F32 ? 1 : 3;
-    // pieces of the pair (x, y)
-    template <int NP>
-    __device__ __forceinline__ static void pieces(f32x4 x, f32x4 y, V8 (&r)[NP]) {
-        if constexpr (F32) {
-            r[0] = V8{x, y};
-        } else {
+    // the next piece of the pair (x, y), which keep what is left
+    __device__ __forceinline__ static V8 piece(f32x4 &x, f32x4 &y) {
+        const V8 r = AttnOp<F32>::pair(x, y);
+        if constexpr (!F32) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                r[p] = AttnOp<F32>::pair(x, y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] -= (float)r[p][i];
-                    y[i] -= (float)r[p][4 + i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                x[i] -= (float)r[i];
+                y[i] -= (float)r[4 + i];
             }
         }
+        return r;
+    }
+    template <int NP>
+    __device__ __forceinline__ static void pieces(f32x4 x, f32x4 y, V8 (&r)[NP]) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) r[p] = piece(x, y);
     }
     __device__ __forceinline__ static void split(const V8 &v, f32x4 &x, f32x4 &y) {
         if constexpr (F32) {
