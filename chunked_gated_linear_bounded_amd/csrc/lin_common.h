@@ -97,15 +97,23 @@ template <bool F32> struct LinOp : AttnOp<F32> {
     static constexpr int MP = F32 ? 1 : 2, SP = F32 ? 1 : 3;
     // the next piece of the pair (x, y), which keep what is left
     __device__ __forceinline__ static V8 piece(f32x4 &x, f32x4 &y) {
-        const V8 r = AttnOp<F32>::pair(x, y);
-        if constexpr (!F32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] -= (float)r[i];
-                y[i] -= (float)r[4 + i];
-            }
+        if constexpr (F32) {
+            return V8{x, y};
+        } else {
+            typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+            const u32x4 r = {take(x, 0), take(x, 2), take(y, 0), take(y, 2)};
+            return __builtin_bit_cast(bf16x8, r);
         }
-        return r;
+    }
+    // x[i], x[i + 1] as a bf16 pair, taken off them.  The pair is a whole number from here on: as two bf16
+    // values the compiler converts each a second time to subtract it.
+    __device__ __forceinline__ static unsigned take(f32x4 &x, int i) {
+        typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+        unsigned u = __builtin_bit_cast(unsigned, b2{(__bf16)x[i], (__bf16)x[i + 1]});
+        asm("" : "+v"(u));
+        x[i] -= __builtin_bit_cast(float, u << 16);
+        x[i + 1] -= __builtin_bit_cast(float, u & 0xffff0000u);
+        return u;
     }
     template <int NP>
     __device__ __forceinline__ static void pieces(f32x4 x, f32x4 y, V8 (&r)[NP]) {
@@ -117,10 +125,14 @@ template <bool F32> struct LinOp : AttnOp<F32> {
             x = v.a;
             y = v.b;
         } else {
+            typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+            const u32x4 u = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = (float)v[i];
-                y[i] = (float)v[4 + i];
+            for (int i = 0; i < 2; ++i) {
+                x[2 * i] = __builtin_bit_cast(float, u[i] << 16);
+                x[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xffff0000u);
+                y[2 * i] = __builtin_bit_cast(float, u[2 + i] << 16);
+                y[2 * i + 1] = __builtin_bit_cast(float, u[2 + i] & 0xffff0000u);
             }
         }
     }
