@@ -41,6 +41,12 @@ size_t lin_bwd_bytes(const LinLaunch &p) { return LinBwdPlan(p).bytes; }
         if (e_ != hipSuccess) return e_;            \
     } while (0)
 
+#define KDA_WALK(call)                  \
+    do {                                \
+        const hipError_t e_ = call;     \
+        if (e_ != hipSuccess) return e_; \
+    } while (0)
+
 template <int DK, int DV, bool F32, bool DOT, bool SUM>
 static hipError_t bwd_t(const LinLaunch &p) {
     using E = typename std::conditional<F32, float, __bf16>::type;
@@ -62,8 +68,8 @@ static hipError_t bwd_t(const LinLaunch &p) {
     s1.into = p.scale;
     s1.seg = f(m.seg[1]);
     s1.seg_decay = f(m.decay[1]);
-    if (many || want_last) KDA_LAUNCH((lin_walk_kernel<DK, DV, F32, false, false, false, false, false>), dim3(grid), dim3(256), 0, p.stream, s0);
-    if (many) KDA_LAUNCH((lin_walk_kernel<DK, DV, F32, true, false, false, false, false>), dim3(grid), dim3(256), 0, p.stream, s1);
+    if (many || want_last) KDA_WALK((lin_walk<DK, DV, F32, false, false, false, false, false>(s0, grid, p.stream)));
+    if (many) KDA_WALK((lin_walk<DK, DV, F32, true, false, false, false, false>(s1, grid, p.stream)));
     if (many || want_last) {
         LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {}};
         s.side[0] = {p.init_state, f(m.seg[0]), want_last ? f(m.last) : nullptr, f(m.decay[0]), want_last};
@@ -81,7 +87,7 @@ static hipError_t bwd_t(const LinLaunch &p) {
     w.seg = f(m.seg[0]);
     w.dots = f(m.dots[0]);
     w.out = SUM ? f(m.parts[0]) : p.dq;
-    KDA_LAUNCH((lin_walk_kernel<DV, DK, F32, false, true, true, DOT, SUM>), dim3(grid), dim3(256), 0, p.stream, w);
+    KDA_WALK((lin_walk<DV, DK, F32, false, true, true, DOT, SUM>(w, grid, p.stream)));
     // dk and dv: backwards in time
     w = a;
     w.a = p.v; w.sa = sv;
@@ -93,7 +99,7 @@ static hipError_t bwd_t(const LinLaunch &p) {
     w.seg = f(m.seg[1]);
     w.dots = f(m.dots[1]);
     w.out = SUM ? f(m.parts[1]) : p.dk_;
-    KDA_LAUNCH((lin_walk_kernel<DV, DK, F32, true, true, true, DOT, SUM>), dim3(grid), dim3(256), 0, p.stream, w);
+    KDA_WALK((lin_walk<DV, DK, F32, true, true, true, DOT, SUM>(w, grid, p.stream)));
     w = a;
     w.a = p.k; w.sa = sk; w.ra = r;
     w.b = p.q; w.sb = sq; w.rb = r;
@@ -103,7 +109,7 @@ static hipError_t bwd_t(const LinLaunch &p) {
     w.final_state = p.dinit;
     w.seg = f(m.seg[1]);
     w.out = p.dv_;
-    KDA_LAUNCH((lin_walk_kernel<DK, DV, F32, true, false, true, false, false>), dim3(grid), dim3(256), 0, p.stream, w);
+    KDA_WALK((lin_walk<DK, DV, F32, true, false, true, false, false>(w, grid, p.stream)));
     if (p.T == 0) return hipSuccess;
     if (DOT) {
         LinDecayGradArgs d{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,

@@ -30,9 +30,9 @@ struct LinLaunch {
 // Tokens of a segment, the piece of a sequence that one work-group walks through, and the segments of
 // one batch entry.
 inline int lin_segment(const LinLaunch &p) {
-    const long long chunks = (((long long)p.T + 63) / 64) * p.B * p.H;
-    long long per = (chunks + 1023) / 1024;
-    per = per < 4 ? 4 : (per > 32 ? 32 : per);
+    const long long chunks = (((long long)p.T + 63) / 64) * p.B * p.H, most = p.fp32 ? 512 : 256;
+    long long per = (chunks + most - 1) / most;
+    per = per < 4 ? 4 : (per > 4096 ? 4096 : per);
     return (int)per * 64;
 }
 inline long long lin_slots(const LinLaunch &p) {
