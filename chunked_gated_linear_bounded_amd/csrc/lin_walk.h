@@ -100,24 +100,27 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
     auto frag = [](int it, int jb) { return REV ? (jb == 1 ? it : 4 + it) : (jb == 0 ? it : 2 + it); };
 
     if (helper) {
-        TileStage<false, DA / 8> ta, tb;
-        TileStage<false, DC / 8> tc;
-        float gn = 0.f;
+        struct Stage {  // one chunk on its way: two of them, so that a chunk's loads have two chunks' time
+            TileStage<false, DA / 8> ta, tb;
+            TileStage<false, DC / 8> tc;
+            float gn;
+        } st0, st1;
         double total = 0.0;
-        auto load = [&](int ci) {
+        auto load = [&](int ci, Stage &s) {
+            if (ci >= nchunk) return;
             const int c = chunk_of(ci);
-            if constexpr (OUT) ta.load(u.ap, p.sa.t, 64 * c, rows, tid);
-            tb.load(u.bp, p.sb.t, 64 * c, rows, tid);
-            tc.load(u.cp, p.sc.t, 64 * c, rows, tid);
-            if (w == 3) gn = 64 * c + lane < rows ? load_g(p.g, u.g0 + (long long)(64 * c + lane) * p.sg.t, p.g32) : 0.f;
+            if constexpr (OUT) s.ta.load(u.ap, p.sa.t, 64 * c, rows, tid);
+            s.tb.load(u.bp, p.sb.t, 64 * c, rows, tid);
+            s.tc.load(u.cp, p.sc.t, 64 * c, rows, tid);
+            if (w == 3) s.gn = 64 * c + lane < rows ? load_g(p.g, u.g0 + (long long)(64 * c + lane) * p.sg.t, p.g32) : 0.f;
         };
-        auto store = [&](int ci) {  // and the decays
+        auto store = [&](int ci, const Stage &st) {  // and the decays
             const int par = ci & 1;
-            if constexpr (OUT) ta.store(tile_a(par), NA, 0, tid);
-            tb.store(tile_b(par), NA, 0, tid);
-            tc.store(tile_c(par), NC, 0, tid);
+            if constexpr (OUT) st.ta.store(tile_a(par), NA, 0, tid);
+            st.tb.store(tile_b(par), NA, 0, tid);
+            st.tc.store(tile_c(par), NC, 0, tid);
             if (w == 3) {
-                const double G = wave_scan64(decay_log2(gn)), last = lane64(G, 63);
+                const double G = wave_scan64(decay_log2(st.gn)), last = lane64(G, 63);
                 const float hi = (float)G, e0 = ex2(hi), e1 = ex2((float)(last - G));
                 lds_f *s = sG + 320 * par;
                 s[lane] = hi;
@@ -170,25 +173,30 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
             const int row = 64 * chunk_of(ci) + tid;
             if (tid < 64 && row < rows) p.dots[u.row0 + row] = (sDot[tid] + sDot[64 + tid]) + (sDot[128 + tid] + sDot[192 + tid]);
         };
+        auto step = [&](int ci, Stage &s) {  // s holds the chunk behind ci
+            if (DOT && ci > 0) dots(ci - 1);
+            if (ci + 1 < nchunk) store(ci + 1, s);
+            load(ci + 3, s);
+            barrier_lds();
+            if constexpr (OUT) {
+                if (ci + 1 < nchunk) scores(ci + 1);
+                barrier_lds();
+            }
+        };
         if (nchunk > 0) {
-            load(0);
-            store(0);
-            if (nchunk > 1) load(1);
+            load(0, st0);
+            load(1, st1);
+            store(0, st0);
+            load(2, st0);
             barrier_lds();
             if constexpr (OUT) {
                 scores(0);
                 barrier_lds();
             }
         }
-        for (int ci = 0; ci < nchunk; ++ci) {
-            if (DOT && ci > 0) dots(ci - 1);
-            if (ci + 1 < nchunk) store(ci + 1);
-            if (ci + 2 < nchunk) load(ci + 2);
-            barrier_lds();
-            if constexpr (OUT) {
-                if (ci + 1 < nchunk) scores(ci + 1);
-                barrier_lds();
-            }
+        for (int ci = 0; ci < nchunk; ci += 2) {
+            step(ci, st1);
+            if (ci + 1 < nchunk) step(ci + 1, st0);
         }
         if (DOT && nchunk > 0) dots(nchunk - 1);
         if (!OUT && threadIdx.x == 448) p.seg_decay[u.sunit] = ex2((float)total);
