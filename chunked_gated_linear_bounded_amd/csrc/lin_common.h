@@ -90,23 +90,14 @@ __device__ __forceinline__ float load_g(const void *g, long long at, bool g32) {
 // ---------------------------------------------------------------- operands
 // What is computed in float32 and enters a product again is carried in pieces where operands are bf16:
 // x = hi + lo keeps 16 bits (M and P, whose products are rounded to bf16 outputs), a third piece all 24
-// (what the float32 state gathers).  bf16 has float's exponents, so pieces need no scaling.  float32
-// inputs use float32 MFMAs and one piece.
-template <bool F32> struct LinOp : AttnOp<F32> {
-    using V8 = typename AttnOp<F32>::V8;
-    static constexpr int MP = F32 ? 1 : 2, SP = F32 ? 1 : 3;
-    // the next piece of the pair (x, y), which keep what is left
-    __device__ __forceinline__ static V8 piece(f32x4 &x, f32x4 &y) {
-        if constexpr (F32) {
-            return V8{x, y};
-        } else {
-            typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
-            const u32x4 r = {take(x, 0), take(x, 2), take(y, 0), take(y, 2)};
-            return __builtin_bit_cast(bf16x8, r);
-        }
-    }
+// (what a float32 state that is handed on gathers).  bf16 has float's exponents, so pieces need no
+// scaling.  float32 inputs use float32 MFMAs and need no pieces.
+template <bool F32> struct LinOp;
+template <> struct LinOp<true> : AttnOp<true> {};
+template <> struct LinOp<false> : AttnOp<false> {
+    typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
     // x[i], x[i + 1] as a bf16 pair, taken off them.  The pair is a whole number from here on: as two bf16
-    // values the compiler converts each a second time to subtract it.
+    // values the compiler converts each a second time to subtract it (64k x 32 heads: 855 us instead of 811).
     __device__ __forceinline__ static unsigned take(f32x4 &x, int i) {
         typedef __attribute__((ext_vector_type(2))) __bf16 b2;
         unsigned u = __builtin_bit_cast(unsigned, b2{(__bf16)x[i], (__bf16)x[i + 1]});
@@ -116,24 +107,18 @@ template <bool F32> struct LinOp : AttnOp<F32> {
         return u;
     }
     template <int NP>
-    __device__ __forceinline__ static void pieces(f32x4 x, f32x4 y, V8 (&r)[NP]) {
+    __device__ __forceinline__ static void pieces(f32x4 x, f32x4 y, bf16x8 (&r)[NP]) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) r[p] = piece(x, y);
+        for (int p = 0; p < NP; ++p) r[p] = __builtin_bit_cast(bf16x8, u32x4{take(x, 0), take(x, 2), take(y, 0), take(y, 2)});
     }
-    __device__ __forceinline__ static void split(const V8 &v, f32x4 &x, f32x4 &y) {
-        if constexpr (F32) {
-            x = v.a;
-            y = v.b;
-        } else {
-            typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
-            const u32x4 u = __builtin_bit_cast(u32x4, v);
+    __device__ __forceinline__ static void split(const bf16x8 &v, f32x4 &x, f32x4 &y) {
+        const u32x4 u = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                x[2 * i] = __builtin_bit_cast(float, u[i] << 16);
-                x[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xffff0000u);
-                y[2 * i] = __builtin_bit_cast(float, u[2 + i] << 16);
-                y[2 * i + 1] = __builtin_bit_cast(float, u[2 + i] & 0xffff0000u);
-            }
+        for (int i = 0; i < 2; ++i) {
+            x[2 * i] = __builtin_bit_cast(float, u[i] << 16);
+            x[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xffff0000u);
+            y[2 * i] = __builtin_bit_cast(float, u[2 + i] << 16);
+            y[2 * i + 1] = __builtin_bit_cast(float, u[2 + i] & 0xffff0000u);
         }
     }
 };

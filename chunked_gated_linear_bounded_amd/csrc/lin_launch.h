@@ -27,12 +27,21 @@ struct LinLaunch {
     float *dinit;
 };
 
-// Tokens of a segment, the piece of a sequence that one work-group walks through, and the segments of
-// one batch entry.
+// Tokens of a segment, the piece of a sequence that one work-group walks through, and the segments of one
+// batch entry.  A segment costs its state written, scanned and read again and its inputs read twice, so
+// there are as many as keep the card busy and no more: one work-group a CU in bf16, whose work-groups have
+// eight waves and 125 KB of LDS (256 against 512 segments in all: 4 x 8192 x 16 heads 226 us against 243,
+// 1 x 65536 x 32 heads 838 against 853, the training step of 2 x 4096 x 32 heads 323 against 386), two in float32.
+// A chunk of 64 tokens is the least, for short sequences wait for one chunk after the other (1 x 1024 x 4
+// heads, forward and backward: 23 and 62 us with segments of 64 tokens, 32 and 93 with 256; float32 42 and
+// 115, 117 and 329); only up to 256 tokens of bf16 is one launch over a single segment better (256 tokens:
+// 17 us against 23 forward, 61 against 55 backward; 192: 17 against 23, 50 against 54).
 inline int lin_segment(const LinLaunch &p) {
     const long long chunks = (((long long)p.T + 63) / 64) * p.B * p.H, most = p.fp32 ? 512 : 256;
     long long per = (chunks + most - 1) / most;
-    per = per < 4 ? 4 : (per > 4096 ? 4096 : per);
+    if (per < 1) per = 1;
+    if (per < 4 && p.T <= 256 && !p.fp32) per = 4;
+    if (per > 4096) per = 4096;
     return (int)per * 64;
 }
 inline long long lin_slots(const LinLaunch &p) {
@@ -52,7 +61,7 @@ inline bool lin_grids_fit(const LinLaunch &p) {
     const long long most = 4294967295LL, units = (long long)p.B * p.H * lin_slots(p);
     const long long states = (long long)p.N * p.H * (p.dk * p.dv / 1024);
     const long long rows = (long long)p.B * p.H * (((long long)p.T + 15) / 16);
-    return (units + 7) / 8 * 8 <= most / 256 && states <= most / 256 && rows <= most / 256;
+    return (units + 7) / 8 * 8 <= most / 512 && states <= most / 256 && rows <= most / 256;
 }
 inline bool lin_decode_grid_fits(const LinLaunch &p) { return (long long)p.B * p.H * (p.dv / 16) * 256 <= 4294967295LL; }
 

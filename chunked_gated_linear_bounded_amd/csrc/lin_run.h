@@ -27,7 +27,7 @@ inline unsigned lin_walk_grid(const LinLaunch &p) { return (unsigned)(((long lon
 // Either walk: bf16 with helpers beside the walkers, float32 (whose tiles fill the LDS once) in one group.
 template <int DA, int DC, bool F32, bool REV, bool TR, bool OUT, bool DOT, bool OUTF>
 inline hipError_t lin_walk(const LinWalkArgs &a, unsigned grid, hipStream_t stream) {
-    if constexpr (F32) hipLaunchKernelGGL((lin_walk_kernel<DA, DC, true, REV, TR, OUT, DOT, OUTF>), dim3(grid), dim3(256), 0, stream, a);
+    if constexpr (F32) hipLaunchKernelGGL((lin_walk32_kernel<DA, DC, REV, TR, OUT, DOT>), dim3(grid), dim3(256), 0, stream, a);
     else hipLaunchKernelGGL((lin_pair_kernel<DA, DC, REV, TR, OUT, DOT, OUTF>), dim3(grid), dim3(512), 0, stream, a);
     return hipGetLastError();
 }

@@ -3,12 +3,12 @@
 // forwards (j <= i, D_ij = e^{G_i - G_j}, wd_i = e^{G_i}, ws_j = e^{G_last - G_j}) or, REV, backwards in
 // time (j >= i, D_ij = e^{G_j - G_i}, wd and ws change places).
 //
-// A work-group of four waves takes one segment of one head, a wave a quarter of c's channels.  Everything but the scores is computed
-// transposed: O^T = C^T M^T + P^T A^T has the channels on the accumulator's rows, so that a lane stores
-// eight consecutive ones; the scores S^T = B A^T are, as they lie, the B operand of M^T; and the state P
-// (rows b's channels, columns c's, 16 DC / 64 columns a wave, in registers throughout) is, as it lies,
-// the A operand of P^T A^T.  C's transposed fragments serve O^T unscaled and, times ws in pieces, the
-// state.  A wave makes the scores of 16 rows and hands them round through LDS.
+// A work-group takes one segment of one head, each of four waves a quarter of c's channels.  Everything but
+// the scores is computed transposed: O^T = C^T M^T + P^T A^T has the channels on the accumulator's rows, so
+// that a lane stores eight consecutive ones; the scores S^T = B A^T are, as they lie, the B operand of M^T;
+// and the state P (rows b's channels, columns c's, DC / 4 columns a wave, in registers throughout) is, as it
+// lies, the A operand of P^T A^T.  C's transposed fragments serve O^T unscaled and, times ws in pieces, the
+// state.  Scores go round through LDS.
 #pragma once
 #include "lin_common.h"
 
@@ -32,7 +32,7 @@ struct LinWalkArgs {
 
 // Where a work-group's segment lies, and its rows.
 template <typename E> struct LinUnit {
-    int b, h, seq, rows, nchunk;
+    int b, h, seq, first, rows, nchunk;
     bool alone;
     const E *ap, *bp, *cp;
     long long g0;
@@ -46,7 +46,8 @@ template <typename E> struct LinUnit {
         const int slot = unit / p.H % p.nslot;
         int piece;
         if (!p.seqs.find(b, slot, seq, piece)) return false;
-        const int len = p.seqs.length(seq), first = p.seqs.start(seq) + piece * p.seqs.seg;
+        const int len = p.seqs.length(seq);
+        first = p.seqs.start(seq) + piece * p.seqs.seg;
         alone = !p.all && len <= p.seqs.seg;
         rows = max(0, min(p.seqs.seg, len - piece * p.seqs.seg));
         nchunk = (rows + 63) / 64;
@@ -67,7 +68,11 @@ template <typename E> struct LinUnit {
 //   walkers   a_i P                          | + M C, out; state
 //   helpers   next tile into LDS, decays     | next scores
 // As one group of four waves that did all of it in turn, two work-groups on a CU, a chunk took 17,400 cycles
-// of a work-group, half of them waits, and the parts' times added up.
+// of a work-group, half of them waits, and the parts' times added up (4 x 8192 x 16 heads 248 us against 202).
+//
+// 1 x 65536 x 32 heads of 128 x 128: pass 1 takes 300 us, of which its reads (1.07 GB) are 230 at a copy's
+// rate; pass 2 560, where its traffic (2.1 GB) alone takes 414 and the walkers' chain of MFMAs, LDS reads and
+// pieces alone 409, 3.2 us a chunk: one group a CU has nothing to put into either's gaps.
 //
 // OUT: pass 2, the outputs; else pass 1, the segment's own contribution to the state.  TR: states in memory
 // have b's channels as rows, else c's.
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
             P[ct][2 * kb + 1] = y;
         }
     const int lane0 = lane;
-    const E *yp = DOT ? reinterpret_cast<const E *>(p.y) + u.b * p.sy.b + u.h / p.ry * p.sy.h + (long long)(u.row0 - ((size_t)u.b * p.H + u.h) * p.seqs.T) * p.sy.t : nullptr;
+    const E *yp = DOT ? reinterpret_cast<const E *>(p.y) + u.b * p.sy.b + u.h / p.ry * p.sy.h + (long long)u.first * p.sy.t : nullptr;
     // Products in steps of one fragment from LDS, read AHEAD steps before its MFMAs, and beside the MFMAs a
     // share of what the vector unit has to do for the steps to come: the pieces of P for the next 32 of b's
     // channels, those of the weighted C for the next 32 tokens.  The order is fixed step by step: left alone,
@@ -454,40 +459,25 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
         }
 }
 
-// OUT: pass 2, the outputs; else pass 1, the segment's own contribution to the state.  TR: states in
-// memory have b's channels as rows, else c's.
-template <int DA, int DC, bool F32, bool REV, bool TR, bool OUT, bool DOT, bool OUTF>
-__global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWalkArgs p) {
-    using Op = LinOp<F32>;
-    using E = typename Op::E;
+// float32: tiles fill the LDS once, so one group of four waves does everything in turn, on float32 MFMAs,
+// whose rate (an eighth of bf16's) leaves little for helpers to hide.  Parameters as above.
+template <int DA, int DC, bool REV, bool TR, bool OUT, bool DOT>
+__global__ __launch_bounds__(256, 1) void lin_walk32_kernel(const LinWalkArgs p) {
+    using Op = LinOp<true>;
     using V8 = typename Op::V8;
-    constexpr int NA = DA / 32, NC = DC / 32, NDT = DA / 16, NW = 4, NCT = DC / 16 / NW, MP = Op::MP, SP = Op::SP, FB = Op::FB;
+    constexpr int NA = DA / 32, NC = DC / 32, NDT = DA / 16, NW = 4, NCT = DC / 16 / NW, FB = Op::FB;
     typedef __attribute__((address_space(3))) float lds_f;
     typedef __attribute__((address_space(3))) f32x4 lds_f4;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[(4 * NA * (OUT ? 2 : 1) + 4 * NC + (OUT ? 8 * MP : 0)) * FB];
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[(4 * NA * (OUT ? 2 : 1) + 4 * NC + (OUT ? 8 : 0)) * FB];
     // by chunk parity: prefix sums in two floats, weights of the outputs and of the sources, e^{G_last}
     __shared__ __attribute__((aligned(16))) float sg[2 * 320 + 64 + (DOT ? 64 * NW : 0)];
     lds_u8 *sB = lds_base(smem), *sC = sB + 4 * NA * FB, *sA = sC + 4 * NC * FB, *sM = sA + 4 * NA * FB;
     lds_f *sG = (lds_f *)lds_base(sg), *sD = sG + 640, *sDot = sG + 704;
     const int tid0 = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid0 >> 6);
-    // units in eight runs, one an XCD: heads that share rows are neighbours there
-    const unsigned units = (unsigned)p.B * p.H * p.nslot, per = (units + 7) / 8, unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || unit >= units) return;
-    const int h = unit % p.H, slot = unit / p.H % p.nslot, b = unit / p.H / p.nslot;
-    int seq, piece;
-    if (!p.seqs.find(b, slot, seq, piece)) return;
-    const int len = p.seqs.length(seq);
-    const bool alone = !p.all && len <= p.seqs.seg;
-    if (!OUT && alone) return;
-    const int first = p.seqs.start(seq) + piece * p.seqs.seg, rows = max(0, min(p.seqs.seg, len - piece * p.seqs.seg));
-    const int nchunk = (rows + 63) / 64;
-    const E *ap = reinterpret_cast<const E *>(p.a) + b * p.sa.b + h / p.ra * p.sa.h + (long long)first * p.sa.t;
-    const E *bp = reinterpret_cast<const E *>(p.b) + b * p.sb.b + h / p.rb * p.sb.h + (long long)first * p.sb.t;
-    const E *cp = reinterpret_cast<const E *>(p.c) + b * p.sc.b + h / p.rc * p.sc.h + (long long)first * p.sc.t;
-    const long long g0 = b * p.sg.b + h * p.sg.h + (long long)first * p.sg.t;
-    const size_t row0 = ((size_t)b * p.H + h) * p.seqs.T + first, sunit = ((size_t)b * p.H + h) * p.nslot + slot;
-    const size_t nstate = ((size_t)seq * p.H + h) * (DA * DC);
+    LinUnit<float> u;
+    if (!u.find(p, DA * DC) || (!OUT && u.alone)) return;
+    const int rows = u.rows, nchunk = u.nchunk;
 
     // the lane's 8 rows 32 kb + 8 g .. of its column in tile ct of a state in memory
     auto state_at = [&](int kb, int ct) {
@@ -497,10 +487,8 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
     };
     f32x4 P[NCT][NDT];
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    const float *from = !OUT ? nullptr : alone ? (p.init ? p.init + nstate : nullptr) : p.seg + sunit * (DA * DC);
-    float *to = !OUT ? p.seg + sunit * (DA * DC) : alone && p.final_state ? p.final_state + nstate : nullptr;
-    // a state that is handed on keeps all 24 bits; one that only feeds outputs does with 16
-    const bool whole = to != nullptr;
+    const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sunit * (DA * DC);
+    float *to = !OUT ? p.seg + u.sunit * (DA * DC) : u.alone && p.final_state ? p.final_state + u.nstate : nullptr;
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -523,16 +511,17 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
             P[ct][2 * kb + 1] = y;
         }
 
-    TileStage<F32, DA / 8> ta, tb;
-    TileStage<F32, DC / 8> tc;
+    const float *yp = DOT ? reinterpret_cast<const float *>(p.y) + u.b * p.sy.b + u.h / p.ry * p.sy.h + (long long)u.first * p.sy.t : nullptr;
+    TileStage<true, DA / 8> ta, tb;
+    TileStage<true, DC / 8> tc;
     float gn = 0.f;
     double total = 0.0;
     auto load = [&](int c, int tid) {
         const int lane = tid & 63;
-        if constexpr (OUT) ta.load(ap, p.sa.t, 64 * c, rows, tid);
-        tb.load(bp, p.sb.t, 64 * c, rows, tid);
-        tc.load(cp, p.sc.t, 64 * c, rows, tid);
-        if (w == NW - 1) gn = 64 * c + lane < rows ? load_g(p.g, g0 + (long long)(64 * c + lane) * p.sg.t, p.g32) : 0.f;
+        if constexpr (OUT) ta.load(u.ap, p.sa.t, 64 * c, rows, tid);
+        tb.load(u.bp, p.sb.t, 64 * c, rows, tid);
+        tc.load(u.cp, p.sc.t, 64 * c, rows, tid);
+        if (w == NW - 1) gn = 64 * c + lane < rows ? load_g(p.g, u.g0 + (long long)(64 * c + lane) * p.sg.t, p.g32) : 0.f;
     };
     auto decays = [&](int c, int par, int lane) {  // the last wave: it has least to do with the scores
         const double G = wave_scan64(decay_log2(gn)), last = lane64(G, 63);
@@ -600,10 +589,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
                         s[o][x] = (REV ? j + x < i || 64 * c + j + x >= rows : j + x > i) || (DOT && self) ? 0.f : m;
                     }
                 }
-                V8 m[MP];
-                Op::pieces(s[0], s[1], m);
-#pragma unroll
-                for (int x = 0; x < MP; ++x) Op::put_lane(sM + ((2 * it + jb) * MP + x) * FB, lane, m[x]);
+                Op::put_lane(sM + (2 * it + jb) * FB, lane, V8{s[0], s[1]});
             }
             __builtin_amdgcn_sched_barrier(0);
             f32x4 O[NCT][4];
@@ -613,16 +599,11 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
                 for (int it = 0; it < 4; ++it) O[ct][it] = zero;
 #pragma unroll
             for (int kb = 0; kb < NA; ++kb) {
-                V8 pf[NCT][MP];
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) Op::pieces(P[ct][2 * kb], P[ct][2 * kb + 1], pf[ct]);
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     const V8 af = Op::get(sA + (it * NA + kb) * FB, kb, lane);
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                        for (int x = 0; x < MP; ++x) O[ct][it] = Op::mma(pf[ct][x], af, O[ct][it]);
+                    for (int ct = 0; ct < NCT; ++ct) O[ct][it] = Op::mma(V8{P[ct][2 * kb], P[ct][2 * kb + 1]}, af, O[ct][it]);
                 }
             }
 #pragma unroll
@@ -637,12 +618,9 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     if (REV ? kb < (it >> 1) : kb > (it >> 1)) continue;
+                    const V8 m = Op::get_lane(sM + (2 * it + kb) * FB, lane);
 #pragma unroll
-                    for (int x = 0; x < MP; ++x) {
-                        const V8 m = Op::get_lane(sM + ((2 * it + kb) * MP + x) * FB, lane);
-#pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) O[ct][it] = Op::mma(cf[ct][kb], m, O[ct][it]);
-                    }
+                    for (int ct = 0; ct < NCT; ++ct) O[ct][it] = Op::mma(cf[ct][kb], m, O[ct][it]);
                 }
             const int c0 = perm_row(w * NCT, 4 * g);  // the lane's channels c0 .. + 4 NCT
 #pragma unroll
@@ -651,7 +629,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
                 if constexpr (DOT) {
                     float d = 0.f;
                     if (row < rows) {
-                        const E *y = reinterpret_cast<const E *>(p.y) + b * p.sy.b + h / p.ry * p.sy.h + (long long)(first + row) * p.sy.t + c0;
+                        const float *y = yp + (long long)row * p.sy.t + c0;
 #pragma unroll
                         for (int ct = 0; ct < NCT; ++ct) {
                             float v[4];
@@ -664,26 +642,18 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
                     if (g == 0) sDot[64 * w + i] = d;
                     // the term j = i, in float32: rows of C as they lie
                     const float m = sD[i];
-                    f32x4 x, y;
-                    Op::split(Op::get(sC + (it * NC + (w * NCT >> 1)) * FB, w * NCT >> 1, lane), x, y);
+                    const V8 x = Op::get(sC + (it * NC + (w * NCT >> 1)) * FB, w * NCT >> 1, lane);
                     if constexpr (NCT == 2) {
-                        O[0][it] += m * x;
-                        O[1][it] += m * y;
+                        O[0][it] += m * x.a;
+                        O[1][it] += m * x.b;
                     } else {
-                        O[0][it] += m * (w & 1 ? y : x);
+                        O[0][it] += m * (w & 1 ? x.b : x.a);
                     }
                 }
                 if (row < rows) {
-                    const size_t at = (row0 + row) * DC + c0;
-                    if constexpr (OUTF) {
-                        float *o = reinterpret_cast<float *>(p.out) + at;
+                    float *o = reinterpret_cast<float *>(p.out) + (u.row0 + row) * DC + c0;
 #pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) *reinterpret_cast<f32x4 *>(o + 4 * ct) = O[ct][it];
-                    } else if constexpr (NCT == 2) {
-                        Op::store8(reinterpret_cast<E *>(p.out) + at, O[0][it], O[1][it]);
-                    } else {
-                        st_tile(reinterpret_cast<E *>(p.out) + at, 0, O[0][it]);
-                    }
+                    for (int ct = 0; ct < NCT; ++ct) *reinterpret_cast<f32x4 *>(o + 4 * ct) = O[ct][it];
                 }
             }
         }
@@ -696,26 +666,15 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const f32x4 w0 = *reinterpret_cast<const lds_f4 *>(sWs + 32 * kb + 8 * g), w1 = *reinterpret_cast<const lds_f4 *>(sWs + 32 * kb + 8 * g + 4);
-            V8 xf[NCT][SP];
+            V8 xf[NCT];
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                f32x4 x, y;
-                Op::split(cf[ct][kb], x, y);
-                x *= w0;
-                y *= w1;
-                xf[ct][0] = Op::piece(x, y);
-                if constexpr (SP > 1) xf[ct][1] = Op::piece(x, y);
-                if (SP > 2 && (!OUT || whole)) xf[ct][SP - 1] = Op::piece(x, y);
-            }
+            for (int ct = 0; ct < NCT; ++ct) xf[ct] = V8{cf[ct][kb].a * w0, cf[ct][kb].b * w1};
 #pragma unroll
             for (int dt = 0; dt < NDT; ++dt) {
                 const lds_u8 *f = sB + (2 * kb * NA + (dt >> 1)) * FB;
                 const V8 bt = Op::get_t(f, f + NA * FB, dt, lane);
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-                    for (int x = 0; x < SP; ++x)
-                        if (!OUT || x < 2 || whole) P[ct][dt] = Op::mma(bt, xf[ct][x], P[ct][dt]);
+                for (int ct = 0; ct < NCT; ++ct) P[ct][dt] = Op::mma(bt, xf[ct], P[ct][dt]);
             }
         }
         if constexpr (DOT) {
@@ -724,11 +683,11 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void lin_walk_kernel(const LinWal
                 float d = 0.f;
 #pragma unroll
                 for (int k = 0; k < NW; ++k) d += sDot[64 * k + tid];
-                p.dots[row0 + 64 * c + tid] = d;
+                p.dots[u.row0 + 64 * c + tid] = d;
             }
         }
     }
-    if (!OUT && w == NW - 1 && (tid0 & 63) == 0) p.seg_decay[sunit] = ex2((float)total);
+    if (!OUT && w == NW - 1 && (tid0 & 63) == 0) p.seg_decay[u.sunit] = ex2((float)total);
     if (!to) return;
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct)

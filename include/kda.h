@@ -473,11 +473,12 @@ int kda_latent_tree_step(const void *q, const void *cache, const int *block_tabl
  *    g <= 0, and anything below -1000, -inf too, is a decay to zero.
  *  - the t strides of q, k, v and dout are not negative, and 64 of them take less than 2^31 bytes
  *    (KDA_ERR_SHAPE otherwise).
- *  - launches below 2^32 work-items (KDA_ERR_SHAPE): 2^24 segments of 256 to 2048 tokens over all heads,
- *    2^24 / (dk dv / 1024) sequences and heads, 2^24 pieces of 16 tokens of a head.
+ *  - launches below 2^32 work-items (KDA_ERR_SHAPE): 2^24 / (dk dv / 1024) sequences and heads, 2^24
+ *    pieces of 16 tokens of a head.
  *  - What is not finite in q reaches its token's outputs; in v its channel of the outputs from its chunk
  *    of 64 tokens on and of the state; in k or g its head's.
- * What feeds the state keeps all 24 bits, also with bf16 inputs. */
+ * States that are handed on (final_state, dinitial_state, between segments) gather all 24 bits, also with
+ * bf16 inputs; with bf16 inputs the state that only feeds a segment's outputs gathers 16. */
 size_t kda_lin_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
 
 int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
