@@ -214,8 +214,10 @@ def _append(latent, k_rope, cache, block_table, lengths, freqs, cu_seqlens, norm
     pk, sk = _view(k_rope, "k_rope", dtype, dev)
     pr, sr = _view(q_rope, "q_rope", dtype, dev) if q_rope is not None else (None, None)
     # (.., b, t) and (b, t, h) as the library's (b, h, t)
-    sl, sk = _S3(sl[1], 0, sl[2]), _S3(sk[1], 0, sk[2])
-    sr = None if sr is None else _S3(sr[0], sr[2], sr[1])
+    for s in (sl, sk):
+        s[0], s[1] = s[1], 0
+    if sr is not None:
+        sr[1], sr[2] = sr[2], sr[1]
     args = [_plain(cache, "cache", dtype, dev, (pages, page, dc + dr)),
             _plain(block_table, "block_table", torch.int32, dev, (N, max_pages)), _plain(lengths, "lengths", torch.int32, dev, (N,)),
             _plain(freqs, "freqs", torch.float32, dev, (dr // 2,)), _plain(norm_weight, "norm_weight", dtype, dev, (dc,)), float(eps),
@@ -281,16 +283,22 @@ def latent_tree_step(q, cache, block_table, lengths, tree_mask, scale, dc=512, c
             _plain(block_table, "block_table", torch.int32, dev, (B, max_pages)),
             _plain(lengths, "lengths", torch.int32, dev, (B,)), _plain(counts, "counts", torch.int32, dev, (B,)),
             _plain(tree_mask, "tree_mask", torch.int64, dev, (B, T))]
+    po, pl = _plain(out, "out", dtype, dev, (B, T, H, dc)), _plain(lse, "lse", torch.float32, dev, (B, T, H))
+    L, io = lib(), _DTYPES[dtype]
     with _on_device(dev):
         if out is None:
             out = _empty((B, T, H, dc), dtype, dev, stream)
+            po = out.data_ptr()
         if lse is None:
             lse = _empty((B, T, H), torch.float32, dev, stream)
-        need = latent_tree_workspace_bytes(B, T, H, page, max_pages, dc, D - dc, dtype)
-        workspace = _workspace(workspace, need, dev, stream)
-        st = lib().kda_latent_tree_step(*ptrs, B, T, H, pages, page, max_pages, dc, D - dc, _DTYPES[dtype], float(scale),
-                                        _plain(out, "out", dtype, dev, (B, T, H, dc)), _plain(lse, "lse", torch.float32, dev, (B, T, H)),
-                                        workspace.data_ptr(), workspace.numel(), _stream_of(stream, dev))
+            pl = lse.data_ptr()
+        need = L.kda_latent_tree_workspace_bytes(B, T, H, page, max_pages, dc, D - dc, io)
+        room = (None, 0)
+        if need or workspace is not None:
+            workspace = _workspace(workspace, need, dev, stream)
+            room = (workspace.data_ptr(), workspace.numel())
+        st = L.kda_latent_tree_step(*ptrs, B, T, H, pages, page, max_pages, dc, D - dc, io, float(scale), po, pl, *room,
+                                    _stream_of(stream, dev))
     if st != KDA_OK:
         raise KdaError("kda_latent_tree_step", st)
     return (out, lse) if return_lse else out

@@ -52,16 +52,23 @@ def _fwd(q, k, v, g, cu_seqlens, scale, out, final_state, return_final_state, in
     args += _view(g, "g", g.dtype, dev, inner=False)
     cu = None if cu_seqlens is None else _plain(cu_seqlens, "cu_seqlens", torch.int32, dev, (N + 1,))
     s0 = _plain(initial_state, "initial_state", torch.float32, dev, (N, H, dv, dk))
+    po = _plain(out, "out", dtype, dev, lead + (H, T, dv))
+    pf = _plain(final_state, "final_state", torch.float32, dev, (N, H, dv, dk))
+    L, io = lib(), _DTYPES[dtype]
     with _on_device(dev):
         if out is None:
             out = _empty(lead + (H, T, dv), dtype, dev, stream)
+            po = out.data_ptr()
         if final_state is None and return_final_state:
             final_state = _empty((N, H, dv, dk), torch.float32, dev, stream)
-        po = _plain(out, "out", dtype, dev, lead + (H, T, dv))
-        pf = _plain(final_state, "final_state", torch.float32, dev, (N, H, dv, dk))
-        workspace = _workspace(workspace, lin_workspace_bytes(N, Hk, H, T, dk, dv, dtype, cu is not None), dev, stream)
-        st = lib().kda_lin_chunk_fwd(*args, cu, N, Hk, H, T, dk, dv, _DTYPES[dtype], _DTYPES[g.dtype], float(scale), s0, po, pf,
-                                     workspace.data_ptr(), workspace.numel(), _stream_of(stream, dev))
+            pf = final_state.data_ptr()
+        need = L.kda_lin_workspace_bytes(0, int(cu is not None), N, Hk, H, T, dk, dv, io)
+        room = (None, 0)
+        if need or workspace is not None:
+            workspace = _workspace(workspace, need, dev, stream)
+            room = (workspace.data_ptr(), workspace.numel())
+        st = L.kda_lin_chunk_fwd(*args, cu, N, Hk, H, T, dk, dv, io, _DTYPES[g.dtype], float(scale), s0, po, pf, *room,
+                                 _stream_of(stream, dev))
     if st != KDA_OK:
         raise KdaError("kda_lin_chunk_fwd", st)
     return (out, final_state) if return_final_state else out
