@@ -435,7 +435,8 @@ int kda_latent_decode_step(const void *q, const void *cache, const int *block_ta
  *    sequences, boundaries clipped to the stream; counts is NULL then (KDA_ERR_NULL otherwise).
  *  - A token whose row is negative, behind the table, or on a page outside the cache is not written into
  *    the cache; what is no token (behind its sequence's count, outside the boundaries) is not written at
- *    all.  Two tokens on one row (a page twice in the table) leave one of the two.
+ *    all.  Two tokens on one row (a page twice in the table) leave pieces of 16 bytes of either.
+ *  - q_rope may be the last dr channels of q itself; nothing else of what is read may be written.
  *  - dc in {256, 512}, dr = 64; eps >= 0 (KDA_ERR_SCALE otherwise); a launch below 2^32 work-items
  *    (KDA_ERR_SHAPE): 2^26 tokens and 32 heads. */
 int kda_latent_append(const void *latent, const kda_strides *latent_strides, const void *k_rope,

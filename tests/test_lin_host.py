@@ -110,3 +110,13 @@ def test_binding_refusals():
         kda.lin_chunk_bwd_varlen(x[0], x[0], x[0], g[0], x[0], None)
     with pytest.raises(ValueError):
         kda.lin_decode_step(x[:, :, 0], x[:, :, 0], x[:, :, 0], g[..., 0], torch.zeros(1, 2, 64, 64))
+
+
+def test_leaves_are_not_captured(monkeypatch):
+    """A leaf gathers its gradient on another stream than the captured one where an eager graph of it lives."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    x, g = torch.zeros(1, 2, 8, 64), torch.zeros(1, 2, 8)
+    with pytest.raises(RuntimeError, match="leaf"):
+        kda.LinChunkFunction.apply(x, x, x.clone().requires_grad_(), g)
+    with pytest.raises(ValueError):  # none: as far as the check of the device
+        kda.LinChunkFunction.apply(x, x, x.clone().requires_grad_() * 1, g)
