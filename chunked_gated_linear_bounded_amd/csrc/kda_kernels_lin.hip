@@ -29,7 +29,7 @@ static hipError_t fwd_t(const LinLaunch &p) {
         const size_t units = (size_t)p.B * p.H * a.nslot;
         a.seg = reinterpret_cast<float *>(p.workspace);
         a.seg_decay = a.seg + units * DK * DV;
-        hipError_t e = lin_walk<DK, DV, F32, false, false, false, false, false>(a, grid, p.stream);
+        hipError_t e = lin_own_states<DK, DV, F32, false>(p, a);
         if (e != hipSuccess) return e;
         LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {{p.init_state, a.seg, p.final_state, a.seg_decay, false}, {}}};
         hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)p.N * p.H * (DK * DV / 1024)), dim3(256), 0, p.stream, s);

@@ -68,8 +68,8 @@ static hipError_t bwd_t(const LinLaunch &p) {
     s1.into = p.scale;
     s1.seg = f(m.seg[1]);
     s1.seg_decay = f(m.decay[1]);
-    if (many || want_last) KDA_WALK((lin_walk<DK, DV, F32, false, false, false, false, false>(s0, grid, p.stream)));
-    if (many) KDA_WALK((lin_walk<DK, DV, F32, true, false, false, false, false>(s1, grid, p.stream)));
+    if (many || want_last) KDA_WALK((lin_own_states<DK, DV, F32, false>(p, s0)));
+    if (many) KDA_WALK((lin_own_states<DK, DV, F32, true>(p, s1)));
     if (many || want_last) {
         LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {}};
         s.side[0] = {p.init_state, f(m.seg[0]), want_last ? f(m.last) : nullptr, f(m.decay[0]), want_last};

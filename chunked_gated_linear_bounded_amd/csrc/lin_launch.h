@@ -58,7 +58,7 @@ hipError_t launch_lin_decode(const LinLaunch &p);
 // Whether the launches of a call stay below 2^32 work-items in x, which is as far as a launch goes, and
 // their unit counts in 32 bits.
 inline bool lin_grids_fit(const LinLaunch &p) {
-    const long long most = 4294967295LL, units = (long long)p.B * p.H * lin_slots(p);
+    const long long most = 4294967295LL, units = (long long)p.B * p.H * lin_slots(p) * (p.dv / 64);
     const long long states = (long long)p.N * p.H * (p.dk * p.dv / 1024);
     const long long rows = (long long)p.B * p.H * (((long long)p.T + 15) / 16);
     return (units + 7) / 8 * 8 <= most / 512 && states <= most / 256 && rows <= most / 256;

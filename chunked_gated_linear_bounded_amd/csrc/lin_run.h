@@ -20,9 +20,12 @@ inline LinWalkArgs lin_walk_args(const LinLaunch &p) {
     a.nslot = (int)lin_slots(p);
     a.scale = p.scale;
     a.inter = a.into = 1.f;
+    a.parts = 1;
     return a;
 }
-inline unsigned lin_walk_grid(const LinLaunch &p) { return (unsigned)(((long long)p.B * p.H * lin_slots(p) + 7) / 8 * 8); }
+inline unsigned lin_walk_grid(const LinLaunch &p, int parts = 1) {
+    return (unsigned)(((long long)p.B * p.H * lin_slots(p) * parts + 7) / 8 * 8);
+}
 
 // Either walk: bf16 with helpers beside the walkers, float32 (whose tiles fill the LDS once) in one group.
 template <int DA, int DC, bool F32, bool REV, bool TR, bool OUT, bool DOT, bool OUTF>
@@ -30,6 +33,18 @@ inline hipError_t lin_walk(const LinWalkArgs &a, unsigned grid, hipStream_t stre
     if constexpr (F32) hipLaunchKernelGGL((lin_walk32_kernel<DA, DC, REV, TR, OUT, DOT>), dim3(grid), dim3(256), 0, stream, a);
     else hipLaunchKernelGGL((lin_pair_kernel<DA, DC, REV, TR, OUT, DOT, OUTF>), dim3(grid), dim3(512), 0, stream, a);
     return hipGetLastError();
+}
+
+// Pass 1, the segments' own states.  In bf16 work-groups of 64 of c's channels: they read b twice, from the
+// second's neighbour's L2, but two of them share a CU.
+template <int DA, int DC, bool F32, bool REV>
+inline hipError_t lin_own_states(const LinLaunch &p, LinWalkArgs a) {
+    if constexpr (F32) {
+        return lin_walk<DA, DC, true, REV, false, false, false, false>(a, lin_walk_grid(p), p.stream);
+    } else {
+        a.parts = DC / 64;
+        return lin_walk<DA, 64, false, REV, false, false, false, false>(a, lin_walk_grid(p, a.parts), p.stream);
+    }
 }
 
 }  // namespace kda

@@ -20,6 +20,7 @@ struct LinWalkArgs {
     int ra, rb, rc, ry;              // value heads that share a head of that tensor
     LinSeqs seqs;
     int B, H, nslot;
+    int parts;                       // work-groups that share the columns of a segment's own state (pass 1)
     bool g32, all;                   // all: segments that are alone in their sequence take part as others do
     float scale, inter, into;
     const float *init;               // [N][H] start states of the sequences (NULL: zero), for segments that are alone
@@ -32,15 +33,18 @@ struct LinWalkArgs {
 
 // Where a work-group's segment lies, and its rows.
 template <typename E> struct LinUnit {
-    int b, h, seq, first, rows, nchunk;
+    int b, h, part, seq, first, rows, nchunk;
     bool alone;
     const E *ap, *bp, *cp;
     long long g0;
     size_t row0, sunit, nstate;
-    // false: nothing there.  Units in eight runs, one an XCD: heads that share rows are neighbours there.
-    __device__ __forceinline__ bool find(const LinWalkArgs &p, int state) {
-        const unsigned units = (unsigned)p.B * p.H * p.nslot, per = (units + 7) / 8, unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-        if ((blockIdx.x >> 3) >= per || unit >= units) return false;
+    // false: nothing there.  Units in eight runs, one an XCD: parts of a state and heads that share rows are
+    // neighbours there.
+    __device__ __forceinline__ bool find(const LinWalkArgs &p, int state, int parts = 1) {
+        const unsigned all = (unsigned)p.B * p.H * p.nslot * parts, per = (all + 7) / 8, at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+        if ((blockIdx.x >> 3) >= per || at >= all) return false;
+        part = at % parts;
+        const unsigned unit = at / parts;
         h = unit % p.H;
         b = unit / p.H / p.nslot;
         const int slot = unit / p.H % p.nslot;
@@ -86,16 +90,17 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
     typedef __attribute__((address_space(3))) float lds_f;
     typedef __attribute__((address_space(3))) f32x4 lds_f4;
     __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * TILE + (OUT ? 2 * MB : 0)];
-    // by chunk parity: prefix sums in two floats, weights of the outputs and of the sources, e^{G_last}; the
-    // scores of tokens with themselves; and the walkers' dot products
-    __shared__ __attribute__((aligned(16))) float sg[2 * 320 + (DOT ? 2 * 64 + 4 * 64 : 0)];
+    // for eight chunks: prefix sums in two floats, weights of the outputs and of the sources, e^{G_last}; the
+    // scores of tokens with themselves, by parity; and the walkers' dot products
+    __shared__ __attribute__((aligned(16))) float sg[8 * 320 + (DOT ? 2 * 64 + 4 * 64 : 0)];
     lds_u8 *sT = lds_base(smem), *sM = sT + 2 * TILE;
-    lds_f *sG = (lds_f *)lds_base(sg), *sD = sG + 640, *sDot = sG + 768;
+    lds_f *sG = (lds_f *)lds_base(sg), *sD = sG + 8 * 320, *sDot = sD + 128;
     const int tid = threadIdx.x & 255, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool helper = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     LinUnit<E> u;
-    if (!u.find(p, DA * DC) || (!OUT && u.alone)) return;
+    if (!u.find(p, DA * DC, OUT ? 1 : p.parts) || (!OUT && u.alone)) return;
+    if (!OUT) u.cp += u.part * DC;
     const int nchunk = u.nchunk, rows = u.rows;
     auto chunk_of = [&](int ci) { return REV ? nchunk - 1 - ci : ci; };
     auto tile_b = [&](int par) { return sT + par * TILE; };
@@ -117,30 +122,37 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
             if constexpr (OUT) s.ta.load(u.ap, p.sa.t, 64 * c, rows, tid);
             s.tb.load(u.bp, p.sb.t, 64 * c, rows, tid);
             s.tc.load(u.cp, p.sc.t, 64 * c, rows, tid);
-            if (w == 3) s.gn = 64 * c + lane < rows ? load_g(p.g, u.g0 + (long long)(64 * c + lane) * p.sg.t, p.g32) : 0.f;
+            // log-decays of four chunks at a time, one a wave: a scan in float64 is a long chain, and every chunk
+            // would wait for it
+            if ((ci & 3) == 0 && ci + w < nchunk) {
+                const int row = 64 * chunk_of(ci + w) + lane;
+                s.gn = row < rows ? load_g(p.g, u.g0 + (long long)row * p.sg.t, p.g32) : 0.f;
+            }
         };
-        auto store = [&](int ci, const Stage &st) {  // and the decays
+        auto decays = [&](int ci, float gn) {
+            if (ci + w >= nchunk) return;
+            const double G = wave_scan64(decay_log2(gn)), last = lane64(G, 63);
+            const float hi = (float)G, e0 = ex2(hi), e1 = ex2((float)(last - G));
+            lds_f *s = sG + 320 * ((ci + w) & 7);
+            s[lane] = hi;
+            s[64 + lane] = (float)(G - (double)hi);
+            s[128 + lane] = p.inter * (REV ? e1 : e0);
+            // rows behind the last arrive as zeros, or as earlier rows where rows overlap (strides below a row)
+            s[192 + lane] = 64 * chunk_of(ci + w) + lane < rows ? p.into * (REV ? e0 : e1) : 0.f;
+            if (lane == 0) s[256] = ex2((float)last);
+            total += last;
+        };
+        auto store = [&](int ci, const Stage &st) {  // and the decays of this chunk and the next three
             const int par = ci & 1;
             if constexpr (OUT) st.ta.store(tile_a(par), NA, 0, tid);
             st.tb.store(tile_b(par), NA, 0, tid);
             st.tc.store(tile_c(par), NC, 0, tid);
-            if (w == 3) {
-                const double G = wave_scan64(decay_log2(st.gn)), last = lane64(G, 63);
-                const float hi = (float)G, e0 = ex2(hi), e1 = ex2((float)(last - G));
-                lds_f *s = sG + 320 * par;
-                s[lane] = hi;
-                s[64 + lane] = (float)(G - (double)hi);
-                s[128 + lane] = p.inter * (REV ? e1 : e0);
-                // rows behind the last arrive as zeros, or as earlier rows where rows overlap (strides below a row)
-                s[192 + lane] = 64 * chunk_of(ci) + lane < rows ? p.into * (REV ? e0 : e1) : 0.f;
-                if (lane == 0) s[256] = ex2((float)last);
-                total += last;
-            }
+            if ((ci & 3) == 0) decays(ci, st.gn);
         };
         auto scores = [&](int ci) {
             const int par = ci & 1, left = rows - 64 * chunk_of(ci);
             const lds_u8 *sA = tile_a(par), *sB = tile_b(par);
-            const lds_f *sH = sG + 320 * par;
+            const lds_f *sH = sG + 320 * (ci & 7);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int f = w == 0 ? 4 * k : w == 1 ? 1 + 4 * k : w;  // waves 0 and 1 take two of the six
@@ -204,7 +216,13 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
             if (ci + 1 < nchunk) step(ci + 1, st0);
         }
         if (DOT && nchunk > 0) dots(nchunk - 1);
-        if (!OUT && threadIdx.x == 448) p.seg_decay[u.sunit] = ex2((float)total);
+        if constexpr (!OUT) {
+            typedef __attribute__((address_space(3))) double lds_d;
+            lds_d *sum = (lds_d *)sG;
+            if (lane == 0) sum[w] = total;
+            barrier_lds();
+            if (tid == 0 && u.part == 0) p.seg_decay[u.sunit] = ex2((float)((sum[0] + sum[1]) + (sum[2] + sum[3])));
+        }
         return;
     }
 
@@ -216,7 +234,7 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
     f32x4 P[NCT][NDT];
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sunit * (DA * DC);
-    float *to = !OUT ? p.seg + u.sunit * (DA * DC) : u.alone && p.final_state ? p.final_state + u.nstate : nullptr;
+    float *to = !OUT ? p.seg + (u.sunit * p.parts + u.part) * (DA * DC) : u.alone && p.final_state ? p.final_state + u.nstate : nullptr;
     // a state that is handed on keeps all 24 bits; one that only feeds outputs does with 16
     const bool whole = to != nullptr;
 #pragma unroll
@@ -270,7 +288,7 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
         const int c = chunk_of(ci), par = ci & 1;
         // (through lane_here: a chunk's addresses are made in the chunk, or they would fill the registers)
         const int lane = lane_here(lane0), g = lane >> 4, n = lane & 15, c0 = perm_row(w * NCT, 4 * g);  // the lane's channels c0 .. + 4 NCT
-        const lds_f *sH = sG + 320 * par, *sWd = sH + 128, *sWs = sH + 192;
+        const lds_f *sH = sG + 320 * (ci & 7), *sWd = sH + 128, *sWs = sH + 192;
         const lds_u8 *sA = tile_a(par), *sB = tile_b(par), *sC = tile_c(par);
         V8 ring[RING];
         V8 cf[NCT][2];  // C transposed, the wave's columns
@@ -439,6 +457,7 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
         }
         barrier_lds();
     }
+    if constexpr (!OUT) barrier_lds();  // the helpers' sums
     if (!to) return;
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct)
