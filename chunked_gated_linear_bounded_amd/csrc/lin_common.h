@@ -83,8 +83,12 @@ __device__ __forceinline__ double lane64(double x, int lane) {
 // a log-decay in log2 units; below -1000 (-inf too) it is a decay to zero, and sums stay finite
 __device__ __forceinline__ double decay_log2(float g) { return (double)(g < -1000.f ? -1000.f : g) * 1.4426950408889634; }
 
-__device__ __forceinline__ float load_g(const void *g, long long at, bool g32) {
-    return g32 ? reinterpret_cast<const float *>(g)[at] : (float)reinterpret_cast<const __bf16 *>(g)[at];
+// a log-decay as it lies in memory, and its value: apart, so that nothing waits for the load before its use
+__device__ __forceinline__ unsigned load_g_bits(const void *g, long long at, bool g32) {
+    return g32 ? reinterpret_cast<const unsigned *>(g)[at] : reinterpret_cast<const unsigned short *>(g)[at];
+}
+__device__ __forceinline__ float g_value(unsigned bits, bool g32) { return __builtin_bit_cast(float, g32 ? bits : bits << 16); }
+__device__ __forceinline__ float load_g(const void *g, long long at, bool g32) { return g_value(load_g_bits(g, at, g32), g32);
 }
 
 // ---------------------------------------------------------------- operands

@@ -113,25 +113,26 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
         struct Stage {  // one chunk on its way: two of them, so that a chunk's loads have two chunks' time
             TileStage<false, DA / 8> ta, tb;
             TileStage<false, DC / 8> tc;
-            float gn;
+            unsigned g;
         } st0, st1;
         double total = 0.0;
+        // (of no rows behind the last chunk: were the loads left out there, none could be waited for without
+        // those behind it)
         auto load = [&](int ci, Stage &s) {
-            if (ci >= nchunk) return;
-            const int c = chunk_of(ci);
-            if constexpr (OUT) s.ta.load(u.ap, p.sa.t, 64 * c, rows, tid);
-            s.tb.load(u.bp, p.sb.t, 64 * c, rows, tid);
-            s.tc.load(u.cp, p.sc.t, 64 * c, rows, tid);
+            const int c = ci < nchunk ? chunk_of(ci) : 0, n = ci < nchunk ? rows : 0;
+            if constexpr (OUT) s.ta.load(u.ap, p.sa.t, 64 * c, n, tid);
+            s.tb.load(u.bp, p.sb.t, 64 * c, n, tid);
+            s.tc.load(u.cp, p.sc.t, 64 * c, n, tid);
             // log-decays of four chunks at a time, one a wave: a scan in float64 is a long chain, and every chunk
             // would wait for it
             if ((ci & 3) == 0 && ci + w < nchunk) {
                 const int row = 64 * chunk_of(ci + w) + lane;
-                s.gn = row < rows ? load_g(p.g, u.g0 + (long long)row * p.sg.t, p.g32) : 0.f;
+                s.g = row < rows ? load_g_bits(p.g, u.g0 + (long long)row * p.sg.t, p.g32) : 0u;
             }
         };
-        auto decays = [&](int ci, float gn) {
+        auto decays = [&](int ci, unsigned bits) {
             if (ci + w >= nchunk) return;
-            const double G = wave_scan64(decay_log2(gn)), last = lane64(G, 63);
+            const double G = wave_scan64(decay_log2(g_value(bits, p.g32))), last = lane64(G, 63);
             const float hi = (float)G, e0 = ex2(hi), e1 = ex2((float)(last - G));
             lds_f *s = sG + 320 * ((ci + w) & 7);
             s[lane] = hi;
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
             if constexpr (OUT) st.ta.store(tile_a(par), NA, 0, tid);
             st.tb.store(tile_b(par), NA, 0, tid);
             st.tc.store(tile_c(par), NC, 0, tid);
-            if ((ci & 3) == 0) decays(ci, st.gn);
+            if ((ci & 3) == 0) decays(ci, st.g);
         };
         auto scores = [&](int ci) {
             const int par = ci & 1, left = rows - 64 * chunk_of(ci);
@@ -211,10 +212,12 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
                 barrier_lds();
             }
         }
-        for (int ci = 0; ci < nchunk; ci += 2) {
+        int ci = 0;  // (steps in pairs, or loads in flight would be counted as if every step could be the last)
+        for (; ci + 1 < nchunk; ci += 2) {
             step(ci, st1);
-            if (ci + 1 < nchunk) step(ci + 1, st0);
+            step(ci + 1, st0);
         }
+        if (ci < nchunk) step(ci, st1);
         if (DOT && nchunk > 0) dots(nchunk - 1);
         if constexpr (!OUT) {
             typedef __attribute__((address_space(3))) double lds_d;
