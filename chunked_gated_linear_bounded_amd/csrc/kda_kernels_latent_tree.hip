@@ -7,35 +7,45 @@
 namespace kda {
 
 static long long rows(const LatentTreeLaunch &p) { return (long long)p.T * p.H; }
-// column tiles of 16 rows a work-group takes (float32: the queries of 32 rows fill the registers)
+static long long key_tiles(const LatentTreeLaunch &p) { return ((long long)p.max_pages * p.page + 63) / 64; }
+// Column tiles of 16 rows a work-group takes: as many as there are rows for (float32: the queries of 32 rows fill
+// the registers), because a fragment of keys is read once for all of them (24 sequences x 8 tokens x 128
+// heads on 9000 rows: 452 us with four, 774 with two); fewer where there would not be two tiles of keys for every CU
+// (3 x 5 x 16 on 700: 15 us of kernel with one, 18 with two, 24 with four; 8 x 4 x 16 on 1500: 30 us a call with one,
+// 35 with two).
 static int tiles(const LatentTreeLaunch &p) {
     const int most = rows(p) <= 16 ? 1 : rows(p) <= 32 || p.fp32 ? 2 : 4;
-    const long long keys = ((long long)p.max_pages * p.page + 63) / 64;
     for (int n = most; n > 1; n /= 2)
-        if (p.B * ((rows(p) + 16 * n - 1) / (16 * n)) * keys >= 512) return n;
+        if (p.B * ((rows(p) + 16 * n - 1) / (16 * n)) * key_tiles(p) >= 512) return n;
     return 1;
 }
 static int groups(const LatentTreeLaunch &p) { return (int)((rows(p) + 16 * tiles(p) - 1) / (16 * tiles(p))); }
-// Work-groups that share all tiles evenly (latent_tree.h), one a CU, as long as the units alone do not fill
-// the card four times over, and no more than there can be tiles; 0: one a unit.
+// Work-groups that share all tiles evenly (latent_tree.h), one a CU and no more than there can be tiles; 0: one a
+// unit.  Pieces cost their float32 values written and read again and a launch, as much as some 24 tiles of 64
+// rows; units of their own leave CUs idle in the last round.  (256 units of 64 rows, up to 3000 keys: 204 us
+// shared, 156 a unit each; 512: 341 and 303; 384 of 9000: 452 and 478; 1 x 1 x 16 on 40,000: 97 and 974.  Four
+// rounds even out by themselves: 1500 units on 1000 keys 399 and 355.)  Tiles of fewer rows are as much
+// shorter.  float32 tiles are eight times as long, and uneven lengths cost more than pieces: 256 units of 32 rows
+// on up to 2000 keys 377 us shared, 430 a unit each.
 static int shared(const LatentTreeLaunch &p) {
-    const long long units = (long long)p.B * groups(p), most = units * (((long long)p.max_pages * p.page + 63) / 64);
-    return units >= 1024 ? 0 : most < 256 ? (int)most : 256;
+    const long long units = (long long)p.B * groups(p), idle = ((units + 255) / 256 * 256 - units) * key_tiles(p) / 256;
+    const long long most = units * key_tiles(p);
+    if (units >= 1024 || most == 1 || (!p.fp32 && idle < 6 * tiles(p))) return 0;
+    return most < 256 ? (int)most : 256;
 }
 static size_t part_rows(const LatentTreeLaunch &p) { return 2 * (size_t)shared(p) * 16 * tiles(p); }
 size_t latent_tree_bytes(const LatentTreeLaunch &p) {
-    return shared(p) <= 1 ? 0 : part_rows(p) * (p.dc + 1) * 4 + ((size_t)p.B + 2) * 4;
+    return shared(p) == 0 ? 0 : part_rows(p) * (p.dc + 1) * 4 + ((size_t)p.B + 2) * 4;
 }
 bool latent_tree_grid_fits(const LatentTreeLaunch &p) {
-    const long long units = (long long)p.B * groups(p), tiles = ((long long)p.max_pages * p.page + 63) / 64;
-    return (units + 7) / 8 * 8 <= 4294967295LL / 256 && (units >= 1024 || units * tiles <= 2147483647LL);
+    const long long units = (long long)p.B * groups(p);
+    return (units + 7) / 8 * 8 <= 4294967295LL / 256 && (shared(p) == 0 || units * key_tiles(p) <= 2147483647LL);
 }
 
 template <int DC, bool F32, int NQ>
 static hipError_t run(const LatentTreeLaunch &p) {
     LatentTreeArgs a{p.q, p.cache, p.table, p.lengths, p.counts, p.mask, p.B, p.T, p.H, p.pages, p.page, p.max_pages, groups(p),
                      p.scale, p.out, p.lse, shared(p), reinterpret_cast<float *>(p.workspace), nullptr, nullptr};
-    if (a.groups == 1) a.groups = 0;  // one unit of one tile
     a.part_lse = a.part + part_rows(p) * DC;
     a.from = reinterpret_cast<int *>(a.part_lse + part_rows(p));
     const long long all = a.groups > 0 ? a.groups : (long long)p.B * a.rgroups;

@@ -50,11 +50,12 @@ def test_tree_refusals(kw, want):
 
 
 def test_tree_workspace_bytes():
-    # nothing from 1024 units (of 64 rows) on; below that two units' rows of out and lse for each of up to 256
-    # work-groups, and the sequences' first tiles
+    # nothing from 1024 units (of 64 rows) on, and where a last round of units leaves few CUs idle; else two
+    # units' rows of out and lse for each of up to 256 work-groups, and the sequences' first tiles
     assert kda.latent_tree_workspace_bytes(64, 32, 128, 64, 40, 512, 64, BF) == 0
     assert kda.latent_tree_workspace_bytes(16, 32, 128, 64, 40, 512, 64, BF) == 0
-    assert kda.latent_tree_workspace_bytes(15, 32, 128, 64, 40, 512, 64, BF) == 2 * 256 * 64 * 513 * 4 + 17 * 4
+    assert kda.latent_tree_workspace_bytes(12, 32, 128, 64, 40, 512, 64, BF) == 0
+    assert kda.latent_tree_workspace_bytes(13, 32, 128, 64, 40, 512, 64, BF) == 2 * 256 * 64 * 513 * 4 + 15 * 4
     # few tiles: 16 rows a unit, and no more work-groups than tiles
     assert kda.latent_tree_workspace_bytes(1, 5, 16, 64, 40, 512, 64, BF) == 2 * 200 * 16 * 513 * 4 + 3 * 4
     assert kda.latent_tree_workspace_bytes(1, 1, 3, 64, 1, 256, 64, F32) == 0  # one tile
