@@ -12,6 +12,10 @@
 //    MFMAs; P is handed round through LDS.
 // 64 keys are a tile, loaded straight into LDS, the next one into a second buffer meanwhile: 136 MFMAs a
 // wave (2,176 cycles) on 45 KiB of LDS reads.
+// 24 sequences x 8 tokens x 128 heads on up to 9000 rows: 410 us, 0.9 PFLOP/s, matrix units 43 % busy, vector
+// unit 24 %, LDS 41 % and 7 in bank conflicts.  With one wave a SIMD nothing covers a tile's softmax, its
+// barrier and the first reads behind it; a third buffer, for the next scores to run beside them, does not fit the
+// LDS.
 //
 // The exponentials are taken against a maximum that may be 2^8 too small, so that the accumulator is
 // scaled a few times a row and not every tile: a wave makes P with the maximum it has, says whether a row
@@ -183,7 +187,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
     if ((blockIdx.x >> 3) >= run || me >= all) return;
     int b, rg, t0 = 0, left;
     if (p.groups > 0) {
-        // tiles in front of each sequence: 256 sequences a step
+        // tiles in front of each sequence (fewer than 1024 where work is shared): 256 sequences a step
         lds_i *si = (lds_i *)lds_base(smem);
         int total = 0;
         for (int b0 = 0; b0 < p.B; b0 += 256) {
@@ -511,7 +515,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
 // Joins the pieces of the units that more than one work-group had: weights 2^(lse_i - max).  Work-group x of
 // the first grid dimension takes the unit that work-group x of the kernel above began and did not end; a
 // wave takes 256 channels of one row, lane i the weight of piece i, and four pieces' values are on their way
-// at a time.
+// at a time.  It moves bytes: 24 x 8 x 128 heads 23 us, 67 MB read and 17 written.
 template <int DC, int NQ, typename E>
 __global__ __launch_bounds__(256) void latent_tree_join_kernel(const LatentTreeArgs p) {
     constexpr int WPR = DC / 256, ROWS = 4 / WPR;  // waves a row; rows a work-group

@@ -2,7 +2,7 @@
 //   S <- e^g S + v k^T,   o = scale S q.
 // The state is read and written once (8 dk dv bytes a head), so HBM bounds a full batch and the launch a
 // single user.  As in the gated delta rule's step a wave takes 4 value rows, 16 bytes of a row a lane,
-// every load issued before the first use.
+// every load issued before the first use.  256 users x 32 heads of 128 x 128: 1.07 GB in 187 us, 5.7 TB/s.
 #pragma once
 #include "kda_decode.h"
 #include "lin_common.h"

@@ -36,7 +36,8 @@ inline hipError_t lin_walk(const LinWalkArgs &a, unsigned grid, hipStream_t stre
 }
 
 // Pass 1, the segments' own states.  In bf16 work-groups of 64 of c's channels: they read b twice, from the
-// second's neighbour's L2, but two of them share a CU.
+// second's neighbour's L2, but two of them share a CU (64k x 32 heads 797 us a call against 808, the training step of 2 x 4096 x 16 heads 314
+// against 319).
 template <int DA, int DC, bool F32, bool REV>
 inline hipError_t lin_own_states(const LinLaunch &p, LinWalkArgs a) {
     if constexpr (F32) {

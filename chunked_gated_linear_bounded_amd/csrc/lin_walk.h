@@ -74,9 +74,11 @@ template <typename E> struct LinUnit {
 // As one group of four waves that did all of it in turn, two work-groups on a CU, a chunk took 17,400 cycles
 // of a work-group, half of them waits, and the parts' times added up (4 x 8192 x 16 heads 248 us against 202).
 //
-// 1 x 65536 x 32 heads of 128 x 128: pass 1 takes 300 us, of which its reads (1.07 GB) are 230 at a copy's
-// rate; pass 2 560, where its traffic (2.1 GB) alone takes 414 and the walkers' chain of MFMAs, LDS reads and
-// pieces alone 409, 3.2 us a chunk: one group a CU has nothing to put into either's gaps.
+// 1 x 65536 x 32 heads of 128 x 128, 256 segments of 128 chunks: pass 1 takes 236 us (its loads of 0.8 GB alone
+// 153, its products and pieces alone 205), pass 2 460 (its 1.6 GB alone 290, the rest alone 375).  A SIMD has some
+// 1000 vector instructions of 4 cycles a chunk of pass 2, most of them pieces of P and of the weighted C, beside
+// 160 MFMAs of 16: vector issue 49 % and matrix units 37 % busy (pass 1: 67 and 44), in two waves a SIMD that go
+// each in order.
 //
 // OUT: pass 2, the outputs; else pass 1, the segment's own contribution to the state.  TR: states in memory
 // have b's channels as rows, else c's.
