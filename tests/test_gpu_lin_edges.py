@@ -215,3 +215,49 @@ def test_values_far_apart(dtype):
     ref = U.one(q[0, 0], k[0, 0], v[0, 0], g[0, 0], 0.1, dtype, dtype, s0[0, 0], do[0, 0], df[0, 0])
     for n, (value, bound) in ref.items():
         U.check(got[n][0, 0], value, bound + U.HALF[dtype] * value.abs() * 1.01, n)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,Hk,H,T,dk,dv", [
+    (8, 4, 8, 1297, 64, 64),     # 21 chunks a head: segments of six, six, six and three (float32: of three)
+    (4, 8, 32, 1100, 128, 64),   # 18: nine and nine, key heads shared by four
+    (16, 16, 32, 450, 64, 128),  # eight: all of a sequence in one
+    (1, 64, 128, 833, 128, 128),  # 14: seven and seven, the last of one row
+])
+def test_segments_of_several_chunks(B, Hk, H, T, dk, dv, dtype):
+    """Full cards, where a segment is several chunks: the first and the last key head against float64."""
+    q, k, v, g, do, s0, df = (t.cpu() for t in case(B, Hk, H, T, dk, dv, dtype, 31))
+    got = both(*(t.cuda() for t in (q, k, v, g, do, s0, df)))
+    torch.cuda.synchronize()
+    r = H // Hk
+    for b, j in ((0, 0), (B - 1, Hk - 1)):
+        x = {n: t[b, j:j + 1] if n in ("dq", "dk") else t[b, j * r:(j + 1) * r] for n, t in got.items()}
+        U.check_sequence(x, "%d %d " % (b, j), r, r, lambda h: U.one(
+            q[b, j], k[b, j], v[b, j * r + h], g[b, j * r + h], 0.1, dtype, g.dtype, s0[b, j * r + h], do[b, j * r + h], df[b, j * r + h]),
+            dtype, g.dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_packed_segments_of_several_chunks(dtype):
+    """Documents of one row to many segments in a stream that fills the card."""
+    H, d, lens = 32, 64, [1, 700, 64, 2049, 0, 385, 1500, 3]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T, N = cu[-1], len(lens)
+    q, k, v, g = U.inputs(0, H, H, T, d, d, dtype, 33, packed=True)
+    do = U.inputs(0, H, H, T, d, d, dtype, 34, packed=True)[2]
+    gen = torch.Generator().manual_seed(35)
+    s0, df = (torch.randn(N, H, d, d, generator=gen) for _ in range(2))
+    x = [t.cuda() for t in (q, k, v, g)]
+    c = torch.tensor(cu, dtype=torch.int32).cuda()
+    out, fs = kda.lin_chunk_fwd_varlen(*x, c, scale=0.1, initial_state=s0.cuda(), return_final_state=True)
+    grads = kda.lin_chunk_bwd_varlen(*x, do.cuda(), c, scale=0.1, initial_state=s0.cuda(), dfinal_state=df.cuda())
+    torch.cuda.synchronize()
+    for i in range(N):
+        s = slice(cu[i], cu[i + 1])
+        for h0 in (0, H - 1):
+            got = {"out": out[h0:h0 + 1, s], "final_state": fs[i, h0:h0 + 1], "dinitial_state": grads["dinitial_state"][i, h0:h0 + 1],
+                   **{n: grads[n][h0:h0 + 1, s] for n in ("dq", "dk", "dv", "dg")}}
+            U.check_sequence(got, "%d %d " % (i, h0), 1, 1, lambda h: U.one(q[h0, s], k[h0, s], v[h0, s], g[h0, s], 0.1, dtype, dtype,
+                                                                             s0[i, h0], do[h0, s], df[i, h0]), dtype, dtype)
