@@ -36,7 +36,8 @@ static hipError_t fwd_t(const LinLaunch &p) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return lin_walk<DK, DV, F32, false, false, true, false, false>(a, grid, p.stream);
+    if constexpr (F32) return lin_walk32<DK, DV, false, false, true, false>(a, grid, p.stream);
+    else return lin_walks<LinWalk<DK, DV, false, false, true, false, false>>(grid, p.stream, a);
 }
 
 template <bool F32>

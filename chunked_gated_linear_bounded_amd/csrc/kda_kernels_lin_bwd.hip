@@ -68,8 +68,14 @@ static hipError_t bwd_t(const LinLaunch &p) {
     s1.into = p.scale;
     s1.seg = f(m.seg[1]);
     s1.seg_decay = f(m.decay[1]);
-    if (many || want_last) KDA_WALK((lin_own_states<DK, DV, F32, false>(p, s0)));
-    if (many) KDA_WALK((lin_own_states<DK, DV, F32, true>(p, s1)));
+    if (many && !F32) {
+        if constexpr (!F32)
+            KDA_WALK((lin_walks<LinOwnStates<DK, false>, LinOwnStates<DK, true>>(lin_walk_grid(p, DV / 64), p.stream, lin_in_parts<DV>(s0),
+                                                                               lin_in_parts<DV>(s1))));
+    } else {
+        if (many || want_last) KDA_WALK((lin_own_states<DK, DV, F32, false>(p, s0)));
+        if (many) KDA_WALK((lin_own_states<DK, DV, F32, true>(p, s1)));
+    }
     if (many || want_last) {
         LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {}};
         s.side[0] = {p.init_state, f(m.seg[0]), want_last ? f(m.last) : nullptr, f(m.decay[0]), want_last};
@@ -77,39 +83,44 @@ static hipError_t bwd_t(const LinLaunch &p) {
         KDA_LAUNCH(lin_scan_kernel, dim3((unsigned)p.N * p.H * (DK * DV / 1024), 2), block, 0, p.stream, s);
     }
     // dq: forwards, with the transposed state
-    LinWalkArgs w = a;
-    w.a = p.dout; w.sa = sdo;
-    w.b = p.v; w.sb = sv;
-    w.c = p.k; w.sc = sk; w.rc = r;
-    w.y = p.q; w.sy = sq; w.ry = r;
-    w.inter = p.scale;
-    w.init = p.init_state;
-    w.seg = f(m.seg[0]);
-    w.dots = f(m.dots[0]);
-    w.out = SUM ? f(m.parts[0]) : p.dq;
-    KDA_WALK((lin_walk<DV, DK, F32, false, true, true, DOT, SUM>(w, grid, p.stream)));
+    LinWalkArgs wq = a, wk = a, wv = a;
+    wq.a = p.dout; wq.sa = sdo;
+    wq.b = p.v; wq.sb = sv;
+    wq.c = p.k; wq.sc = sk; wq.rc = r;
+    wq.y = p.q; wq.sy = sq; wq.ry = r;
+    wq.inter = p.scale;
+    wq.init = p.init_state;
+    wq.seg = f(m.seg[0]);
+    wq.dots = f(m.dots[0]);
+    wq.out = SUM ? f(m.parts[0]) : p.dq;
     // dk and dv: backwards in time
-    w = a;
-    w.a = p.v; w.sa = sv;
-    w.b = p.dout; w.sb = sdo;
-    w.c = p.q; w.sc = sq; w.rc = r;
-    w.y = p.k; w.sy = sk; w.ry = r;
-    w.into = p.scale;
-    w.init = p.dfinal;
-    w.seg = f(m.seg[1]);
-    w.dots = f(m.dots[1]);
-    w.out = SUM ? f(m.parts[1]) : p.dk_;
-    KDA_WALK((lin_walk<DV, DK, F32, true, true, true, DOT, SUM>(w, grid, p.stream)));
-    w = a;
-    w.a = p.k; w.sa = sk; w.ra = r;
-    w.b = p.q; w.sb = sq; w.rb = r;
-    w.c = p.dout; w.sc = sdo;
-    w.into = p.scale;
-    w.init = p.dfinal;
-    w.final_state = p.dinit;
-    w.seg = f(m.seg[1]);
-    w.out = p.dv_;
-    KDA_WALK((lin_walk<DK, DV, F32, true, false, true, false, false>(w, grid, p.stream)));
+    wk.a = p.v; wk.sa = sv;
+    wk.b = p.dout; wk.sb = sdo;
+    wk.c = p.q; wk.sc = sq; wk.rc = r;
+    wk.y = p.k; wk.sy = sk; wk.ry = r;
+    wk.into = p.scale;
+    wk.init = p.dfinal;
+    wk.seg = f(m.seg[1]);
+    wk.dots = f(m.dots[1]);
+    wk.out = SUM ? f(m.parts[1]) : p.dk_;
+    wv.a = p.k; wv.sa = sk; wv.ra = r;
+    wv.b = p.q; wv.sb = sq; wv.rb = r;
+    wv.c = p.dout; wv.sc = sdo;
+    wv.into = p.scale;
+    wv.init = p.dfinal;
+    wv.final_state = p.dinit;
+    wv.seg = f(m.seg[1]);
+    wv.out = p.dv_;
+    if constexpr (F32) {
+        KDA_WALK((lin_walk32<DV, DK, false, true, true, DOT>(wq, grid, p.stream)));
+        KDA_WALK((lin_walk32<DV, DK, true, true, true, DOT>(wk, grid, p.stream)));
+        KDA_WALK((lin_walk32<DK, DV, true, false, true, false>(wv, grid, p.stream)));
+    } else {
+        using Q = LinWalk<DV, DK, false, true, true, DOT, SUM>;
+        using K = LinWalk<DV, DK, true, true, true, DOT, SUM>;
+        using V = LinWalk<DK, DV, true, false, true, false, false>;
+        KDA_WALK((lin_walks<Q, K, V>(grid, p.stream, wq, wk, wv)));
+    }
     if (p.T == 0) return hipSuccess;
     if (DOT) {
         LinDecayGradArgs d{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,

@@ -27,25 +27,32 @@ inline unsigned lin_walk_grid(const LinLaunch &p, int parts = 1) {
     return (unsigned)(((long long)p.B * p.H * lin_slots(p) * parts + 7) / 8 * 8);
 }
 
-// Either walk: bf16 with helpers beside the walkers, float32 (whose tiles fill the LDS once) in one group.
-template <int DA, int DC, bool F32, bool REV, bool TR, bool OUT, bool DOT, bool OUTF>
-inline hipError_t lin_walk(const LinWalkArgs &a, unsigned grid, hipStream_t stream) {
-    if constexpr (F32) hipLaunchKernelGGL((lin_walk32_kernel<DA, DC, REV, TR, OUT, DOT>), dim3(grid), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((lin_pair_kernel<DA, DC, REV, TR, OUT, DOT, OUTF>), dim3(grid), dim3(512), 0, stream, a);
+template <typename... W, typename... A>
+inline hipError_t lin_walks(unsigned grid, hipStream_t stream, const A &...a) {
+    static_assert(sizeof...(W) == sizeof...(A), "a walk's arguments each");
+    hipLaunchKernelGGL((lin_pair_kernel<W...>), dim3(grid, sizeof...(W)), dim3(512), 0, stream, LinWalkList<sizeof...(W)>{{a...}});
+    return hipGetLastError();
+}
+// float32's walks, one a launch
+template <int DA, int DC, bool REV, bool TR, bool OUT, bool DOT>
+inline hipError_t lin_walk32(const LinWalkArgs &a, unsigned grid, hipStream_t stream) {
+    hipLaunchKernelGGL((lin_walk32_kernel<DA, DC, REV, TR, OUT, DOT>), dim3(grid), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
 // Pass 1, the segments' own states.  In bf16 work-groups of 64 of c's channels: they read b twice, from the
-// second's neighbour's L2, but two of them share a CU (64k x 32 heads 797 us a call against 808, the training step of 2 x 4096 x 16 heads 314
-// against 319).
+// second's neighbour's L2, but two of them share a CU (64k x 32 heads 797 us a call against 808, the training step
+// of 2 x 4096 x 16 heads 314 against 319).
+template <int DA, bool REV> using LinOwnStates = LinWalk<DA, 64, REV, false, false, false, false>;
+template <int DC>
+inline LinWalkArgs lin_in_parts(LinWalkArgs a) {
+    a.parts = DC / 64;
+    return a;
+}
 template <int DA, int DC, bool F32, bool REV>
-inline hipError_t lin_own_states(const LinLaunch &p, LinWalkArgs a) {
-    if constexpr (F32) {
-        return lin_walk<DA, DC, true, REV, false, false, false, false>(a, lin_walk_grid(p), p.stream);
-    } else {
-        a.parts = DC / 64;
-        return lin_walk<DA, 64, false, REV, false, false, false, false>(a, lin_walk_grid(p, a.parts), p.stream);
-    }
+inline hipError_t lin_own_states(const LinLaunch &p, const LinWalkArgs &a) {
+    if constexpr (F32) return lin_walk32<DA, DC, REV, false, false, false>(a, lin_walk_grid(p), p.stream);
+    else return lin_walks<LinOwnStates<DA, REV>>(lin_walk_grid(p, DC / 64), p.stream, lin_in_parts<DC>(a));
 }
 
 }  // namespace kda

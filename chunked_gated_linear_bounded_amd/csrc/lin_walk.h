@@ -82,21 +82,25 @@ template <typename E> struct LinUnit {
 //
 // OUT: pass 2, the outputs; else pass 1, the segment's own contribution to the state.  TR: states in memory
 // have b's channels as rows, else c's.
+template <int DA, int DC, bool OUT, bool DOT> struct LinPairLds {
+    static constexpr int FB = LinOp<false>::FB;
+    static constexpr int TILE = (4 * (DA / 32) * (OUT ? 2 : 1) + 4 * (DC / 32)) * FB, MB = 6 * 2 * FB;  // of a chunk: rows, scores
+    static constexpr int BYTES = 2 * TILE + (OUT ? 2 * MB : 0);
+    // for eight chunks: prefix sums in two floats, weights of the outputs and of the sources, e^{G_last}; the
+    // scores of tokens with themselves, by parity; and the walkers' dot products
+    static constexpr int FLOATS = 8 * 320 + (DOT ? 2 * 64 + 4 * 64 : 0);
+};
 template <int DA, int DC, bool REV, bool TR, bool OUT, bool DOT, bool OUTF>
-__global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
+__device__ __forceinline__ void lin_pair(const LinWalkArgs &p, lds_u8 *sT, __attribute__((address_space(3))) float *sG) {
     using Op = LinOp<false>;
     using E = __bf16;
     using V8 = bf16x8;
-    constexpr int NA = DA / 32, NC = DC / 32, NDT = DA / 16, NCT = DC / 64, FB = Op::FB;
-    constexpr int TILE = (4 * NA * (OUT ? 2 : 1) + 4 * NC) * FB, MB = 6 * 2 * FB;
+    using Lds = LinPairLds<DA, DC, OUT, DOT>;
+    constexpr int NA = DA / 32, NC = DC / 32, NDT = DA / 16, NCT = DC / 64, FB = Op::FB, TILE = Lds::TILE, MB = Lds::MB;
     typedef __attribute__((address_space(3))) float lds_f;
     typedef __attribute__((address_space(3))) f32x4 lds_f4;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * TILE + (OUT ? 2 * MB : 0)];
-    // for eight chunks: prefix sums in two floats, weights of the outputs and of the sources, e^{G_last}; the
-    // scores of tokens with themselves, by parity; and the walkers' dot products
-    __shared__ __attribute__((aligned(16))) float sg[8 * 320 + (DOT ? 2 * 64 + 4 * 64 : 0)];
-    lds_u8 *sT = lds_base(smem), *sM = sT + 2 * TILE;
-    lds_f *sG = (lds_f *)lds_base(sg), *sD = sG + 8 * 320, *sDot = sD + 128;
+    lds_u8 *sM = sT + 2 * TILE;
+    lds_f *sD = sG + 8 * 320, *sDot = sD + 128;
     const int tid = threadIdx.x & 255, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool helper = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
@@ -481,6 +485,34 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkArgs p) {
                 *reinterpret_cast<f32x4 *>(s + 4) = y;
             }
         }
+}
+
+// One walk, or walks that do not depend on each other in one launch, where the next one's work-groups follow
+// on a CU as soon as the last one's are done (11 packed documents, 5003 tokens, training step: 102 -> 95 us).
+template <int DA, int DC, bool REV, bool TR, bool OUT, bool DOT, bool OUTF> struct LinWalk {
+    static constexpr int BYTES = LinPairLds<DA, DC, OUT, DOT>::BYTES, FLOATS = LinPairLds<DA, DC, OUT, DOT>::FLOATS;
+    __device__ __forceinline__ static void run(const LinWalkArgs &p, lds_u8 *sT, __attribute__((address_space(3))) float *sG) {
+        lin_pair<DA, DC, REV, TR, OUT, DOT, OUTF>(p, sT, sG);
+    }
+};
+template <int N> struct LinWalkList {
+    LinWalkArgs a[N];
+};
+template <typename... W>
+__global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkList<sizeof...(W)> list) {
+    constexpr int N = sizeof...(W);
+    constexpr int bytes[N] = {W::BYTES...}, floats[N] = {W::FLOATS...};
+    constexpr auto most = [](const int (&x)[N]) {
+        int m = 0;
+        for (int i = 0; i < N; ++i) m = x[i] > m ? x[i] : m;
+        return m;
+    };
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[most(bytes)];
+    __shared__ __attribute__((aligned(16))) float sg[most(floats)];
+    // (the list's entry by its number: by the walk, all walks' arguments would be read ahead and kept)
+    const LinWalkArgs &p = list.a[N > 1 ? blockIdx.y : 0];
+    int i = 0;
+    ((void)(i++ == (int)blockIdx.y && (W::run(p, lds_base(smem), (__attribute__((address_space(3))) float *)lds_base(sg)), true)), ...);
 }
 
 // float32: tiles fill the LDS once, so one group of four waves does everything in turn, on float32 MFMAs,
