@@ -122,20 +122,19 @@ static hipError_t bwd_t(const LinLaunch &p) {
         KDA_WALK((lin_walks<Q, K, V>(grid, p.stream, wq, wk, wv)));
     }
     if (p.T == 0) return hipSuccess;
-    if (DOT) {
-        LinDecayGradArgs d{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,
+    LinFinish<E> z{};
+    z.d = LinDecayGradArgs{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,
                            f(m.dots[0]), f(m.dots[1]), p.dg};
-        KDA_LAUNCH(lin_decay_grad_kernel, dim3((unsigned)m.units), block, 0, p.stream, d);
-    }
-    if (SUM) {
-        const long long n4 = (long long)p.T * DK / 4, all = n4 * p.B * p.Hk;
-        KDA_LAUNCH((lin_head_sum_kernel<E>), dim3((unsigned)((all + 255) / 256), 2), block, 0, p.stream,
-                   f(m.parts[0]), f(m.parts[1]), static_cast<E *>(p.dq), static_cast<E *>(p.dk_), r, n4, all);
-    }
-    if (p.packed) {
-        const LinUncovered<E> u{static_cast<E *>(p.dq), static_cast<E *>(p.dk_), static_cast<E *>(p.dv_), p.dg, a.seqs, p.Hk, p.H, DK, DV, p.g32};
-        KDA_LAUNCH((lin_uncovered_kernel<E>), dim3((unsigned)((p.T + 63) / 64), p.H), block, 0, p.stream, u);
-    }
+    z.part[0] = f(m.parts[0]);
+    z.part[1] = f(m.parts[1]);
+    z.dq = static_cast<E *>(p.dq); z.dk = static_cast<E *>(p.dk_); z.dv = static_cast<E *>(p.dv_);
+    z.r = r; z.Hk = p.Hk; z.H = p.H; z.DK = DK; z.DV = DV;
+    z.n4 = (long long)p.T * DK / 4;
+    z.all = z.n4 * p.B * p.Hk;
+    z.grads = DOT ? (unsigned)m.units : 0;
+    z.sums = SUM ? (unsigned)((z.all + 255) / 256) : 0;
+    const unsigned blocks = (unsigned)lin_finish_grid(p, DOT);
+    if (blocks > 0) KDA_LAUNCH((lin_finish_kernel<E>), dim3(blocks), block, 0, p.stream, z);
     return hipSuccess;
 }
 template <int DK, int DV, bool F32>

@@ -55,13 +55,19 @@ hipError_t launch_lin_fwd(const LinLaunch &p);
 hipError_t launch_lin_bwd(const LinLaunch &p);
 hipError_t launch_lin_decode(const LinLaunch &p);
 
+// Work-groups of the backward's last launch (lin_scan.h).
+inline long long lin_finish_grid(const LinLaunch &p, bool grads) {
+    const long long sums = p.H == p.Hk ? 0 : ((long long)p.B * p.Hk * p.T * p.dk / 4 + 255) / 256;
+    return (grads ? (long long)p.B * p.H * lin_slots(p) : 0) + sums + (p.packed ? ((long long)p.T + 63) / 64 * p.H : 0);
+}
+
 // Whether the launches of a call stay below 2^32 work-items in x, which is as far as a launch goes, and
 // their unit counts in 32 bits.
 inline bool lin_grids_fit(const LinLaunch &p) {
     const long long most = 4294967295LL, units = (long long)p.B * p.H * lin_slots(p) * (p.dv / 64);
     const long long states = (long long)p.N * p.H * (p.dk * p.dv / 1024);
     const long long rows = (long long)p.B * p.H * (((long long)p.T + 15) / 16);
-    return (units + 7) / 8 * 8 <= most / 512 && states <= most / 256 && rows <= most / 256;
+    return (units + 7) / 8 * 8 <= most / 512 && states <= most / 256 && rows <= most / 256 && lin_finish_grid(p, true) <= most / 256;
 }
 inline bool lin_decode_grid_fits(const LinLaunch &p) { return (long long)p.B * p.H * (p.dv / 16) * 256 <= 4294967295LL; }
 

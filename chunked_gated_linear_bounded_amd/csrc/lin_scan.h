@@ -1,8 +1,9 @@
 // Decayed linear attention between segments: the scan that turns segments' own contributions into
 // start states, and what the backward pass still does behind its walks (the log-decays' gradient, sums
 // over value heads, rows that no document covers).  All of it moves bytes and nothing else.  Training step of
-// 2 x 4096 x 8/16 heads of 128 x 128 (288 us): scans 2 x 8 us, 34 MB each read and written; the gradient of the
-// log-decays 11, of which the <R, S> are 34 MB; the sums over heads 32, 134 MB read and 34 written (5.2 TB/s).
+// 2 x 4096 x 8/16 heads of 128 x 128 (288 us): scans 2 x 8 us, 34 MB each read and written; all that is behind the
+// walks 35, 134 MB of partials and 34 of states read, 34 written (5.8 TB/s; as launches of their own the
+// sums over heads took 32 and the log-decays 11).
 #pragma once
 #include "lin_common.h"
 
@@ -68,11 +69,11 @@ struct LinDecayGradArgs {
 // dg_t = sum over the pairs (i, j) of tokens with i >= t > j of their part of the loss.  Inside a segment
 // that is the sum over u >= t of row_u - col_u, plus the pairs that reach over the segment's end, <R, S>
 // there.
-static __global__ __launch_bounds__(256) void lin_decay_grad_kernel(const LinDecayGradArgs p) {
+static __device__ __forceinline__ void lin_decay_grad(const LinDecayGradArgs &p, unsigned block) {
     __shared__ double part[4];
     __shared__ double tail[4];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int slot = blockIdx.x % p.nslot, h = blockIdx.x / p.nslot % p.H, b = blockIdx.x / p.nslot / p.H;
+    const int slot = block % p.nslot, h = block / p.nslot % p.H, b = block / p.nslot / p.H;
     int seq, piece;
     if (!p.seqs.find(b, slot, seq, piece)) return;
     const int len = p.seqs.length(seq), rows = min(p.seqs.seg, len - piece * p.seqs.seg);
@@ -113,47 +114,67 @@ static __global__ __launch_bounds__(256) void lin_decay_grad_kernel(const LinDec
     }
 }
 
-// Sums over the r value heads of a key head of their float32 partials, of dq (y = 0) and dk: four
-// elements a thread, n4 = T dk / 4 of a head, `all` of them.
-template <typename E>
-__global__ __launch_bounds__(256) void lin_head_sum_kernel(const float *part0, const float *part1, E *out0, E *out1, int r, long long n4,
-                                                           long long all) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= all) return;
-    const f32x4 *x = reinterpret_cast<const f32x4 *>(blockIdx.y ? part1 : part0) + (i / n4 * r) * n4 + i % n4;
-    f32x4 s = x[0];
-    for (int k = 1; k < r; ++k) s += x[k * n4];
-    st_tile((blockIdx.y ? out1 : out0) + 4 * i, 0, s);
-}
-
-// Gradients of the rows of a packed stream that no document covers, [0, cu[0]) and [cu[N], T): zeros.
-template <typename E> struct LinUncovered {
+// What the backward pass does behind its walks, in one launch of `grads` work-groups for the log-decays'
+// gradient, `sums` for the sums over the r value heads of a key head of their float32 partials of dq and dk
+// (four elements of both a thread, n4 = T dk / 4 of a head, `all` of them; r = 1: none), and the rest for the rows
+// of a packed stream that no document covers, [0, cu[0]) and [cu[N], T): zeros.
+template <typename E> struct LinFinish {
+    LinDecayGradArgs d;
+    unsigned grads, sums;
+    const float *part[2];
     E *dq, *dk, *dv;
-    void *dg;
-    LinSeqs seqs;
-    int Hk, H, DK, DV;
-    bool g32;
+    int r, Hk, H, DK, DV;
+    long long n4, all;
 };
 template <typename E>
-__global__ __launch_bounds__(256) void lin_uncovered_kernel(const LinUncovered<E> p) {
-    const int from = p.seqs.clip(p.seqs.cu[0]), to = max(from, p.seqs.clip(p.seqs.cu[p.seqs.N])), h = blockIdx.y;
-    const int t0 = blockIdx.x * 64, t1 = min(t0 + 64, p.seqs.T);
+__global__ __launch_bounds__(256) void lin_finish_kernel(const LinFinish<E> p) {
+    unsigned block = blockIdx.x;
+    if (block < p.grads) {
+        lin_decay_grad(p.d, block);
+        return;
+    }
+    block -= p.grads;
+    const LinSeqs &seqs = p.d.seqs;
+    int from = 0, to = seqs.T;  // the rows that documents cover
+    if (seqs.cu) {
+        from = seqs.clip(seqs.cu[0]);
+        to = max(from, seqs.clip(seqs.cu[seqs.N]));
+    }
+    if (block < p.sums) {
+        const long long i = (long long)block * 256 + threadIdx.x;
+        if (i >= p.all) return;
+        const int t = (int)(i % p.n4 / (p.DK / 4));
+        const long long at = (i / p.n4 * p.r) * p.n4 + i % p.n4;
+        const f32x4 *x = reinterpret_cast<const f32x4 *>(p.part[0]) + at, *y = reinterpret_cast<const f32x4 *>(p.part[1]) + at;
+        f32x4 u = x[0], v = y[0];
+        for (int k = 1; k < p.r; ++k) {
+            u += x[k * p.n4];
+            v += y[k * p.n4];
+        }
+        const bool none = t < from || t >= to;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        st_tile(p.dq + 4 * i, 0, none ? zero : u);
+        st_tile(p.dk + 4 * i, 0, none ? zero : v);
+        return;
+    }
+    block -= p.sums;
+    const int nx = (seqs.T + 63) / 64, h = block / nx, t0 = block % nx * 64, t1 = min(t0 + 64, seqs.T);
     if (t0 >= from && t1 <= to) return;
     auto clear = [&](E *x, int d) {
         for (int i = threadIdx.x; i < (t1 - t0) * d; i += 256) {
             const int t = t0 + i / d;
-            if (t < from || t >= to) x[((size_t)h * p.seqs.T + t0) * d + i] = (E)0.f;
+            if (t < from || t >= to) x[((size_t)h * seqs.T + t0) * d + i] = (E)0.f;
         }
     };
-    if (h < p.Hk) {
+    if (p.sums == 0) {  // (else with the sums)
         clear(p.dq, p.DK);
         clear(p.dk, p.DK);
     }
     clear(p.dv, p.DV);
     const int t = t0 + threadIdx.x;
-    if (p.dg && t < t1 && (t < from || t >= to)) {
-        if (p.g32) static_cast<float *>(p.dg)[(size_t)h * p.seqs.T + t] = 0.f;
-        else static_cast<__bf16 *>(p.dg)[(size_t)h * p.seqs.T + t] = (__bf16)0.f;
+    if (p.d.dg && t < t1 && (t < from || t >= to)) {
+        if (p.d.g32) static_cast<float *>(p.d.dg)[(size_t)h * seqs.T + t] = 0.f;
+        else static_cast<__bf16 *>(p.d.dg)[(size_t)h * seqs.T + t] = (__bf16)0.f;
     }
 }
 
