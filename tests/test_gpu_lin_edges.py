@@ -261,3 +261,40 @@ def test_packed_segments_of_several_chunks(dtype):
                    **{n: grads[n][h0:h0 + 1, s] for n in ("dq", "dk", "dv", "dg")}}
             U.check_sequence(got, "%d %d " % (i, h0), 1, 1, lambda h: U.one(q[h0, s], k[h0, s], v[h0, s], g[h0, s], 0.1, dtype, dtype,
                                                                              s0[i, h0], do[h0, s], df[i, h0]), dtype, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_no_tokens(dtype):
+    """A batch of none, a stream of none and a stream of empty documents: end states are the start states."""
+    H, d = 2, 64
+    q = torch.zeros(3, H, 0, d, dtype=dtype, device="cuda")
+    s0 = torch.randn(3, H, d, d, device="cuda")
+    out, fs = kda.lin_chunk_fwd(q, q, q, q[..., 0], initial_state=s0, return_final_state=True)
+    assert out.shape == q.shape and torch.equal(fs, s0)
+    out, fs = kda.lin_chunk_fwd(q, q, q, q[..., 0], return_final_state=True)
+    assert bool((fs == 0).all())
+    c = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out, fs = kda.lin_chunk_fwd_varlen(q[0], q[0], q[0], q[0, ..., 0], c, initial_state=s0, return_final_state=True)
+    assert out.shape == q[0].shape and torch.equal(fs, s0)
+    x, g = torch.randn(H, 90, d, device="cuda").to(dtype), torch.zeros(H, 90, device="cuda")
+    out, fs = kda.lin_chunk_fwd_varlen(x, x, x, g, c, out=torch.full_like(x, 7), initial_state=s0, return_final_state=True)
+    grads = kda.lin_chunk_bwd_varlen(x, x, x, g, x, c, initial_state=s0, dfinal_state=s0)
+    torch.cuda.synchronize()
+    assert bool((out == 7).all()) and torch.equal(fs, s0) and torch.equal(grads["dinitial_state"], s0)
+    assert all(bool((grads[n] == 0).all()) for n in ("dq", "dk", "dv", "dg"))
+
+
+def test_boundaries_out_of_order():
+    """Boundaries below zero, behind the stream and going back: no access outside, and documents that stand by
+    themselves get what they get alone."""
+    H, T, d = 2, 200, 64
+    q, k, v, g, do, *_ = (t[0] if t.dim() == 4 or t.dim() == 3 else t for t in case(1, H, H, T, d, d, BF, 41))
+    c = torch.tensor([-50, 70, 30, 30, 10 ** 6], dtype=torch.int32, device="cuda")
+    out, fs = kda.lin_chunk_fwd_varlen(q, k, v, g, c, scale=0.1, return_final_state=True)
+    kda.lin_chunk_bwd_varlen(q, k, v, g, do, c, scale=0.1)
+    torch.cuda.synchronize()
+    assert torch.isfinite(fs).all()
+    c = torch.tensor([-50, 70, 10 ** 6], dtype=torch.int32, device="cuda")
+    out, fs = kda.lin_chunk_fwd_varlen(q, k, v, g, c, scale=0.1, return_final_state=True)
+    want = kda.lin_chunk_fwd_varlen(q, k, v, g, torch.tensor([0, 70, T], dtype=torch.int32, device="cuda"), scale=0.1, return_final_state=True)
+    assert torch.equal(out, want[0]) and torch.equal(fs, want[1])
