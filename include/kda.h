@@ -491,7 +491,9 @@ int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k
 /* Gradients of sum(dout * out) + sum(dfinal_state * final_state), from the inputs alone.  dq, dk_out :
  * [B][Hk][T][dk] (summed over the value heads of a key head), dv_out : [B][H][T][dv] in io_dtype, dg :
  * [B][H][T] in g_dtype or NULL (not wanted), dinitial_state : [N][H][dv][dk] float32 or NULL; all
- * contiguous.  The gradients of tokens that no document covers are written as zeros.  No float atomics.
+ * contiguous; none of them, dinitial_state neither, in the place of anything that is read (final_state of the
+ * forward may be its initial_state).  The gradients of tokens that no document covers are written as zeros.
+ * No float atomics.
  * dg is what is left of a segment's sums of larger terms: where decays are strong its floor is these sums'
  * rounding. */
 int kda_lin_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
