@@ -140,15 +140,21 @@ def lin_chunk_bwd_varlen(q, k, v, g, dout, cu_seqlens, scale=1.0, initial_state=
 class LinChunkFunction(torch.autograd.Function):
     """out, final_state = LinChunkFunction.apply(q, k, v, g, scale, initial_state, cu_seqlens): the chunked
     forward with its backward, for a batch or (cu_seqlens given) for packed documents.  Once
-    differentiable: a gradient of the gradients is an error.  So is a capture into a graph with leaves among
-    the inputs: a leaf gathers its gradient on the stream it was first used on, and where an eager graph of it
-    lives that is not the captured one, which ends the process.  lin_chunk_fwd and lin_chunk_bwd may be captured."""
+    differentiable: a gradient of the gradients is an error.  So is, with gradients enabled, a capture into a
+    graph with leaves among the inputs: a leaf gathers its gradient on the stream it was first used on, and
+    where an eager graph of it lives that is not the captured one, which ends the process.  lin_chunk_fwd and
+    lin_chunk_bwd may be captured, and under no_grad this function."""
+
+    @classmethod
+    def apply(cls, *args):
+        # (here, because forward itself runs with gradients disabled)
+        if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad and t.is_leaf for t in args) and \
+                torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a leaf's gradient cannot be captured here: capture lin_chunk_fwd and lin_chunk_bwd")
+        return super().apply(*args)
 
     @staticmethod
     def forward(ctx, q, k, v, g, scale=1.0, initial_state=None, cu_seqlens=None):
-        if any(isinstance(t, torch.Tensor) and t.requires_grad and t.is_leaf for t in (q, k, v, g, initial_state)) and \
-                torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("a leaf's gradient cannot be captured here: capture lin_chunk_fwd and lin_chunk_bwd")
         out, fs = _fwd(q, k, v, g, cu_seqlens, scale, None, None, True, initial_state, None, None)
         ctx.save_for_backward(q, k, v, g, initial_state, cu_seqlens)
         ctx.scale = scale
