@@ -244,8 +244,9 @@ __device__ __forceinline__ void lin_pair(const LinWalkArgs &p, lds_u8 *sT, __att
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
     const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sunit * (DA * DC);
     float *to = !OUT ? p.seg + (u.sunit * p.parts + u.part) * (DA * DC) : u.alone && p.final_state ? p.final_state + u.nstate : nullptr;
-    // a state that is handed on keeps all 24 bits; one that only feeds outputs does with 16
-    const bool whole = to != nullptr;
+    // a state that can be handed on keeps all 24 bits, whether it is asked for or not, or the outputs made from
+    // it would depend on that; one that only feeds outputs does with 16
+    const bool whole = !OUT || (!TR && u.alone);
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll

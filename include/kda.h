@@ -478,8 +478,10 @@ int kda_latent_tree_step(const void *q, const void *cache, const int *block_tabl
  *    pieces of 16 tokens of a head (a part of it less where key heads are shared).
  *  - What is not finite in q reaches its token's outputs; in v its channel of the outputs from its chunk
  *    of 64 tokens on and of the state; in k or g its head's.
- * States that are handed on (final_state, dinitial_state, between segments) gather all 24 bits, also with
- * bf16 inputs; with bf16 inputs the state that only feeds a segment's outputs gathers 16. */
+ * States that can be handed on (final_state, dinitial_state, between segments) gather all 24 bits, also with
+ * bf16 inputs; with bf16 inputs the state that only feeds a segment's outputs gathers 16.
+ * The same inputs give the same bits.  What else is asked for does not change them, but for dq and dk with
+ * and without dg, which differ by the rounding of a token's term with itself. */
 size_t kda_lin_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
 
 int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,

@@ -38,3 +38,42 @@ def test_function_captured_without_gradients(dtype):
             want = kda.lin_chunk_fwd(*xs[k % 2], scale=0.1, initial_state=s0, return_final_state=True)
             torch.cuda.synchronize()
             assert torch.equal(out, want[0]) and torch.equal(fs, want[1]), k
+
+
+def case(B, Hk, H, T, d, dtype, seed, packed=False):
+    x = U.inputs(B, Hk, H, T, d, d, dtype, seed, packed=packed)
+    do = U.inputs(B, Hk, H, T, d, d, dtype, seed + 1, packed=packed)[2]
+    return [t.cuda() for t in (*x, do)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,Hk,H,T,d,lens", [
+    (2, 1, 2, 200, 64, None), (1, 2, 2, 256, 128, None),   # four chunks of a sequence that is one segment
+    (1, 1, 2, 700, 128, None),                              # eleven segments
+    (16, 16, 32, 450, 64, None),                            # a full card: all of a sequence in one segment again
+    (0, 1, 2, 240, 64, [70, 0, 130, 40]), (0, 32, 32, 3000, 64, [100, 64, 700, 1, 2135]),
+])
+def test_the_same_bits_whatever_is_asked_for(B, Hk, H, T, d, lens, dtype):
+    """out with and without the end state; every gradient with and without dinitial_state, and with the end
+    state's gradient left out or zeros; dv and dinitial_state with and without dg."""
+    q, k, v, g, do = case(B, Hk, H, T, d, dtype, 81, packed=lens is not None)
+    N = B if lens is None else len(lens)
+    if lens is None:
+        more, fwd, bwd = (), kda.lin_chunk_fwd, kda.lin_chunk_bwd
+    else:
+        more, fwd, bwd = (torch.tensor([0, *lens], dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda(),), kda.lin_chunk_fwd_varlen, kda.lin_chunk_bwd_varlen
+    s0 = torch.randn(N, H, d, d, device="cuda")
+    for init in (None, s0):
+        a = fwd(q, k, v, g, *more, scale=0.1, initial_state=init)
+        b, _ = fwd(q, k, v, g, *more, scale=0.1, initial_state=init, return_final_state=True)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b), "out"
+        back = lambda **kw: bwd(q, k, v, g, do, *more, scale=0.1, initial_state=init, **kw)
+        want = back()
+        for kw in (dict(want_dinitial=False), dict(dfinal_state=torch.zeros_like(s0)), dict(want_dg=False),
+                   dict(dfinal_state=torch.zeros_like(s0), want_dinitial=False)):
+            got = back(**kw)
+            torch.cuda.synchronize()
+            for n, t in got.items():
+                if t is not None and not (n in ("dq", "dk") and "want_dg" in kw):
+                    assert torch.equal(t, want[n]), (n, kw.keys())
