@@ -82,7 +82,7 @@ extern "C" {
 size_t kda_lin_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype) {
     if (check_shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype) != KDA_OK) return 0;
     const kda::LinLaunch p = shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype);
-    return backward ? kda::lin_bwd_bytes(p) : kda::lin_fwd_bytes(p);
+    return backward ? kda::lin_bwd_bytes(p, backward != 2) : kda::lin_fwd_bytes(p);
 }
 
 int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
@@ -121,7 +121,7 @@ int kda_lin_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k
         !set_strides(p.sdo, dout_strides, p.B, H, T, dv, p.fp32 ? 4 : 8))
         return KDA_ERR_ALIGN;
     st = inputs(p, q, q_strides, k, k_strides, v, v_strides, g, g_strides, g_dtype, cu_seqlens, scale, initial_state, workspace,
-                workspace_bytes, kda::lin_bwd_bytes(p));
+                workspace_bytes, kda::lin_bwd_bytes(p, dg && dfinal_state));
     if (st != KDA_OK) return st;
     if (far_rows(p, p.sdo)) return KDA_ERR_SHAPE;
     if (T == 0 && !dinitial_state) return KDA_OK;

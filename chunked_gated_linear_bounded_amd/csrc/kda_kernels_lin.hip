@@ -10,7 +10,7 @@ namespace kda {
 size_t lin_fwd_bytes(const LinLaunch &p) {
     if (p.T <= lin_segment(p)) return 0;  // every sequence is one segment
     const size_t units = (size_t)p.B * p.H * lin_slots(p);
-    return units * p.dk * p.dv * 4 + (units * 4 + 15) / 16 * 16;
+    return lin_all_states(p) * p.dk * p.dv * 4 + (units * 4 + 15) / 16 * 16;
 }
 
 template <int DK, int DV, bool F32>
@@ -26,12 +26,11 @@ static hipError_t fwd_t(const LinLaunch &p) {
     a.out = p.out;
     const unsigned grid = lin_walk_grid(p);
     if (p.T > a.seqs.seg) {
-        const size_t units = (size_t)p.B * p.H * a.nslot;
         a.seg = reinterpret_cast<float *>(p.workspace);
-        a.seg_decay = a.seg + units * DK * DV;
+        a.seg_decay = a.seg + lin_all_states(p) * DK * DV;
         hipError_t e = lin_own_states<DK, DV, F32, false>(p, a);
         if (e != hipSuccess) return e;
-        LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {{p.init_state, a.seg, p.final_state, a.seg_decay, false}, {}}};
+        LinScanArgs s{a.seqs, p.B, p.H, a.nslot, a.nstate, DK * DV / 4, {{p.init_state, a.seg, p.final_state, a.seg_decay, false}, {}}};
         hipLaunchKernelGGL(lin_scan_kernel, dim3((unsigned)p.N * p.H * (DK * DV / 1024)), dim3(256), 0, p.stream, s);
         e = hipGetLastError();
         if (e != hipSuccess) return e;

@@ -5,15 +5,16 @@
 
 namespace kda {
 
-// Workspace: start states of the segments, forwards and backwards, and their decays; the sequences' end
-// states; the two dot products a token that the decays' gradient is made of; and, where key heads are
-// shared, the value heads' float32 partials of dq and dk.
+// Workspace: start states of the segments, forwards and backwards, and their decays; the two dot products a
+// token that the decays' gradient is made of; where key heads are shared, the value heads' float32 partials
+// of dq and dk; and, where the decays' gradient needs them, the sequences' end states.
 struct LinBwdPlan {
-    size_t units, state, tokens, part;
+    size_t units, state, states, tokens, part;
     size_t seg[2], decay[2], last, dots[2], parts[2], bytes;
-    explicit LinBwdPlan(const LinLaunch &p) {
+    LinBwdPlan(const LinLaunch &p, bool end_states) {
         units = (size_t)p.B * p.H * lin_slots(p);
         state = (size_t)p.dk * p.dv;
+        states = lin_all_states(p);
         tokens = (size_t)p.B * p.H * p.T;
         part = p.H == p.Hk ? 0 : tokens * p.dk;
         size_t at = 0;
@@ -23,16 +24,16 @@ struct LinBwdPlan {
             return here;
         };
         for (int i = 0; i < 2; ++i) {
-            seg[i] = take(units * state);
+            seg[i] = take(states * state);
             decay[i] = take(units);
             dots[i] = take(tokens);
             parts[i] = take(part);
         }
-        last = take((size_t)p.N * p.H * state);
+        last = take(end_states ? (size_t)p.N * p.H * state : 0);
         bytes = at;
     }
 };
-size_t lin_bwd_bytes(const LinLaunch &p) { return LinBwdPlan(p).bytes; }
+size_t lin_bwd_bytes(const LinLaunch &p, bool end_states) { return LinBwdPlan(p, end_states).bytes; }
 
 #define KDA_LAUNCH(...)                             \
     do {                                            \
@@ -50,12 +51,12 @@ size_t lin_bwd_bytes(const LinLaunch &p) { return LinBwdPlan(p).bytes; }
 template <int DK, int DV, bool F32, bool DOT, bool SUM>
 static hipError_t bwd_t(const LinLaunch &p) {
     using E = typename std::conditional<F32, float, __bf16>::type;
-    const LinBwdPlan m(p);
+    const bool want_last = DOT && p.dfinal != nullptr, many = p.T > lin_segment(p);
+    const LinBwdPlan m(p, want_last);
     auto f = [&](size_t at) { return reinterpret_cast<float *>(p.workspace + at); };
     const int r = p.H / p.Hk;
     const Strides3 sq = lin_st3(p.sq), sk = lin_st3(p.sk), sv = lin_st3(p.sv), sdo = lin_st3(p.sdo);
     const unsigned grid = lin_walk_grid(p);
-    const bool want_last = DOT && p.dfinal != nullptr, many = p.T > lin_segment(p);
     LinWalkArgs a = lin_walk_args(p);
     const dim3 block(256);
     // each segment's own part of the state, and of the gradient by it
@@ -64,6 +65,7 @@ static hipError_t bwd_t(const LinLaunch &p) {
     s0.seg = f(m.seg[0]);
     s0.seg_decay = f(m.decay[0]);
     s0.all = want_last;
+    s0.final_state = f(m.last);
     s1.b = p.q; s1.sb = sq; s1.rb = r; s1.c = p.dout; s1.sc = sdo;
     s1.into = p.scale;
     s1.seg = f(m.seg[1]);
@@ -77,7 +79,7 @@ static hipError_t bwd_t(const LinLaunch &p) {
         if (many) KDA_WALK((lin_own_states<DK, DV, F32, true>(p, s1)));
     }
     if (many || want_last) {
-        LinScanArgs s{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, {}};
+        LinScanArgs s{a.seqs, p.B, p.H, a.nslot, a.nstate, DK * DV / 4, {}};
         s.side[0] = {p.init_state, f(m.seg[0]), want_last ? f(m.last) : nullptr, f(m.decay[0]), want_last};
         s.side[1] = {p.dfinal, many ? f(m.seg[1]) : nullptr, p.dinit, f(m.decay[1]), false};
         KDA_LAUNCH(lin_scan_kernel, dim3((unsigned)p.N * p.H * (DK * DV / 1024), 2), block, 0, p.stream, s);
@@ -123,7 +125,7 @@ static hipError_t bwd_t(const LinLaunch &p) {
     }
     if (p.T == 0) return hipSuccess;
     LinFinish<E> z{};
-    z.d = LinDecayGradArgs{a.seqs, p.B, p.H, a.nslot, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,
+    z.d = LinDecayGradArgs{a.seqs, p.B, p.H, a.nslot, a.nstate, DK * DV / 4, p.g32, f(m.seg[0]), f(m.seg[1]), f(m.last), p.dfinal,
                            f(m.dots[0]), f(m.dots[1]), p.dg};
     z.part[0] = f(m.parts[0]);
     z.part[1] = f(m.parts[1]);

@@ -48,8 +48,16 @@ inline long long lin_slots(const LinLaunch &p) {
     const long long seg = lin_segment(p), n = p.packed ? p.T / seg + p.N : (p.T + seg - 1) / seg;
     return n < 1 ? 1 : n;
 }
+// Segment states of one batch entry and head.  Only sequences longer than a segment have any, so that a packed
+// stream needs no more of them the more short documents are in it; of the two ways to place them
+// (LinSeqs::state0) the one that takes less.
+inline bool lin_sparse(const LinLaunch &p) { return p.packed && p.N > p.T / lin_segment(p) + 1; }
+inline long long lin_states(const LinLaunch &p) { return lin_sparse(p) ? 2 * (long long)(p.T / lin_segment(p)) + 1 : lin_slots(p); }
+// all of them (one at least)
+inline size_t lin_all_states(const LinLaunch &p) { return p.T <= lin_segment(p) ? 1 : (size_t)p.B * p.H * lin_states(p); }
 size_t lin_fwd_bytes(const LinLaunch &p);
-size_t lin_bwd_bytes(const LinLaunch &p);
+// end_states: of a call with dfinal and dg
+size_t lin_bwd_bytes(const LinLaunch &p, bool end_states);
 
 hipError_t launch_lin_fwd(const LinLaunch &p);
 hipError_t launch_lin_bwd(const LinLaunch &p);

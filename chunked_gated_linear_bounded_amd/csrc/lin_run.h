@@ -14,10 +14,11 @@ inline LinWalkArgs lin_walk_args(const LinLaunch &p) {
     a.sg = lin_st3(p.sg);
     a.g32 = p.g32;
     a.ra = a.rb = a.rc = a.ry = 1;
-    a.seqs = LinSeqs{p.cu, p.N, p.T, lin_segment(p)};
+    a.seqs = LinSeqs{p.cu, p.N, p.T, lin_segment(p), lin_sparse(p)};
     a.B = p.B;
     a.H = p.H;
     a.nslot = (int)lin_slots(p);
+    a.nstate = (int)lin_states(p);
     a.scale = p.scale;
     a.inter = a.into = 1.f;
     a.parts = 1;

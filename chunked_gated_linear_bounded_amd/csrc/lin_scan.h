@@ -11,12 +11,12 @@ namespace kda {
 
 struct LinScanArgs {
     LinSeqs seqs;
-    int B, H, nslot, n4;         // n4: dk dv / 4
+    int B, H, nslot, nstate, n4; // n4: dk dv / 4
     struct Side {
         const float *init;       // [N][H] (NULL: zero)
-        float *seg, *last;       // [B][H][nslot] in place; [N][H] end states (NULL: not wanted)
+        float *seg, *last;       // [B][H][nstate] in place; [N][H] end states (NULL: not wanted)
         const float *decay;      // [B][H][nslot]
-        bool all;                // segments that are alone in their sequence take part as others do
+        bool all;                // last holds what segments that are alone in their sequence add to its state
     } side[2];                   // forwards; backwards in time
 };
 
@@ -30,12 +30,17 @@ static __global__ __launch_bounds__(256) void lin_scan_kernel(const LinScanArgs 
     if (a.seg == nullptr) return;
     const int len = p.seqs.length(seq);
     if (!a.all && len <= p.seqs.seg) return;
-    const int ns = max(1, p.seqs.segments(seq)), b = p.seqs.cu ? 0 : seq;
+    const int ns = p.seqs.segments(seq), b = p.seqs.cu ? 0 : seq;
     const size_t s0 = ((size_t)b * p.H + h) * p.nslot + p.seqs.slot0(seq);
-    f32x4 *st = reinterpret_cast<f32x4 *>(a.seg) + s0 * p.n4 + e;
     const size_t at = ((size_t)seq * p.H + h) * p.n4 + e;
     f32x4 carry = {0.f, 0.f, 0.f, 0.f};
     if (a.init) carry = reinterpret_cast<const f32x4 *>(a.init)[at];
+    if (len <= p.seqs.seg) {
+        f32x4 *last = reinterpret_cast<f32x4 *>(a.last) + at;
+        *last = carry * a.decay[s0] + *last;
+        return;
+    }
+    f32x4 *st = reinterpret_cast<f32x4 *>(a.seg) + (((size_t)b * p.H + h) * p.nstate + p.seqs.state0(seq)) * p.n4 + e;
     for (int s = 0; s < ns; s += 8) {
         f32x4 x[8];
         float d[8];
@@ -58,7 +63,7 @@ static __global__ __launch_bounds__(256) void lin_scan_kernel(const LinScanArgs 
 
 struct LinDecayGradArgs {
     LinSeqs seqs;
-    int B, H, nslot, n4;
+    int B, H, nslot, nstate, n4;
     bool g32;
     const float *fwd, *rev;      // start states of the segments, of either walk
     const float *last, *dfinal;  // [N][H]: end states, and the gradient by them (NULL: zero)
@@ -78,11 +83,11 @@ static __device__ __forceinline__ void lin_decay_grad(const LinDecayGradArgs &p,
     if (!p.seqs.find(b, slot, seq, piece)) return;
     const int len = p.seqs.length(seq), rows = min(p.seqs.seg, len - piece * p.seqs.seg);
     if (rows <= 0) return;
-    const size_t sunit = ((size_t)b * p.H + h) * p.nslot + slot, row0 = ((size_t)b * p.H + h) * p.seqs.T + p.seqs.start(seq) + piece * p.seqs.seg;
+    const size_t state = ((size_t)b * p.H + h) * p.nstate + p.seqs.state0(seq) + piece, row0 = ((size_t)b * p.H + h) * p.seqs.T + p.seqs.start(seq) + piece * p.seqs.seg;
     const bool end = (piece + 1) * (long long)p.seqs.seg >= len;
     const size_t at = ((size_t)seq * p.H + h) * p.n4;
-    const f32x4 *R = end ? reinterpret_cast<const f32x4 *>(p.dfinal) + at : reinterpret_cast<const f32x4 *>(p.rev) + sunit * p.n4;
-    const f32x4 *S = end ? reinterpret_cast<const f32x4 *>(p.last) + at : reinterpret_cast<const f32x4 *>(p.fwd) + (sunit + 1) * p.n4;
+    const f32x4 *R = end ? reinterpret_cast<const f32x4 *>(p.dfinal) + at : reinterpret_cast<const f32x4 *>(p.rev) + state * p.n4;
+    const f32x4 *S = end ? reinterpret_cast<const f32x4 *>(p.last) + at : reinterpret_cast<const f32x4 *>(p.fwd) + (state + 1) * p.n4;
     double over = 0.0;
     if (!end || p.dfinal) {
         for (int e = tid; e < p.n4; e += 256) {

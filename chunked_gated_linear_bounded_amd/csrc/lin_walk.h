@@ -19,13 +19,13 @@ struct LinWalkArgs {
     Strides3 sa, sb, sc, sg, sy;
     int ra, rb, rc, ry;              // value heads that share a head of that tensor
     LinSeqs seqs;
-    int B, H, nslot;
+    int B, H, nslot, nstate;         // work slots and states of a batch entry's head
     int parts;                       // work-groups that share the columns of a segment's own state (pass 1)
-    bool g32, all;                   // all: segments that are alone in their sequence take part as others do
+    bool g32, all;                   // all (pass 1): also of segments that are alone in their sequence, into final_state
     float scale, inter, into;
     const float *init;               // [N][H] start states of the sequences (NULL: zero), for segments that are alone
     float *final_state;              // [N][H] end states, from segments that are alone (NULL: not wanted)
-    float *seg;                      // [B][H][nslot] states of the others: local sums (pass 1), start states (pass 2)
+    float *seg;                      // [B][H][nstate] states of the others: local sums (pass 1), start states (pass 2)
     float *seg_decay;                // [B][H][nslot], written by pass 1
     void *out;                       // [B][H][T][DC], in the inputs' type or (OUTF) float32
     float *dots;                     // [B][H][T]: y_i . (out_i without the term j = i)
@@ -37,7 +37,7 @@ template <typename E> struct LinUnit {
     bool alone;
     const E *ap, *bp, *cp;
     long long g0;
-    size_t row0, sunit, nstate;
+    size_t row0, sunit, sstate, nstate;  // places of its decay, of its state in seg, and (alone) of its sequence's
     // false: nothing there.  Units in eight runs, one an XCD: parts of a state and heads that share rows are
     // neighbours there.
     __device__ __forceinline__ bool find(const LinWalkArgs &p, int state, int parts = 1) {
@@ -52,7 +52,7 @@ template <typename E> struct LinUnit {
         if (!p.seqs.find(b, slot, seq, piece)) return false;
         const int len = p.seqs.length(seq);
         first = p.seqs.start(seq) + piece * p.seqs.seg;
-        alone = !p.all && len <= p.seqs.seg;
+        alone = len <= p.seqs.seg;
         rows = max(0, min(p.seqs.seg, len - piece * p.seqs.seg));
         nchunk = (rows + 63) / 64;
         ap = reinterpret_cast<const E *>(p.a) + b * p.sa.b + h / p.ra * p.sa.h + (long long)first * p.sa.t;
@@ -61,6 +61,7 @@ template <typename E> struct LinUnit {
         g0 = b * p.sg.b + h * p.sg.h + (long long)first * p.sg.t;
         row0 = ((size_t)b * p.H + h) * p.seqs.T + first;
         sunit = ((size_t)b * p.H + h) * p.nslot + slot;
+        sstate = ((size_t)b * p.H + h) * p.nstate + p.seqs.state0(seq) + piece;
         nstate = ((size_t)seq * p.H + h) * state;
         return true;
     }
@@ -105,7 +106,7 @@ __device__ __forceinline__ void lin_pair(const LinWalkArgs &p, lds_u8 *sT, __att
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool helper = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     LinUnit<E> u;
-    if (!u.find(p, DA * DC, OUT ? 1 : p.parts) || (!OUT && u.alone)) return;
+    if (!u.find(p, DA * DC, OUT ? 1 : p.parts) || (!OUT && u.alone && !p.all)) return;
     if (!OUT) u.cp += u.part * DC;
     const int nchunk = u.nchunk, rows = u.rows;
     auto chunk_of = [&](int ci) { return REV ? nchunk - 1 - ci : ci; };
@@ -242,8 +243,9 @@ __device__ __forceinline__ void lin_pair(const LinWalkArgs &p, lds_u8 *sT, __att
     };
     f32x4 P[NCT][NDT];
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sunit * (DA * DC);
-    float *to = !OUT ? p.seg + (u.sunit * p.parts + u.part) * (DA * DC) : u.alone && p.final_state ? p.final_state + u.nstate : nullptr;
+    const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sstate * (DA * DC);
+    float *to = !u.alone ? (OUT ? nullptr : p.seg + (u.sstate * p.parts + u.part) * (DA * DC))
+                : p.final_state ? p.final_state + (OUT ? u.nstate : u.nstate * p.parts + u.part * (DA * DC)) : nullptr;
     // a state that can be handed on keeps all 24 bits, whether it is asked for or not, or the outputs made from
     // it would depend on that; one that only feeds outputs does with 16
     const bool whole = !OUT || (!TR && u.alone);
@@ -533,7 +535,7 @@ __global__ __launch_bounds__(256, 1) void lin_walk32_kernel(const LinWalkArgs p)
     const int tid0 = threadIdx.x;
     const int w = __builtin_amdgcn_readfirstlane(tid0 >> 6);
     LinUnit<float> u;
-    if (!u.find(p, DA * DC) || (!OUT && u.alone)) return;
+    if (!u.find(p, DA * DC) || (!OUT && u.alone && !p.all)) return;
     const int rows = u.rows, nchunk = u.nchunk;
 
     // the lane's 8 rows 32 kb + 8 g .. of its column in tile ct of a state in memory
@@ -544,8 +546,8 @@ __global__ __launch_bounds__(256, 1) void lin_walk32_kernel(const LinWalkArgs p)
     };
     f32x4 P[NCT][NDT];
     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sunit * (DA * DC);
-    float *to = !OUT ? p.seg + u.sunit * (DA * DC) : u.alone && p.final_state ? p.final_state + u.nstate : nullptr;
+    const float *from = !OUT ? nullptr : u.alone ? (p.init ? p.init + u.nstate : nullptr) : p.seg + u.sstate * (DA * DC);
+    float *to = !u.alone ? (OUT ? nullptr : p.seg + u.sstate * (DA * DC)) : p.final_state ? p.final_state + u.nstate : nullptr;
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll

@@ -37,10 +37,11 @@ def _shapes(q, k, v, g, cu_seqlens):
     return lead, cu_seqlens.numel() - 1, Hk, H, T, dk, dv
 
 
-def lin_workspace_bytes(N, Hk, H, T, dk, dv, dtype, packed=False, backward=False) -> int:
-    """Bytes of workspace for a call on N sequences (packed: N documents in a stream of T tokens)."""
+def lin_workspace_bytes(N, Hk, H, T, dk, dv, dtype, packed=False, backward=False, end_state=True) -> int:
+    """Bytes of workspace for a call on N sequences (packed: N documents in a stream of T tokens); of a
+    backward that is not given dfinal_state, or not asked for dg, less with end_state=False."""
     io = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(lib().kda_lin_workspace_bytes(int(backward), int(packed), N, Hk, H, T, dk, dv, io))
+    return int(lib().kda_lin_workspace_bytes((1 if end_state else 2) if backward else 0, int(packed), N, Hk, H, T, dk, dv, io))
 
 
 def _fwd(q, k, v, g, cu_seqlens, scale, out, final_state, return_final_state, initial_state, workspace, stream):
@@ -109,7 +110,7 @@ def _bwd(q, k, v, g, dout, cu_seqlens, scale, initial_state, dfinal_state, works
         out = {n: _empty(shape, dt, dev, stream) if want else None for n, shape, dt, want in (
             ("dq", q.shape, dtype, True), ("dk", q.shape, dtype, True), ("dv", v.shape, dtype, True),
             ("dg", g.shape, g.dtype, want_dg), ("dinitial_state", (N, H, dv, dk), torch.float32, want_dinitial))}
-        need = lin_workspace_bytes(N, Hk, H, T, dk, dv, dtype, cu is not None, backward=True)
+        need = lin_workspace_bytes(N, Hk, H, T, dk, dv, dtype, cu is not None, backward=True, end_state=want_dg and df is not None)
         workspace = _workspace(workspace, need, dev, stream)
         st = lib().kda_lin_chunk_bwd(*args, cu, N, Hk, H, T, dk, dv, _DTYPES[dtype], _DTYPES[g.dtype], float(scale), s0, df,
                                      *(None if t is None else t.data_ptr() for t in out.values()),

@@ -482,6 +482,10 @@ int kda_latent_tree_step(const void *q, const void *cache, const int *block_tabl
  * bf16 inputs; with bf16 inputs the state that only feeds a segment's outputs gathers 16.
  * The same inputs give the same bits.  What else is asked for does not change them, but for dq and dk with
  * and without dg, which differ by the rounding of a token's term with itself. */
+/* Bytes of workspace kda_lin_chunk_fwd (backward 0) or kda_lin_chunk_bwd (1; 2: without dfinal_state or
+ * without dg) needs; 0 for an invalid problem, and it may be 0 for a forward.  Only sequences that are cut into
+ * segments have states there: of a stream of T tokens those of T / 32 tokens a head at most, however many
+ * documents are in it, and with dfinal_state and dg (1) one a document and head more. */
 size_t kda_lin_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype);
 
 int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
