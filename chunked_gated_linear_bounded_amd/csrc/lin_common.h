@@ -26,7 +26,7 @@ namespace kda {
 struct LinSeqs {
     const int *cu;    // NULL: fixed-length
     int N, T, seg;    // sequences; tokens of one sequence (fixed) or of the stream; tokens of a segment
-    bool sparse;      // where states lie (state0)
+    bool sparse;      // where states lie (state_slot)
     __device__ __forceinline__ int clip(int x) const { return x < 0 ? 0 : (x > T ? T : x); }
     __device__ __forceinline__ int start(int n) const { return cu ? clip(cu[n]) : 0; }
     __device__ __forceinline__ int length(int n) const {
@@ -37,10 +37,11 @@ struct LinSeqs {
     // first work slot of sequence n inside its batch entry; as in GdrSeqs, floor(start / seg) + n
     // leaves every sequence room for its segments (and at least one slot)
     __device__ __forceinline__ int slot0(int n) const { return cu ? clip(cu[n]) / seg + n : 0; }
-    // first state slot of sequence n, which is longer than a segment (no other has states in the workspace).
-    // sparse: 2 floor(start / seg), whatever the number of sequences: one of m segments and a piece, m >= 1,
-    // has m + 1 slots, and the next one starts m segments behind it or later, 2 m slots.
-    __device__ __forceinline__ int state0(int n) const { return sparse ? 2 * (clip(cu[n]) / seg) : slot0(n); }
+    // state slot of segment c of sequence n, which is longer than a segment (no other has states in the
+    // workspace).  sparse: 2 floor(start / seg) + c, whatever the number of sequences: one of m segments and a
+    // piece, m >= 1, has m + 1 slots, and the next one starts m segments behind it or later, 2 m slots.  Else
+    // the segment's work slot.
+    __device__ __forceinline__ int state_slot(int n, int c, int slot) const { return sparse ? 2 * (clip(cu[n]) / seg) + c : slot; }
     __device__ __forceinline__ int segments(int n) const { return (length(n) + seg - 1) / seg; }
     // the segment at slot j of batch entry b: its sequence n, its number in it; false: none there
     __device__ __forceinline__ bool find(int b, int j, int &n, int &c) const {

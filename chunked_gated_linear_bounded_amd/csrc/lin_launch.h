@@ -50,7 +50,7 @@ inline long long lin_slots(const LinLaunch &p) {
 }
 // Segment states of one batch entry and head.  Only sequences longer than a segment have any, so that a packed
 // stream needs no more of them the more short documents are in it; of the two ways to place them
-// (LinSeqs::state0) the one that takes less.
+// (LinSeqs::state_slot) the one that takes less.
 inline bool lin_sparse(const LinLaunch &p) { return p.packed && p.N > p.T / lin_segment(p) + 1; }
 inline long long lin_states(const LinLaunch &p) { return lin_sparse(p) ? 2 * (long long)(p.T / lin_segment(p)) + 1 : lin_slots(p); }
 // all of them (one at least)

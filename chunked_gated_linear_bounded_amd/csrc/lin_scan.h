@@ -30,8 +30,8 @@ static __global__ __launch_bounds__(256) void lin_scan_kernel(const LinScanArgs 
     if (a.seg == nullptr) return;
     const int len = p.seqs.length(seq);
     if (!a.all && len <= p.seqs.seg) return;
-    const int ns = p.seqs.segments(seq), b = p.seqs.cu ? 0 : seq;
-    const size_t s0 = ((size_t)b * p.H + h) * p.nslot + p.seqs.slot0(seq);
+    const int ns = p.seqs.segments(seq), b = p.seqs.cu ? 0 : seq, slot = p.seqs.slot0(seq);
+    const size_t s0 = ((size_t)b * p.H + h) * p.nslot + slot;
     const size_t at = ((size_t)seq * p.H + h) * p.n4 + e;
     f32x4 carry = {0.f, 0.f, 0.f, 0.f};
     if (a.init) carry = reinterpret_cast<const f32x4 *>(a.init)[at];
@@ -40,7 +40,7 @@ static __global__ __launch_bounds__(256) void lin_scan_kernel(const LinScanArgs 
         *last = carry * a.decay[s0] + *last;
         return;
     }
-    f32x4 *st = reinterpret_cast<f32x4 *>(a.seg) + (((size_t)b * p.H + h) * p.nstate + p.seqs.state0(seq)) * p.n4 + e;
+    f32x4 *st = reinterpret_cast<f32x4 *>(a.seg) + (((size_t)b * p.H + h) * p.nstate + p.seqs.state_slot(seq, 0, slot)) * p.n4 + e;
     for (int s = 0; s < ns; s += 8) {
         f32x4 x[8];
         float d[8];
@@ -83,7 +83,7 @@ static __device__ __forceinline__ void lin_decay_grad(const LinDecayGradArgs &p,
     if (!p.seqs.find(b, slot, seq, piece)) return;
     const int len = p.seqs.length(seq), rows = min(p.seqs.seg, len - piece * p.seqs.seg);
     if (rows <= 0) return;
-    const size_t state = ((size_t)b * p.H + h) * p.nstate + p.seqs.state0(seq) + piece, row0 = ((size_t)b * p.H + h) * p.seqs.T + p.seqs.start(seq) + piece * p.seqs.seg;
+    const size_t state = ((size_t)b * p.H + h) * p.nstate + p.seqs.state_slot(seq, piece, slot), row0 = ((size_t)b * p.H + h) * p.seqs.T + p.seqs.start(seq) + piece * p.seqs.seg;
     const bool end = (piece + 1) * (long long)p.seqs.seg >= len;
     const size_t at = ((size_t)seq * p.H + h) * p.n4;
     const f32x4 *R = end ? reinterpret_cast<const f32x4 *>(p.dfinal) + at : reinterpret_cast<const f32x4 *>(p.rev) + state * p.n4;

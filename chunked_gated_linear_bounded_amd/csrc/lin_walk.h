@@ -61,7 +61,7 @@ template <typename E> struct LinUnit {
         g0 = b * p.sg.b + h * p.sg.h + (long long)first * p.sg.t;
         row0 = ((size_t)b * p.H + h) * p.seqs.T + first;
         sunit = ((size_t)b * p.H + h) * p.nslot + slot;
-        sstate = ((size_t)b * p.H + h) * p.nstate + p.seqs.state0(seq) + piece;
+        sstate = ((size_t)b * p.H + h) * p.nstate + p.seqs.state_slot(seq, piece, slot);
         nstate = ((size_t)seq * p.H + h) * state;
         return true;
     }
