@@ -1,0 +1,44 @@
+"""Drafted tokens over histories that many work-groups share, on the GPU: every tile of keys shows in the
+result by itself (latent_pieces_util.py; test_latent_pieces_host.py shows what is noticed)."""
+import pytest
+import torch
+
+import chunked_gated_linear_bounded_amd as kda
+from tests import latent_pieces_util as P
+from tests.test_gpu_latent_serving import BF, F32, attend, check
+
+pytestmark = pytest.mark.gpu
+SCALE = 0.07
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    kda.lib()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,H,dc,page,lens", [
+    (1, 2, 8, 512, 64, [20011]), (1, 1, 1, 512, 16, [32768]), (1, 2, 8, 256, 64, [16384]),  # more pieces of a unit than a wave has lanes
+    (1, 3, 21, 512, 64, [9001]), (2, 3, 20, 256, 1, [6001, 9]), (3, 2, 128, 512, 64, [3000, 1, 2500]), (5, 4, 16, 512, 7, [700, 64, 129, 0, 1000]),
+    (24, 2, 24, 256, 64, [64 * (1 + 7 * i % 40) - i for i in range(24)]),
+])
+def test_every_tile_counts(B, T, H, dc, page, lens, dtype):
+    gen = torch.Generator().manual_seed(7)
+    mp = (max(lens) + page - 1) // page
+    table = torch.randperm(B * mp, generator=gen).reshape(B, mp).to(torch.int32)
+    cache, q = torch.full((B * mp, page, dc + 64), float("nan"), dtype=dtype), P.queries(B, T, H, dc, dtype, gen)
+    rows = [P.history(n, dc, dtype, gen) for n in lens]
+    for b, n in enumerate(lens):
+        j = torch.arange(n)
+        cache[table[b, j // page].long(), j % page] = rows[b]
+    mask = torch.tensor([[(2 << i) - 1 for i in range(T)]] * B, dtype=torch.int64)
+    out, lse = kda.latent_tree_step(q.cuda(), cache.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), mask.cuda(), SCALE, dc=dc,
+                                    return_lse=True)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        for i in range(T):
+            seen = rows[b][:max(0, n - T + i + 1)]
+            ref, tol, lref, _ = attend(q[b, i], seen, SCALE, dc, dtype)
+            check(out[b, i], ref, tol, "out %d %d" % (b, i))
+            check(lse[b, i], lref, P.lse_bound(q[b, i], seen, SCALE, lref), "lse %d %d" % (b, i))
