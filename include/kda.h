@@ -500,8 +500,9 @@ int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k
  * contiguous; none of them, dinitial_state neither, in the place of anything that is read (final_state of the
  * forward may be its initial_state).  The gradients of tokens that no document covers are written as zeros.
  * No float atomics.
- * dg is what is left of a segment's sums of larger terms: where decays are strong its floor is these sums'
- * rounding. */
+ * dg is what is left of a segment's sums of larger terms, so its floor is these sums' rounding: measured
+ * 2e-6 of dg's root mean square over the head in segments of 64 tokens, 1.4e-5 in segments of 1,024 (float32 inputs:
+ * 3e-7, and 1e-6 in segments of 512).  The dg of a token that forgets all but some e^-12 of the state is below that. */
 int kda_lin_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k, const kda_strides *k_strides,
                       const void *v, const kda_strides *v_strides, const void *g, const kda_strides *g_strides,
                       const void *dout, const kda_strides *dout_strides, const int *cu_seqlens, int N, int Hk, int H,
