@@ -157,6 +157,7 @@ class LinChunkFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, g, scale=1.0, initial_state=None, cu_seqlens=None):
         out, fs = _fwd(q, k, v, g, cu_seqlens, scale, None, None, True, initial_state, None, None)
+        ctx.set_materialize_grads(False)  # an end state that nobody used costs the backward nothing
         ctx.save_for_backward(q, k, v, g, initial_state, cu_seqlens)
         ctx.scale = scale
         return out, fs
@@ -165,7 +166,10 @@ class LinChunkFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout, dfinal):
         q, k, v, g, s0, cu = ctx.saved_tensors
-        d = _bwd(q, k, v, g, dout.contiguous(), cu, ctx.scale, s0, dfinal.contiguous(), None, None, ctx.needs_input_grad[3],
+        if dout is None and dfinal is None:
+            return (None,) * 7
+        dout = v.new_zeros(v.shape) if dout is None else dout.contiguous()
+        d = _bwd(q, k, v, g, dout, cu, ctx.scale, s0, None if dfinal is None else dfinal.contiguous(), None, None, ctx.needs_input_grad[3],
                  s0 is not None and ctx.needs_input_grad[5])
         return d["dq"], d["dk"], d["dv"], d["dg"], None, d["dinitial_state"], None
 

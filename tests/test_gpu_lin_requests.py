@@ -77,3 +77,24 @@ def test_the_same_bits_whatever_is_asked_for(B, Hk, H, T, d, lens, dtype):
             for n, t in got.items():
                 if t is not None and not (n in ("dq", "dk") and "want_dg" in kw):
                     assert torch.equal(t, want[n]), (n, kw.keys())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("used", ["out", "state", "both"])
+def test_function_with_one_of_its_results(used, dtype):
+    """Gradients through LinChunkFunction of its output, its end state or both: the entry points' bits."""
+    q, k, v, g, do = case(2, 1, 2, 200, 64, dtype, 91)
+    s0, df = (torch.randn(2, 2, 64, 64, device="cuda") for _ in range(2))
+    x = [t.clone().requires_grad_() for t in (q, k, v, g, s0)]
+    out, fs = kda.LinChunkFunction.apply(*x[:4], 0.1, x[4])
+    loss = 0.0
+    if used != "state":
+        loss = loss + (out * do).sum()
+    if used != "out":
+        loss = loss + (fs * df).sum()
+    got = torch.autograd.grad(loss, x)
+    want = kda.lin_chunk_bwd(q, k, v, g, torch.zeros_like(do) if used == "state" else do, scale=0.1, initial_state=s0,
+                             dfinal_state=None if used == "out" else df)
+    torch.cuda.synchronize()
+    for t, n in zip(got, ("dq", "dk", "dv", "dg", "dinitial_state")):
+        assert torch.equal(t, want[n]), n
