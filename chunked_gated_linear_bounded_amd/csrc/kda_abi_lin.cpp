@@ -18,14 +18,15 @@ kda::LinLaunch shape(bool packed, int N, int Hk, int H, int T, int dk, int dv, i
     return p;
 }
 
-int check_shape(bool packed, int N, int Hk, int H, int T, int dk, int dv, int io) {
+int check_shape(bool backward, bool packed, int N, int Hk, int H, int T, int dk, int dv, int io) {
     if (io != KDA_BF16 && io != KDA_FP32) return KDA_ERR_DTYPE;
     if (N < 1 || Hk < 1 || H < 1 || T < 0 || H % Hk != 0 || H > 65535) return KDA_ERR_SHAPE;
     if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return KDA_ERR_SHAPE;
     if (!packed && N > 65535) return KDA_ERR_SHAPE;
-    if (T > 2147483647 - 4096 || (long long)T / 64 + N > 2147483647LL) return KDA_ERR_SHAPE;
+    if (T > 2147483647 - (1 << 19) || (long long)T / 64 + N > 2147483647LL) return KDA_ERR_SHAPE;  // a segment behind T still counts in 32 bits
     if ((packed ? 1.0 : (double)N) * H * (double)T * (dk > dv ? dk : dv) >= 1099511627776.0) return KDA_ERR_SHAPE;  // 2^40
-    return kda::lin_grids_fit(shape(packed, N, Hk, H, T, dk, dv, io)) ? KDA_OK : KDA_ERR_SHAPE;
+    if (backward && (packed ? 1 : N) * (long long)H * (((long long)T + 15) / 16) >= 1 << 24) return KDA_ERR_SHAPE;
+    return kda::lin_grids_fit(shape(packed, N, Hk, H, T, dk, dv, io), backward) ? KDA_OK : KDA_ERR_SHAPE;
 }
 
 // g in float32, or in the other tensors' type
@@ -80,7 +81,7 @@ int inputs(kda::LinLaunch &p, const void *q, const kda_strides *qs, const void *
 extern "C" {
 
 size_t kda_lin_workspace_bytes(int backward, int packed, int N, int Hk, int H, int T, int dk, int dv, int io_dtype) {
-    if (check_shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype) != KDA_OK) return 0;
+    if (check_shape(backward != 0, packed != 0, N, Hk, H, T, dk, dv, io_dtype) != KDA_OK) return 0;
     const kda::LinLaunch p = shape(packed != 0, N, Hk, H, T, dk, dv, io_dtype);
     return backward ? kda::lin_bwd_bytes(p, backward != 2) : kda::lin_fwd_bytes(p);
 }
@@ -90,7 +91,7 @@ int kda_lin_chunk_fwd(const void *q, const kda_strides *q_strides, const void *k
                       const int *cu_seqlens, int N, int Hk, int H, int T, int dk, int dv, int io_dtype, int g_dtype,
                       float scale, const float *initial_state, void *out, float *final_state, void *workspace,
                       size_t workspace_bytes, hipStream_t stream) {
-    int st = check_shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
+    int st = check_shape(false, cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
     if (st == KDA_OK) st = check_g(io_dtype, g_dtype);
     if (st != KDA_OK) return st;
     kda::LinLaunch p = shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
@@ -111,7 +112,7 @@ int kda_lin_chunk_bwd(const void *q, const kda_strides *q_strides, const void *k
                       int T, int dk, int dv, int io_dtype, int g_dtype, float scale, const float *initial_state,
                       const float *dfinal_state, void *dq, void *dk_out, void *dv_out, void *dg, float *dinitial_state,
                       void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    int st = check_shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
+    int st = check_shape(true, cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);
     if (st == KDA_OK) st = check_g(io_dtype, g_dtype);
     if (st != KDA_OK) return st;
     kda::LinLaunch p = shape(cu_seqlens != nullptr, N, Hk, H, T, dk, dv, io_dtype);

@@ -71,11 +71,10 @@ inline long long lin_finish_grid(const LinLaunch &p, bool grads) {
 
 // Whether the launches of a call stay below 2^32 work-items in x, which is as far as a launch goes, and
 // their unit counts in 32 bits.
-inline bool lin_grids_fit(const LinLaunch &p) {
+inline bool lin_grids_fit(const LinLaunch &p, bool backward) {
     const long long most = 4294967295LL, units = (long long)p.B * p.H * lin_slots(p) * (p.dv / 64);
     const long long states = (long long)p.N * p.H * (p.dk * p.dv / 1024);
-    const long long rows = (long long)p.B * p.H * (((long long)p.T + 15) / 16);
-    return (units + 7) / 8 * 8 <= most / 512 && states <= most / 256 && rows <= most / 256 && lin_finish_grid(p, true) <= most / 256;
+    return (units + 7) / 8 * 8 <= most / 512 && states <= most / 256 && (!backward || lin_finish_grid(p, true) <= most / 256);
 }
 inline bool lin_decode_grid_fits(const LinLaunch &p) { return (long long)p.B * p.H * (p.dv / 16) * 256 <= 4294967295LL; }
 

@@ -50,3 +50,21 @@ def test_the_call_asks_for_what_the_query_says():
         assert call(need - 1, df, dg, T) == E_WS
         none = kda.lin_workspace_bytes(N, H, H, 0, d, d, BF, backward=True, end_state=df and dg)
         assert call(none - 1, df, dg, 0) == E_WS and call(none, df, dg, 0) == OK
+
+
+@pytest.mark.parametrize("B,Hk,H,T,forward,backward", [
+    (1, 1, 1, (1 << 28) - 64, True, True), (1, 1, 1, 1 << 28, True, False), (1, 1, 128, (1 << 21) + 64, True, False),
+    (1, 64, 128, (1 << 21) - 64, True, True),                            # shared key heads
+    (2, 64, 64, 1 << 21, True, False), (1, 1, 1, (1 << 31) - (1 << 19) - 1, True, False), (1, 1, 1, (1 << 31) - (1 << 19), False, False),
+])
+def test_limits_of_the_forward_are_its_own(B, Hk, H, T, forward, backward):
+    """What only the backward's launches cannot take, the forward does."""
+    FAKE, E_SHAPE, E_WS = 0x100000, -2, -6
+    d = 64
+    assert (kda.lin_workspace_bytes(B, Hk, H, T, d, d, BF) > 0) == forward
+    assert (kda.lin_workspace_bytes(B, Hk, H, T, d, d, BF, backward=True) > 0) == backward
+    x = [FAKE, None] * 4
+    st = kda.lib().kda_lin_chunk_fwd(*x, None, B, Hk, H, T, d, d, 0, 0, 1.0, None, FAKE, None, None, 0, None)
+    assert st == (E_WS if forward else E_SHAPE)
+    st = kda.lib().kda_lin_chunk_bwd(*x, FAKE, None, None, B, Hk, H, T, d, d, 0, 0, 1.0, None, None, FAKE, FAKE, FAKE, FAKE, None, None, 0, None)
+    assert st == (E_WS if backward else E_SHAPE)
