@@ -272,8 +272,9 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int x = 0; x < NQ; ++x) O[t][x] = zero;
-        // of a row: minus the maximum that its exponentials are taken against (log2 units; 0 while there is
-        // none), the score that outgrows it, and the wave's keys' part of the sum
+        // of a row: minus the maximum that its exponentials are taken against (0 while there is none), the score
+        // that outgrows it, and the wave's keys' part of the sum.  The maximum is taken off before the scale: scaled
+        // first, its own rounding would be an exponent beyond 2^127 from scores of some 10^9 on.
         float nm[NQ], most[NQ], l[NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
@@ -389,7 +390,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
                 for (int x = 0; x < NQ; ++x) {
                     f32x4 P;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) P[i] = ex2(fmaf(s[x][i], c, nm[x]));
+                    for (int i = 0; i < 4; ++i) P[i] = ex2((s[x][i] + nm[x]) * c);
                     Op::put_half(sp + ((w >> 1) * NQ + x) * FB, lane, w & 1, P);
                     sum[x] += (P[0] + P[1]) + (P[2] + P[3]);
                 }
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
                 const int ln = lane_here(lane);
 #pragma unroll
                 for (int x = 0; x < NQ; ++x) {
-                    const float a = col_max(max4(s[x])) * c;
+                    const float a = col_max(max4(s[x]));
                     if (ln < 16) smax[(w * NQ + x) * 16 + ln] = a;
                 }
                 barrier_lds();
@@ -419,9 +420,9 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
                     float now = was;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) now = fmaxf(now, smax[(k * NQ + x) * 16 + (ln & 15)]);
-                    const float alpha = now == -INFINITY ? 1.f : ex2(was - now);
+                    const float alpha = now == -INFINITY ? 1.f : ex2((was - now) * c);
                     nm[x] = now == -INFINITY ? 0.f : -now;
-                    most[x] = now == -INFINITY ? now : (now + 8.f) / c;
+                    most[x] = now == -INFINITY ? now : now + 8.f / c;
                     sum[x] = l[x] * alpha;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) O[t][x] *= alpha;
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(256, 1) void latent_tree_kernel(const LatentTreeArg
             if (row >= R) continue;
             // nothing seen: zeros, -inf; a sum that is NaN stays one
             const bool none = row / p.H >= count || sum == 0.f;
-            const float inv = 1.f / sum, lse2 = none ? -INFINITY : lg2(sum) - nm[x];
+            const float inv = 1.f / sum, lse2 = none ? -INFINITY : fmaf(-nm[x], c, lg2(sum));
             const size_t at = (size_t)b * R + row, in_part = slot * (16 * NQ) + 16 * x + n2;
             if (g2 == 0 && w == 0) {
                 if (whole) p.lse[at] = lse2 * kLn2;
