@@ -77,3 +77,25 @@ def test_scores_far_out(B, T, H, n, size, dtype):
         check(out[b], want, HALF[dtype] * want.abs() * 1.01 + 2.0 ** -22 * want.abs(), "out %d" % b)
         score = 160.0 * float(q[0, 0, 0, dc]) * scale
         check(lse[b], torch.full((T, H), score, dtype=torch.float64), torch.full((T, H), 2.0 ** -21 * score, dtype=torch.float64), "lse %d" % b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [1e-38, 1e-6, 0.5])
+def test_scales(scale, dtype):
+    """From scales that leave every row the same weight on."""
+    B, T, H, dc, page, n = 2, 3, 20, 256, 16, 500
+    gen = torch.Generator().manual_seed(12)
+    mp = -(-n // page)
+    table = torch.randperm(B * mp, generator=gen).reshape(B, mp).to(torch.int32)
+    cache = torch.randn(B * mp, page, dc + 64, generator=gen).to(dtype)
+    q = torch.randn(B, T, H, dc + 64, generator=gen).to(dtype)
+    mask = torch.tensor([[1, 3, 5]] * B, dtype=torch.int64)
+    out, lse = kda.latent_tree_step(q.cuda(), cache.cuda(), table.cuda(), torch.full((B,), n, dtype=torch.int32).cuda(), mask.cuda(), scale, dc=dc,
+                                    return_lse=True)
+    torch.cuda.synchronize()
+    for b in range(B):
+        rows = cache[table[b].long()].reshape(-1, dc + 64)[:n]
+        for i, see in enumerate(((0,), (0, 1), (0, 2))):
+            ref, tol, lref, ltol = attend(q[b, i], rows[list(range(n - T)) + [n - T + j for j in see]], scale, dc, dtype)
+            check(out[b, i], ref, tol, "out %d %d" % (b, i))
+            check(lse[b, i], lref, ltol, "lse %d %d" % (b, i))

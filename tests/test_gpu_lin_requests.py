@@ -98,3 +98,21 @@ def test_function_with_one_of_its_results(used, dtype):
     torch.cuda.synchronize()
     for t, n in zip(got, ("dq", "dk", "dv", "dg", "dinitial_state")):
         assert torch.equal(t, want[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,lens", [(200, None), (700, None), (0, [70, 0, 300, 1, 64, 500]), (0, [9] * 40 + [300, 65] + [0] * 9)])
+def test_states_in_place(T, lens, dtype):
+    """The end states written over the start states: as into other memory, also of many segments and of documents
+    of one and of many side by side."""
+    H, d = 2, 64
+    N, total = (2, T) if lens is None else (len(lens), sum(lens))
+    q, k, v, g, _ = case(2, 1, H, total, d, dtype, 101, packed=lens is not None)
+    s0 = torch.randn(N, H, d, d, device="cuda")
+    more = () if lens is None else (torch.tensor([0, *lens], dtype=torch.int32).cumsum(0, dtype=torch.int32).cuda(),)
+    fwd = kda.lin_chunk_fwd if lens is None else kda.lin_chunk_fwd_varlen
+    want, last = fwd(q, k, v, g, *more, scale=0.1, initial_state=s0, return_final_state=True)
+    state = s0.clone()
+    got = fwd(q, k, v, g, *more, scale=0.1, initial_state=state, final_state=state)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(state, last)
