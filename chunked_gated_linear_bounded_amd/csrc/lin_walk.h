@@ -248,7 +248,7 @@ __device__ __forceinline__ void lin_pair(const LinWalkArgs &p, lds_u8 *sT, __att
                 : p.final_state ? p.final_state + (OUT ? u.nstate : u.nstate * p.parts + u.part * (DA * DC)) : nullptr;
     // a state that can be handed on keeps all 24 bits, whether it is asked for or not, or the outputs made from
     // it would depend on that; one that only feeds outputs does with 16
-    const bool whole = !OUT || (!TR && u.alone);
+    const bool whole = !OUT || (!TR && __builtin_amdgcn_readfirstlane(u.alone) != 0);
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
