@@ -10,9 +10,9 @@ static long long rows(const LatentTreeLaunch &p) { return (long long)p.T * p.H; 
 static long long key_tiles(const LatentTreeLaunch &p) { return ((long long)p.max_pages * p.page + 63) / 64; }
 // Column tiles of 16 rows a work-group takes: as many as there are rows for (float32: the queries of 32 rows fill
 // the registers), because a fragment of keys is read once for all of them (24 sequences x 8 tokens x 128
-// heads on 9000 rows: 452 us with four, 774 with two); fewer where there would not be two tiles of keys for every CU
-// (3 x 5 x 16 on 700: 15 us of kernel with one, 18 with two, 24 with four; 8 x 4 x 16 on 1500: 30 us a call with one,
-// 35 with two).
+// heads on 4500 to 9000 rows: 424 us with four, 593 with two); fewer where there would not be two tiles of keys for
+// every CU (a call on 3 x 5 x 16 on up to 700: 20 us with one, 26 with two, 37 with four; 8 x 4 x 16 on up to 1500: 29
+// with one, 37 with two).
 static int tiles(const LatentTreeLaunch &p) {
     const int most = rows(p) <= 16 ? 1 : rows(p) <= 32 || p.fp32 ? 2 : 4;
     for (int n = most; n > 1; n /= 2)
@@ -22,11 +22,14 @@ static int tiles(const LatentTreeLaunch &p) {
 static int groups(const LatentTreeLaunch &p) { return (int)((rows(p) + 16 * tiles(p) - 1) / (16 * tiles(p))); }
 // Work-groups that share all tiles evenly (latent_tree.h), one a CU and no more than there can be tiles; 0: one a
 // unit.  Pieces cost their float32 values written and read again and a launch, as much as some 24 tiles of 64
-// rows; units of their own leave CUs idle in the last round.  (256 units of 64 rows, up to 3000 keys: 204 us
-// shared, 156 a unit each; 512: 341 and 303; 384 of 9000: 452 and 478; 1 x 1 x 16 on 40,000: 97 and 974.  Four
-// rounds even out by themselves: 1500 units on 1000 keys 399 and 355.)  Tiles of fewer rows are as much
-// shorter.  float32 tiles are eight times as long, and uneven lengths cost more than pieces: 256 units of 32 rows
-// on up to 2000 keys 377 us shared, 430 a unit each.
+// rows; units of their own leave CUs idle in the last round.  Histories of half to all of the longest, shared
+// against a unit each: 384 units on 9000 rows 394 to 430 us against 461 to 478, 24 x 8 x 128 all on 9000 511 against 605;
+// 256 units on 3000 148 and 108, 512 units 242 and 194; 1 x 1 x 16 on 40,000 97 and 980.  Four rounds even out by
+// themselves (1,008 units on up to 1000 keys 416 and 181).  Tiles of fewer rows are as much shorter.
+// What a unit costs to begin and end is not counted, and the lengths are not known here: with histories from next to
+// nothing on, where a work-group's share can be many short units, sharing is the worse (384 units on 8 to 9000 rows:
+// 603 us against 375).  float32 tiles are eight times as long, and uneven lengths cost more than pieces: 256 units of 32
+// rows on up to 2000 keys 258 us shared, 279 a unit each.
 static int shared(const LatentTreeLaunch &p) {
     const long long units = (long long)p.B * groups(p), idle = ((units + 255) / 256 * 256 - units) * key_tiles(p) / 256;
     const long long most = units * key_tiles(p);

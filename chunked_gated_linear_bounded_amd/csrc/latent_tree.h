@@ -12,14 +12,19 @@
 //    MFMAs; P is handed round through LDS.
 // 64 keys are a tile, loaded straight into LDS, the next one into a second buffer meanwhile: 136 MFMAs a
 // wave (2,176 cycles) on 45 KiB of LDS reads.
-// 24 sequences x 8 tokens x 128 heads on up to 9000 rows: 410 us, 0.9 PFLOP/s, matrix units 43 % busy, vector
-// unit 24 %, LDS 41 % and 7 in bank conflicts.  With one wave a SIMD nothing covers a tile's softmax, its
+// 24 sequences x 8 tokens x 128 heads on up to 9000 rows: 409 to 444 us, 0.8 to 0.9 PFLOP/s, matrix units 43 % busy,
+// vector unit 25 %, LDS 41 % and 7 in bank conflicts.  With one wave a SIMD nothing covers a tile's softmax, its
 // barrier and the first reads behind it; a third buffer, for the next scores to run beside them, does not fit the
 // LDS.
 //
 // The exponentials are taken against a maximum that may be 2^8 too small, so that the accumulator is
 // scaled a few times a row and not every tile: a wave makes P with the maximum it has, says whether a row
 // has outgrown it, and only where one has all four waves agree on new maxima and make P again.
+//
+// With bf16 inputs P is rounded to bf16 as the products' operand, as in the one-token step: half the matrix work and
+// half of what is handed round in LDS, against out's error of 1.8e-3 (histories of thousands of rows) to 2.1e-3 (of
+// hundreds) of its norm, where its own rounding to bf16 alone is 1.7e-3.  Sums of P, maxima and the accumulator are
+// float32, and the sum is that of the exponentials before they are rounded.
 //
 // A fragment (16 rows x 32 channels) is rows of 64 bytes, because a direct load fills LDS in lane order and
 // is fast where four neighbouring lanes read one row: with a row a lane it made 64 accesses to the cache in

@@ -99,8 +99,8 @@ __device__ __forceinline__ float load_g(const void *g, long long at, bool g32) {
 
 // ---------------------------------------------------------------- operands
 // What is computed in float32 and enters a product again is carried in pieces where operands are bf16:
-// x = hi + lo keeps 16 bits (M and P, whose products are rounded to bf16 outputs), a third piece all 24
-// (what a float32 state that is handed on gathers).  bf16 has float's exponents, so pieces need no
+// x = hi + lo keeps 16 bits (M and P, whose products are rounded to bf16 outputs: these are off by 1.7e-3 of their
+// norm, as float32's rounded once), a third piece all 24 (what a float32 state that can be handed on gathers).  bf16 has float's exponents, so pieces need no
 // scaling.  float32 inputs use float32 MFMAs and need no pieces.
 template <bool F32> struct LinOp;
 template <> struct LinOp<true> : AttnOp<true> {};

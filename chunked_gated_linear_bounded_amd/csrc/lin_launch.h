@@ -29,13 +29,18 @@ struct LinLaunch {
 
 // Tokens of a segment, the piece of a sequence that one work-group walks through, and the segments of one
 // batch entry.  A segment costs its state written, scanned and read again and its inputs read twice, so
-// there are as many as keep the card busy and no more: one work-group a CU in bf16, whose work-groups have
-// eight waves and 125 KB of LDS (256 against 512 segments in all: 4 x 8192 x 16 heads 226 us against 243,
-// 1 x 65536 x 32 heads 838 against 853, the training step of 2 x 4096 x 32 heads 323 against 386), two in float32.
+// there are as many as keep the card busy and no more, counted over the chunks of all heads.
+// bf16: one work-group a CU, whose eight waves have 130 KiB of LDS at 128 x 128 (256 against 512 segments in all:
+// 4 x 8192 x 16 heads 210 us against 228, 1 x 65536 x 32 heads 729 against 738, the training step of 2 x 4096 x 8/16
+// heads 280 against 341).  Where batch x heads does not divide 256 a head's last segment is short and there are up
+// to a quarter more work-groups than CUs, so a second round: 8192 tokens of 24 heads take 126 us, of 32 heads 108.
+// float32: 512 segments.  At 64 x 64 two work-groups fit a CU (67 KiB; 2 x 4096 x 16 heads 96 us against 116 with 256,
+// backward 267 against 337); at 128 x 128 one does (115 KiB), and two rounds of shorter segments are as good as one (4
+// x 8192 x 16 heads 920 against 978, backward 2,727 against 2,823; 2 x 4096 x 16 heads 259 against 262).
 // A chunk of 64 tokens is the least, for short sequences wait for one chunk after the other (1 x 1024 x 4
-// heads, forward and backward: 23 and 62 us with segments of 64 tokens, 32 and 93 with 256; float32 42 and
-// 115, 117 and 329); only up to 256 tokens of bf16 is one launch over a single segment better (256 tokens:
-// 17 us against 23 forward, 61 against 55 backward; 192: 17 against 23, 50 against 54).
+// heads, forward and backward: 27 and 43 us with segments of 64 tokens, 31 and 46 with 256; float32 43 and
+// 117, 118 and 332); only up to 256 tokens of bf16 is one launch over a single segment better (256 tokens:
+// 18 us against 27 forward, 37 against 44 backward).
 inline int lin_segment(const LinLaunch &p) {
     const long long chunks = (((long long)p.T + 63) / 64) * p.B * p.H, most = p.fp32 ? 512 : 256;
     long long per = (chunks + most - 1) / most;

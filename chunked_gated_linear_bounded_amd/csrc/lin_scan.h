@@ -1,8 +1,8 @@
 // Decayed linear attention between segments: the scan that turns segments' own contributions into
 // start states, and what the backward pass still does behind its walks (the log-decays' gradient, sums
 // over value heads, rows that no document covers).  All of it moves bytes and nothing else.  Training step of
-// 2 x 4096 x 8/16 heads of 128 x 128 (288 us): scans 2 x 8 us, 34 MB each read and written; all that is behind the
-// walks 35, 134 MB of partials and 34 of states read, 34 written (5.8 TB/s; as launches of their own the
+// 2 x 4096 x 8/16 heads of 128 x 128 (286 us): scans 2 x 8 us, 34 MB each read and written; all that is behind the
+// walks 33 to 35, 134 MB of partials and 34 of states read, 34 written (5.8 TB/s; as launches of their own the
 // sums over heads took 32 and the log-decays 11).
 #pragma once
 #include "lin_common.h"

@@ -75,10 +75,10 @@ template <typename E> struct LinUnit {
 // As one group of four waves that did all of it in turn, two work-groups on a CU, a chunk took 17,400 cycles
 // of a work-group, half of them waits, and the parts' times added up (4 x 8192 x 16 heads 248 us against 202).
 //
-// 1 x 65536 x 32 heads of 128 x 128, 256 segments of 128 chunks: pass 1 takes 236 us (its loads of 0.8 GB alone
+// 1 x 65536 x 32 heads of 128 x 128, 256 segments of 128 chunks: pass 1 takes 240 us (its loads of 0.8 GB alone
 // 153, its products and pieces alone 205), pass 2 460 (its 1.6 GB alone 290, the rest alone 375).  A SIMD has some
 // 1000 vector instructions of 4 cycles a chunk of pass 2, most of them pieces of P and of the weighted C, beside
-// 160 MFMAs of 16: vector issue 49 % and matrix units 37 % busy (pass 1: 67 and 44), in two waves a SIMD that go
+// 160 MFMAs of 16: vector issue 51 % and matrix units 38 % busy (pass 1: 67 and 44), in two waves a SIMD that go
 // each in order.
 //
 // OUT: pass 2, the outputs; else pass 1, the segment's own contribution to the state.  TR: states in memory
@@ -491,7 +491,7 @@ __device__ __forceinline__ void lin_pair(const LinWalkArgs &p, lds_u8 *sT, __att
 }
 
 // One walk, or walks that do not depend on each other in one launch, where the next one's work-groups follow
-// on a CU as soon as the last one's are done (11 packed documents, 5003 tokens, training step: 102 -> 95 us).
+// on a CU as soon as the last one's are done (11 packed documents, 5003 tokens, training step: 102 -> 95 us when they came together).
 template <int DA, int DC, bool REV, bool TR, bool OUT, bool DOT, bool OUTF> struct LinWalk {
     static constexpr int BYTES = LinPairLds<DA, DC, OUT, DOT>::BYTES, FLOATS = LinPairLds<DA, DC, OUT, DOT>::FLOATS;
     __device__ __forceinline__ static void run(const LinWalkArgs &p, lds_u8 *sT, __attribute__((address_space(3))) float *sG) {
@@ -518,8 +518,10 @@ __global__ __launch_bounds__(512, 2) void lin_pair_kernel(const LinWalkList<size
     ((void)(i++ == (int)blockIdx.y && (W::run(p, lds_base(smem), (__attribute__((address_space(3))) float *)lds_base(sg)), true)), ...);
 }
 
-// float32: tiles fill the LDS once, so one group of four waves does everything in turn, on float32 MFMAs,
-// whose rate (an eighth of bf16's) leaves little for helpers to hide.  Parameters as above.
+// float32: tiles fill the LDS once, so one group of four waves does everything in turn, on float32 MFMAs, which run
+// at an eighth of bf16's rate.  Parameters as above.  2 x 4096 x 16 heads of 128 x 128: forward 259 us, 104 of them
+// the products themselves at a large matrix product's rate (155 TFLOP/s); the rest are loads, scores and barriers
+// that nothing hides.
 template <int DA, int DC, bool REV, bool TR, bool OUT, bool DOT>
 __global__ __launch_bounds__(256, 1) void lin_walk32_kernel(const LinWalkArgs p) {
     using Op = LinOp<true>;
