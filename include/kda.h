@@ -475,7 +475,8 @@ int kda_latent_tree_step(const void *q, const void *cache, const int *block_tabl
  *  - the t strides of q, k, v and dout are not negative, and 64 of them take less than 2^31 bytes
  *    (KDA_ERR_SHAPE otherwise).
  *  - launches below 2^32 work-items (KDA_ERR_SHAPE): 2^24 / (dk dv / 1024) sequences and heads; in the
- *    backward also below 2^24 pieces of 16 tokens of a head, and of 1024 elements of dq (key heads shared).
+ *    backward also below 2^24 pieces of 16 tokens of a head and, where key heads are shared, of 1024
+ *    elements of dq (with a packed stream's pieces of 64 tokens of a head).
  *  - What is not finite in q reaches its token's outputs; in v its channel of the outputs from its chunk
  *    of 64 tokens on and of the state; in k or g its head's.
  * States that can be handed on (final_state, dinitial_state, between segments) gather all 24 bits, also with
